@@ -9,7 +9,7 @@ _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB = os.path.join(_HERE, "libzeroshard.so")
 SOURCES = [os.path.join(_HERE, "csrc", f)
            for f in ("kernels.hip", "plan.cpp", "abi.cpp", "offload.cpp", "alloc.cpp",
-                     "static_step.hip")]
+                     "static_step.hip", "embed.hip", "norm.hip", "act8.hip", "xent.hip")]
 # host-compiled part: the offloaded update (vector clones picked at load time)
 HOST_SOURCES = [os.path.join(_HERE, "csrc", "host_step.cpp")]
 GXX_FLAGS = ["-O3", "-std=c++17", "-fPIC", "-ffp-contract=off", "-fno-math-errno", "-pthread",
@@ -18,7 +18,7 @@ GXX_FLAGS = ["-O3", "-std=c++17", "-fPIC", "-ffp-contract=off", "-fno-math-errno
 # -ffp-contract=off: no FMA contraction (each operation rounds once);
 # correctly rounded fp32 division / sqrt; fp32 subnormals kept;
 # packed-fp32 instructions disabled.
-HIPCC_FLAGS = ["--offload-arch=gfx950", "-O3", "-std=c++17", "-fPIC", "-shared",
+HIPCC_FLAGS = ["--offload-arch=gfx950", "-O3", "-std=c++17", "-fPIC",
                "-ffp-contract=off", "-fhip-fp32-correctly-rounded-divide-sqrt",
                "-fno-gpu-flush-denormals-to-zero",
                "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops",
@@ -35,8 +35,20 @@ def build(verbose: bool = False, extra_flags=None) -> str:
                 print(" ".join(cmd), flush=True)
             subprocess.run(cmd, check=True)
             objs.append(obj)
-        # the host objects go to the linker as they are (hipcc would read them as source)
-        cmd = ["hipcc", *HIPCC_FLAGS, *(extra_flags or []), "-o", LIB + ".tmp", *SOURCES,
+        # each source by itself, side by side (a file of kernels takes up to a minute)
+        running = []
+        for src in SOURCES:
+            obj = os.path.join(tmp, os.path.basename(src) + ".o")
+            cmd = ["hipcc", *HIPCC_FLAGS, *(extra_flags or []), "-c", src, "-o", obj]
+            if verbose:
+                print(" ".join(cmd), flush=True)
+            running.append((cmd, subprocess.Popen(cmd)))
+            objs.append(obj)
+        for cmd, p in running:
+            if p.wait():
+                raise subprocess.CalledProcessError(p.returncode, cmd)
+        # the objects go to the linker as they are (hipcc would read them as source)
+        cmd = ["hipcc", *HIPCC_FLAGS, "-shared", "-o", LIB + ".tmp",
                *[f"-Wl,{o}" for o in objs], "-pthread"]
         if verbose:
             print(" ".join(cmd), flush=True)

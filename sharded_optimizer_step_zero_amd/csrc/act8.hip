@@ -1,0 +1,329 @@
+// act8.hip -- activations held in 8 bits: packing, unpacking, and the gated unit
+// that keeps its input so and takes its gradient from it.
+//
+// All four are one pass over their arrays and bound by HBM: a lane takes 8
+// neighbouring elements (16 bytes of a 16-bit type, 8 bytes of codes), a group's
+// maximum is a few shuffles among neighbouring lanes.  The scales are powers of
+// two, so scaling is exact and a code is the input rounded once.  The gated unit
+// reads gate and up once for its output and their codes.  The backward pass needs
+// 2 bytes of checkpoint a pair where the 16-bit input takes 4, and gives the
+// unit's output again so that it need not be kept either.
+#include "ops.h"
+
+namespace zs {
+namespace ops {
+namespace {
+
+constexpr int64_t kMaxWidth = 1 << 20;
+constexpr int64_t kMaxBlocks = 0x7fffff;
+
+// A row takes `lanes` (16..256, a power of two) threads a block; wider rows take
+// several blocks.
+struct Place {
+  int64_t row, chunk;
+  bool live;
+};
+struct Spread {
+  int lanes_log2;
+  uint32_t per_row;  // blocks a row
+  int64_t blocks;
+};
+Spread spread(int64_t rows, int64_t width) {
+  const int64_t chunks = (width + 7) / 8;
+  Spread s{4, 1, 0};
+  while (s.lanes_log2 < 8 && (1ll << s.lanes_log2) < chunks) s.lanes_log2++;
+  s.per_row = (uint32_t)((chunks + (1 << s.lanes_log2) - 1) >> s.lanes_log2);
+  const int64_t row_blocks = (rows + (256 >> s.lanes_log2) - 1) >> (8 - s.lanes_log2);
+  s.blocks = row_blocks * s.per_row;
+  return s;
+}
+__device__ __forceinline__ Place place(int lanes_log2, uint32_t per_row, int64_t rows,
+                                       int64_t width) {
+  const uint32_t rb = blockIdx.x / per_row, cb = blockIdx.x - rb * per_row;
+  Place p;
+  p.row = ((int64_t)rb << (8 - lanes_log2)) + (threadIdx.x >> lanes_log2);
+  p.chunk = ((int64_t)cb << lanes_log2) + (threadIdx.x & ((1 << lanes_log2) - 1));
+  p.live = p.row < rows && p.chunk * 8 < width;
+  return p;
+}
+
+template <int DT, bool WIDE, int CODE>
+__global__ __launch_bounds__(256) void pack_kernel(const elem_t<DT>* __restrict__ x,
+                                                   int64_t x_stride, uint8_t* __restrict__ codes,
+                                                   uint8_t* __restrict__ scales, int64_t rows,
+                                                   int64_t width, int group_lanes, int64_t groups,
+                                                   int lanes_log2, uint32_t per_row) {
+  const Place p = place(lanes_log2, per_row, rows, width);
+  const int64_t c = p.chunk * 8, left = width - c;
+  f32x8 v = {};
+  if (p.live) v = load8<DT, WIDE>(x + p.row * x_stride + c, left);
+  uint32_t byte;
+  const u32x2 w = quantise8<CODE>(v, group_lanes, &byte);
+  if (!p.live) return;
+  store_codes<WIDE>(codes + p.row * width + c, left, w);
+  if (p.chunk % group_lanes == 0) scales[p.row * groups + p.chunk / group_lanes] = (uint8_t)byte;
+}
+
+template <int DT, bool WIDE, int CODE>
+__global__ __launch_bounds__(256) void unpack_kernel(const uint8_t* __restrict__ codes,
+                                                     const uint8_t* __restrict__ scales,
+                                                     elem_t<DT>* __restrict__ x, int64_t x_stride,
+                                                     int64_t rows, int64_t width, int group_lanes,
+                                                     int64_t groups, int lanes_log2,
+                                                     uint32_t per_row) {
+  const Place p = place(lanes_log2, per_row, rows, width);
+  if (!p.live) return;
+  const int64_t c = p.chunk * 8, left = width - c;
+  const float s = scale_value(scales[p.row * groups + p.chunk / group_lanes]);
+  const f32x8 v = decode8<CODE>(load_codes<WIDE>(codes + p.row * width + c, left)) * s;
+  store8<DT, WIDE>(x + p.row * x_stride + c, left, v);
+}
+
+// 1 / (1 + e^-x): the hardware's exponential and reciprocal, each within an ulp or
+// two; e^-x past fp32 gives 0.
+__device__ __forceinline__ float sigmoid(float x) {
+  return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(x * -1.44269504f));
+}
+
+// act(x), and its derivative in *slope.  The tanh form of GELU is x times the
+// sigmoid of 2z, z = sqrt(2/pi) (x + 0.044715 x^3).
+template <int ACT>
+__device__ __forceinline__ float activation(float x, float* slope) {
+  if (ACT == ZS_SILU) {
+    const float s = sigmoid(x);
+    *slope = s + x * s * (1.0f - s);
+    return x * s;
+  }
+  const float k = 0.79788456f, xx = x * x;
+  const float s = sigmoid(2.0f * k * (x + 0.044715f * x * xx));
+  const float t = s * (1.0f - s);
+  // far out the sigmoid is flat while x^3 passes fp32: 0, not 0 * infinity
+  *slope = t == 0.0f ? s : s + 2.0f * k * x * t * (1.0f + 0.134145f * xx);
+  return x * s;
+}
+
+template <int DT, bool WIDE, int ACT, int CODE>
+__global__ __launch_bounds__(256) void glu_kernel(
+    const elem_t<DT>* __restrict__ gate_up, int64_t gu_stride, elem_t<DT>* __restrict__ out,
+    int64_t out_stride, uint8_t* __restrict__ codes, uint8_t* __restrict__ scales, int64_t rows,
+    int64_t width, int group_lanes, int64_t groups, int lanes_log2, uint32_t per_row) {
+  const Place p = place(lanes_log2, per_row, rows, width);
+  const int64_t c = p.chunk * 8, left = width - c;
+  f32x8 g = {}, u = {};
+  if (p.live) {
+    const elem_t<DT>* src = gate_up + p.row * gu_stride + c;
+    g = load8<DT, WIDE>(src, left);
+    u = load8<DT, WIDE>(src + width, left);
+    f32x8 o;
+#pragma unroll
+    for (int i = 0; i < 8; i++) {
+      float slope;
+      o[i] = activation<ACT>(g[i], &slope) * u[i];
+    }
+    store8<DT, WIDE>(out + p.row * out_stride + c, left, o);
+  }
+  if (CODE >= 0) {
+    uint32_t gb, ub;
+    const u32x2 gw = quantise8<CODE < 0 ? 0 : CODE>(g, group_lanes, &gb);
+    const u32x2 uw = quantise8<CODE < 0 ? 0 : CODE>(u, group_lanes, &ub);
+    if (!p.live) return;
+    uint8_t* dst = codes + p.row * 2 * width + c;
+    store_codes<WIDE>(dst, left, gw);
+    store_codes<WIDE>(dst + width, left, uw);
+    if (p.chunk % group_lanes == 0) {
+      uint8_t* s = scales + p.row * 2 * groups + p.chunk / group_lanes;
+      s[0] = (uint8_t)gb;
+      s[groups] = (uint8_t)ub;
+    }
+  }
+}
+
+template <int DT, bool WIDE, int ACT, int CODE>
+__global__ __launch_bounds__(256) void glu_grad_kernel(
+    const elem_t<DT>* __restrict__ dout, int64_t dout_stride, const uint8_t* __restrict__ codes,
+    const uint8_t* __restrict__ scales, elem_t<DT>* __restrict__ dgu, int64_t dgu_stride,
+    elem_t<DT>* __restrict__ out, int64_t out_stride, int64_t rows, int64_t width,
+    int group_lanes, int64_t groups, int lanes_log2, uint32_t per_row) {
+  const Place p = place(lanes_log2, per_row, rows, width);
+  if (!p.live) return;
+  const int64_t c = p.chunk * 8, left = width - c;
+  const uint8_t* src = codes + p.row * 2 * width + c;
+  const uint8_t* sc = scales + p.row * 2 * groups + p.chunk / group_lanes;
+  const f32x8 g = decode8<CODE>(load_codes<WIDE>(src, left)) * scale_value(sc[0]);
+  const f32x8 u = decode8<CODE>(load_codes<WIDE>(src + width, left)) * scale_value(sc[groups]);
+  const f32x8 d = load8<DT, WIDE>(dout + p.row * dout_stride + c, left);
+  f32x8 dg, du, o;
+#pragma unroll
+  for (int i = 0; i < 8; i++) {
+    float slope;
+    const float a = activation<ACT>(g[i], &slope);
+    dg[i] = d[i] * u[i] * slope;
+    du[i] = d[i] * a;
+    o[i] = a * u[i];
+  }
+  elem_t<DT>* dst = dgu + p.row * dgu_stride + c;
+  store8<DT, WIDE>(dst, left, dg);
+  store8<DT, WIDE>(dst + width, left, du);
+  if (out) store8<DT, WIDE>(out + p.row * out_stride + c, left, o);
+}
+
+template <typename F>
+void with_act(int32_t act, F f) {
+  if (act == ZS_SILU)
+    f(std::integral_constant<int, ZS_SILU>());
+  else
+    f(std::integral_constant<int, ZS_GELU>());
+}
+
+int check(const char* who, int64_t rows, int64_t width, int32_t dtype) {
+  if (!good_dtype(dtype)) return fail(who, "unknown element type");
+  if (rows < 0 || rows > 0x7fffffff || width < 1 || width > kMaxWidth)
+    return fail(who, "a size is out of range");
+  if (spread(rows, width).blocks > kMaxBlocks) return fail(who, "too many rows for one call");
+  return ZS_OK;
+}
+int check_code(const char* who, int32_t code, int32_t group) {
+  if ((code != ZS_E4M3 && code != ZS_E5M2) || !good_group(group))
+    return fail(who, "the 8-bit form is e4m3 or e5m2 in groups of 32, 64 or 128");
+  return ZS_OK;
+}
+
+}  // namespace
+}  // namespace ops
+}  // namespace zs
+
+using namespace zs::ops;
+
+extern "C" int zs_act8_pack(const void* x, int64_t x_stride, void* codes, void* scales,
+                            int64_t rows, int64_t width, int32_t dtype, int32_t code,
+                            int32_t group, void* stream) {
+  const char* who = "zs_act8_pack";
+  if (int rc = check(who, rows, width, dtype)) return rc;
+  if (int rc = check_code(who, code, group)) return rc;
+  if (x_stride < width) return fail(who, "a row stride is below width");
+  if (rows == 0) return ZS_OK;
+  if (!x || !codes || !scales) return fail(who, "NULL buffer");
+  if (!al(x, elem_bytes(dtype))) return fail(who, "a buffer is not aligned to its elements");
+  const Spread s = spread(rows, width);
+  const bool w = wide(x, x_stride, dtype) && width % 8 == 0 && al(codes, 8);
+  with_dtype(dtype, [&](auto DT) {
+    with_bool(w, [&](auto W) {
+      with_code(code, [&](auto CODE) {
+        pack_kernel<decltype(DT)::value, decltype(W)::value, decltype(CODE)::value>
+            <<<dim3((uint32_t)s.blocks), dim3(256), 0, (hipStream_t)stream>>>(
+                (const elem_t<decltype(DT)::value>*)x, x_stride, (uint8_t*)codes,
+                (uint8_t*)scales, rows, width, group / 8, (width + group - 1) / group,
+                s.lanes_log2, s.per_row);
+      });
+    });
+  });
+  return launched(who);
+}
+
+extern "C" int zs_act8_unpack(const void* codes, const void* scales, void* x, int64_t x_stride,
+                              int64_t rows, int64_t width, int32_t dtype, int32_t code,
+                              int32_t group, void* stream) {
+  const char* who = "zs_act8_unpack";
+  if (int rc = check(who, rows, width, dtype)) return rc;
+  if (int rc = check_code(who, code, group)) return rc;
+  if (x_stride < width) return fail(who, "a row stride is below width");
+  if (rows == 0) return ZS_OK;
+  if (!x || !codes || !scales) return fail(who, "NULL buffer");
+  if (!al(x, elem_bytes(dtype))) return fail(who, "a buffer is not aligned to its elements");
+  const Spread s = spread(rows, width);
+  const bool w = wide(x, x_stride, dtype) && width % 8 == 0 && al(codes, 8);
+  with_dtype(dtype, [&](auto DT) {
+    with_bool(w, [&](auto W) {
+      with_code(code, [&](auto CODE) {
+        unpack_kernel<decltype(DT)::value, decltype(W)::value, decltype(CODE)::value>
+            <<<dim3((uint32_t)s.blocks), dim3(256), 0, (hipStream_t)stream>>>(
+                (const uint8_t*)codes, (const uint8_t*)scales,
+                (elem_t<decltype(DT)::value>*)x, x_stride, rows, width, group / 8,
+                (width + group - 1) / group, s.lanes_log2, s.per_row);
+      });
+    });
+  });
+  return launched(who);
+}
+
+extern "C" int zs_glu_forward(const void* gate_up, int64_t gate_up_stride, void* out,
+                              int64_t out_stride, void* codes, void* scales, int64_t rows,
+                              int64_t width, int32_t dtype, int32_t act, int32_t code,
+                              int32_t group, void* stream) {
+  const char* who = "zs_glu_forward";
+  if (int rc = check(who, rows, width, dtype)) return rc;
+  if (act != ZS_SILU && act != ZS_GELU) return fail(who, "unknown activation");
+  if ((codes == nullptr) != (scales == nullptr)) return fail(who, "codes and scales go together");
+  if (codes)
+    if (int rc = check_code(who, code, group)) return rc;
+  if (gate_up_stride < 2 * width || out_stride < width)
+    return fail(who, "a row stride is below the row's width");
+  if (rows == 0) return ZS_OK;
+  if (!gate_up || !out) return fail(who, "NULL buffer");
+  const int eb = elem_bytes(dtype);
+  if (!al(gate_up, eb) || !al(out, eb)) return fail(who, "a buffer is not aligned to its elements");
+  const Spread s = spread(rows, width);
+  const int g = codes ? group : 128;
+  // gate and up start 16-byte aligned only where the width is a multiple of 16 bytes
+  const bool w = wide(gate_up, gate_up_stride, dtype) && wide(out, out_stride, dtype) &&
+                 width % 8 == 0 && (!codes || al(codes, 8));
+  with_dtype(dtype, [&](auto DT) {
+    with_bool(w, [&](auto W) {
+      with_act(act, [&](auto ACT) {
+        auto go = [&](auto CODE) {
+          using E = elem_t<decltype(DT)::value>;
+          glu_kernel<decltype(DT)::value, decltype(W)::value, decltype(ACT)::value,
+                     decltype(CODE)::value>
+              <<<dim3((uint32_t)s.blocks), dim3(256), 0, (hipStream_t)stream>>>(
+                  (const E*)gate_up, gate_up_stride, (E*)out, out_stride, (uint8_t*)codes,
+                  (uint8_t*)scales, rows, width, g / 8, (width + g - 1) / g, s.lanes_log2,
+                  s.per_row);
+        };
+        if (!codes)
+          go(std::integral_constant<int, -1>());
+        else
+          with_code(code, go);
+      });
+    });
+  });
+  return launched(who);
+}
+
+extern "C" int zs_glu_backward(const void* grad_out, int64_t grad_out_stride, const void* codes,
+                               const void* scales, void* grad_gate_up,
+                               int64_t grad_gate_up_stride, void* out, int64_t out_stride,
+                               int64_t rows, int64_t width, int32_t dtype, int32_t act,
+                               int32_t code, int32_t group, void* stream) {
+  const char* who = "zs_glu_backward";
+  if (int rc = check(who, rows, width, dtype)) return rc;
+  if (act != ZS_SILU && act != ZS_GELU) return fail(who, "unknown activation");
+  if (int rc = check_code(who, code, group)) return rc;
+  if (grad_out_stride < width || grad_gate_up_stride < 2 * width || (out && out_stride < width))
+    return fail(who, "a row stride is below the row's width");
+  if (rows == 0) return ZS_OK;
+  if (!grad_out || !codes || !scales || !grad_gate_up) return fail(who, "NULL buffer");
+  const int eb = elem_bytes(dtype);
+  if (!al(grad_out, eb) || !al(grad_gate_up, eb) || !al(out, eb))
+    return fail(who, "a buffer is not aligned to its elements");
+  const Spread s = spread(rows, width);
+  const bool w = wide(grad_out, grad_out_stride, dtype) &&
+                 wide(grad_gate_up, grad_gate_up_stride, dtype) && width % 8 == 0 &&
+                 al(codes, 8) && (!out || wide(out, out_stride, dtype));
+  with_dtype(dtype, [&](auto DT) {
+    with_bool(w, [&](auto W) {
+      with_act(act, [&](auto ACT) {
+        with_code(code, [&](auto CODE) {
+          using E = elem_t<decltype(DT)::value>;
+          glu_grad_kernel<decltype(DT)::value, decltype(W)::value, decltype(ACT)::value,
+                          decltype(CODE)::value>
+              <<<dim3((uint32_t)s.blocks), dim3(256), 0, (hipStream_t)stream>>>(
+                  (const E*)grad_out, grad_out_stride, (const uint8_t*)codes,
+                  (const uint8_t*)scales, (E*)grad_gate_up, grad_gate_up_stride, (E*)out,
+                  out_stride, rows, width, group / 8, (width + group - 1) / group, s.lanes_log2,
+                  s.per_row);
+        });
+      });
+    });
+  });
+  return launched(who);
+}

@@ -1,0 +1,394 @@
+// embed.hip -- the token embedding and its table's gradient.
+//
+// Forward: out[t] = scale * table[id_t].  A copy of T rows: bound by the bytes
+// (the rows read and written); a lane moves 8 elements, a row takes the least
+// power of two of lanes that covers it, up to a workgroup.
+//
+// Backward: grad_table[v] = scale * sum over {t : id_t = v} of grad_out[t].
+// Frequencies of a language fall as one over the rank: some ids own a tenth of
+// all tokens, most none.  Atomics would make the sum's order a matter of
+// timing, so tokens are grouped by id first:
+//   sort_kernel    one workgroup per bucket of ids (id mod the power-of-two
+//                  number of buckets, so that neighbouring frequent ids part).
+//                  It reads all ids, counts its own per id and wave, and places
+//                  them in order of t; the tokens of lower buckets, counted
+//                  along the way, give its place in the output.  One launch, no
+//                  exchange between workgroups.  T ids are read by every bucket
+//                  twice, out of L2.
+//   reduce_kernel  fixed runs of kRun sorted tokens, a wave per run and 512
+//                  columns: the rows of one id are summed in fp32 in order.  An
+//                  id whose tokens lie in one run is written at once; of one that
+//                  crosses runs, each run stores its part in fp32.  Waves of
+//                  the same launch write the zero rows of ids without tokens.
+//   join_kernel    adds the parts of an id that crosses runs, in their order.
+// The work is balanced by tokens, not ids, and the order is fixed.
+#include "ops.h"
+
+namespace zs {
+namespace ops {
+namespace {
+
+constexpr int kSortThreads = 1024;
+constexpr int kSortWaves = kSortThreads / 64;
+constexpr int kMaxSlots = 512;   // ids of one bucket
+constexpr int kRun = 32;         // sorted tokens of one wave
+constexpr int kCols = 512;       // columns of one wave
+constexpr int kZeroRows = 8;     // rows without tokens that one wave looks at
+
+template <typename I>
+__device__ __forceinline__ int64_t local_id(const void* ids, int64_t t, int64_t start) {
+  return (int64_t)((const I*)ids)[t] - start;
+}
+
+template <int DT, bool WIDE, typename I>
+__global__ __launch_bounds__(256) void gather_kernel(
+    const elem_t<DT>* __restrict__ table, int64_t table_stride, const void* __restrict__ ids,
+    elem_t<DT>* __restrict__ out, int64_t out_stride, int64_t n, int64_t vocab, int64_t width,
+    int64_t start, float scale, int lanes_log2) {
+  const int lanes = 1 << lanes_log2;
+  const int64_t t = ((int64_t)blockIdx.x << (8 - lanes_log2)) + (threadIdx.x >> lanes_log2);
+  if (t >= n) return;
+  const int64_t v = local_id<I>(ids, t, start);
+  const bool in = v >= 0 && v < vocab;
+  const elem_t<DT>* src = table + (in ? v : 0) * table_stride;
+  elem_t<DT>* dst = out + t * out_stride;
+  for (int64_t c = (int64_t)(threadIdx.x & (lanes - 1)) * 8; c < width; c += lanes * 8) {
+    f32x8 x = {};
+    if (in) x = load8<DT, WIDE>(src + c, width - c) * scale;
+    store8<DT, WIDE>(dst + c, width - c, x);
+  }
+}
+
+template <typename I>
+__global__ __launch_bounds__(kSortThreads) void sort_kernel(
+    const void* __restrict__ ids, int32_t n, int64_t vocab, int64_t start, int bucket_log2,
+    int32_t* __restrict__ order, int32_t* __restrict__ sorted, int32_t* __restrict__ first,
+    int32_t* __restrict__ count, int32_t* __restrict__ n_valid) {
+  __shared__ int32_t cnt[kSortWaves][kMaxSlots];
+  __shared__ int32_t scan[kSortWaves];
+  __shared__ int32_t lower;
+  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+  const uint32_t bucket = blockIdx.x, buckets = 1u << bucket_log2;
+  for (int i = threadIdx.x; i < kSortWaves * kMaxSlots; i += kSortThreads)
+    ((int32_t*)cnt)[i] = 0;
+  if (threadIdx.x == 0) lower = 0;
+  __syncthreads();
+  // each wave has a stretch of the tokens, a multiple of 64
+  const int64_t per = ((int64_t)n + kSortThreads - 1) / kSortThreads * 64;
+  const int64_t begin = wave * per, end = begin + per < n ? begin + per : n;
+  int32_t less = 0;
+  for (int64_t t = begin + lane; t < end; t += 64) {
+    const int64_t v = local_id<I>(ids, t, start);
+    if (v < 0 || v >= vocab) continue;
+    const uint32_t b = (uint32_t)v & (buckets - 1);
+    less += b < bucket;
+    if (b == bucket) atomicAdd(&cnt[wave][(uint32_t)v >> bucket_log2], 1);
+  }
+  for (int d = 1; d < 64; d <<= 1) less += __shfl_xor(less, d, 64);
+  if (lane == 0 && less) atomicAdd(&lower, less);
+  __syncthreads();
+  // a thread per id: its tokens before each wave, and all ids' before it
+  int32_t total = 0;
+  if (threadIdx.x < kMaxSlots)
+    for (int w = 0; w < kSortWaves; w++) {
+      const int32_t c = cnt[w][threadIdx.x];
+      cnt[w][threadIdx.x] = total;
+      total += c;
+    }
+  int32_t upto = total;
+  for (int d = 1; d < 64; d <<= 1) {
+    const int32_t o = __shfl_up(upto, d, 64);
+    if (lane >= d) upto += o;
+  }
+  if (lane == 63) scan[wave] = upto;
+  __syncthreads();
+  int32_t at = lower + upto - total;
+  for (int w = 0; w < wave; w++) at += scan[w];
+  if (threadIdx.x < kMaxSlots) {
+    for (int w = 0; w < kSortWaves; w++) cnt[w][threadIdx.x] += at;
+    const int64_t v = ((int64_t)threadIdx.x << bucket_log2) + bucket;
+    if (v < vocab) {
+      first[v] = at;
+      count[v] = total;
+    }
+  }
+  if (bucket == buckets - 1 && threadIdx.x == kMaxSlots - 1) *n_valid = at + total;
+  __syncthreads();
+  for (int64_t t0 = begin; t0 < end; t0 += 64) {
+    const int64_t t = t0 + lane;
+    int64_t v = -1;
+    if (t < end) v = local_id<I>(ids, t, start);
+    const bool mine = v >= 0 && v < vocab && ((uint32_t)v & (buckets - 1)) == bucket;
+    const int32_t slot = (int32_t)((uint32_t)v >> bucket_log2);
+    uint64_t todo = __ballot(mine);
+    while (todo) {  // one id of these 64 tokens at a time, its tokens in order
+      const int leader = __builtin_ctzll(todo);
+      const int32_t s = __builtin_amdgcn_readlane(slot, leader);
+      const bool same = mine && slot == s;
+      const uint64_t peers = __ballot(same);
+      if (same) {
+        const int32_t place =
+            cnt[wave][s] + (int32_t)__builtin_popcountll(peers & ((1ull << lane) - 1));
+        order[place] = (int32_t)t;
+        sorted[place] = (int32_t)v;
+        if (lane == leader) cnt[wave][s] += (int32_t)__builtin_popcountll(peers);
+      }
+      todo &= ~peers;
+    }
+  }
+}
+
+template <int TT, bool TWIDE>
+__device__ __forceinline__ void put_row(elem_t<TT>* p, int64_t n, f32x8 sum, float scale,
+                                        bool add) {
+  f32x8 x = sum * scale;
+  if (add) x += load8<TT, TWIDE>(p, n);
+  store8<TT, TWIDE>(p, n, x);
+}
+
+template <int DT, int TT, bool WIDE, bool TWIDE>
+__global__ __launch_bounds__(256) void reduce_kernel(
+    const elem_t<DT>* __restrict__ grad, int64_t grad_stride, elem_t<TT>* __restrict__ table,
+    int64_t table_stride, int64_t vocab, int64_t width, float scale, int accumulate,
+    const int32_t* __restrict__ order, const int32_t* __restrict__ sorted,
+    const int32_t* __restrict__ first, const int32_t* __restrict__ count,
+    const int32_t* __restrict__ n_valid, float* __restrict__ parts, int64_t part_stride,
+    int64_t run_items, int64_t slabs) {
+  const int lane = threadIdx.x & 63;
+  const int64_t item = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
+  const int64_t unit = item / slabs;
+  const int64_t c = (item - unit * slabs) * kCols + lane * 8;
+  const int64_t left = width - c;
+  if (unit >= run_items) {  // ids without tokens
+    if (left <= 0 || accumulate) return;
+    const f32x8 zero = {};
+    const int64_t v0 = (unit - run_items) * kZeroRows;
+    for (int i = 0; i < kZeroRows && v0 + i < vocab; i++)
+      if (count[v0 + i] == 0) store8<TT, TWIDE>(table + (v0 + i) * table_stride + c, left, zero);
+    return;
+  }
+  const int64_t valid = *n_valid;
+  const int64_t p0 = unit * kRun;
+  const int n = (int)(valid - p0 < kRun ? valid - p0 : kRun);
+  if (n <= 0) return;
+  const int64_t mine = p0 + (lane < n ? lane : n - 1);
+  const int32_t my_t = order[mine], my_v = sorted[mine];
+  const int32_t my_first = first[my_v], my_count = count[my_v];
+  f32x8 sum = {};
+  for (int i = 0; i < n; i += 4) {
+    f32x8 x[4];
+#pragma unroll
+    for (int j = 0; j < 4; j++) {
+      const int k = i + j < n ? i + j : n - 1;
+      const int64_t t = __builtin_amdgcn_readlane(my_t, k);
+      x[j] = left > 0 ? load8<DT, WIDE>(grad + t * grad_stride + c, left) : f32x8{};
+    }
+#pragma unroll
+    for (int j = 0; j < 4; j++) {
+      if (i + j >= n) break;
+      sum += x[j];
+      const int64_t b = __builtin_amdgcn_readlane(my_first, i + j);
+      const int64_t e = b + __builtin_amdgcn_readlane(my_count, i + j);
+      const int64_t next = p0 + i + j + 1;
+      if (next != e && i + j + 1 < n) continue;
+      if (left > 0) {  // the id's last token, or the run's
+        if (b >= p0 && next == e) {
+          const int64_t v = __builtin_amdgcn_readlane(my_v, i + j);
+          put_row<TT, TWIDE>(table + v * table_stride + c, left, sum, scale, accumulate != 0);
+        } else {  // slot 0: the id came from the run before; slot 1: it begins here
+          float* part = parts + (unit * 2 + (b >= p0)) * part_stride + c;
+          store8<ZS_F32, true>(part, 8, sum);
+        }
+      }
+      sum = f32x8{};
+    }
+  }
+}
+
+template <int TT, bool TWIDE>
+__global__ __launch_bounds__(256) void join_kernel(
+    elem_t<TT>* __restrict__ table, int64_t table_stride, int64_t width, float scale,
+    int accumulate, const int32_t* __restrict__ sorted, const int32_t* __restrict__ first,
+    const int32_t* __restrict__ count, const int32_t* __restrict__ n_valid,
+    const float* __restrict__ parts, int64_t part_stride, int64_t run_items, int64_t slabs) {
+  const int lane = threadIdx.x & 63;
+  const int64_t item = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
+  const int64_t unit = item / slabs;
+  const int64_t c = (item - unit * slabs) * kCols + lane * 8;
+  if (unit >= run_items) return;
+  const int64_t last = unit * kRun + kRun - 1;
+  if (last + 1 >= *n_valid) return;  // nothing follows this run
+  const int32_t v = sorted[last];
+  const int64_t b = first[v], e = b + count[v];
+  if (b < unit * kRun || e <= last + 1) return;  // the id begins earlier, or ends here
+  const int64_t left = width - c;
+  if (left <= 0) return;
+  f32x8 sum = load8<ZS_F32, true>(parts + (unit * 2 + 1) * part_stride + c, 8);
+  const int64_t end = (e - 1) / kRun;
+  int64_t r = unit + 1;
+  for (; r + 4 <= end + 1; r += 4) {
+    f32x8 x[4];
+#pragma unroll
+    for (int j = 0; j < 4; j++)
+      x[j] = load8<ZS_F32, true>(parts + (r + j) * 2 * part_stride + c, 8);
+#pragma unroll
+    for (int j = 0; j < 4; j++) sum += x[j];
+  }
+  for (; r <= end; r++) sum += load8<ZS_F32, true>(parts + r * 2 * part_stride + c, 8);
+  put_row<TT, TWIDE>(table + (int64_t)v * table_stride + c, left, sum, scale, accumulate != 0);
+}
+
+struct Layout {
+  int bucket_log2;
+  int64_t runs, slabs, part_stride;
+  size_t order, sorted, first, count, n_valid, parts, total;
+};
+constexpr int64_t kMaxVocab = 1 << 24, kMaxTokens = 0x7fffffff;
+
+Layout layout(int64_t n, int64_t vocab, int64_t width) {
+  Layout l{};
+  l.bucket_log2 = 8;
+  while (((vocab + (1ll << l.bucket_log2) - 1) >> l.bucket_log2) > kMaxSlots) l.bucket_log2++;
+  l.runs = (n + kRun - 1) / kRun;
+  l.slabs = (width + kCols - 1) / kCols;
+  l.part_stride = (width + 7) / 8 * 8;
+  size_t at = 0;
+  auto take = [&](size_t bytes) {
+    const size_t p = at;
+    at += up256(bytes);
+    return p;
+  };
+  l.order = take((size_t)n * 4);
+  l.sorted = take((size_t)n * 4);
+  l.first = take((size_t)vocab * 4);
+  l.count = take((size_t)vocab * 4);
+  l.n_valid = take(4);
+  l.parts = take((size_t)l.runs * 2 * l.part_stride * 4);
+  l.total = at;
+  return l;
+}
+
+constexpr int64_t kMaxWidth = 1 << 20, kMaxBlocks = 0x7fffff;  // 2^31 lanes of a launch
+
+int check_ids(const char* who, const void* ids, int64_t n, int64_t vocab, int64_t width,
+              int32_t id_bytes, float scale) {
+  if (n < 0 || vocab < 1 || vocab > kMaxVocab || width < 1 || width > kMaxWidth ||
+      n > kMaxTokens)
+    return fail(who, "a size is out of range");
+  if (id_bytes != 4 && id_bytes != 8) return fail(who, "ids are 4 or 8 bytes");
+  if (n && !ids) return fail(who, "ids is NULL");
+  if (!al(ids, id_bytes)) return fail(who, "ids are not aligned to their size");
+  if (!__builtin_isfinite(scale)) return fail(who, "scale must be finite");
+  return ZS_OK;
+}
+
+}  // namespace
+}  // namespace ops
+}  // namespace zs
+
+using namespace zs::ops;
+
+extern "C" int zs_embed_forward(const void* table, int64_t table_stride, const void* ids,
+                                void* out, int64_t out_stride, int64_t n_tokens, int64_t vocab,
+                                int64_t width, int64_t vocab_start, float scale, int32_t dtype,
+                                int32_t id_bytes, void* stream) {
+  const char* who = "zs_embed_forward";
+  if (!good_dtype(dtype)) return fail(who, "unknown element type");
+  if (int rc = check_ids(who, ids, n_tokens, vocab, width, id_bytes, scale)) return rc;
+  if (table_stride < width || out_stride < width) return fail(who, "a row stride is below width");
+  if (n_tokens == 0) return ZS_OK;
+  if (!table || !out) return fail(who, "NULL buffer");
+  if (!al(table, elem_bytes(dtype)) || !al(out, elem_bytes(dtype)))
+    return fail(who, "a buffer is not aligned to its elements");
+  int log2 = 3;
+  while (log2 < 8 && (8ll << log2) < width) log2++;
+  const int64_t blocks = (n_tokens + (256 >> log2) - 1) >> (8 - log2);
+  if (blocks > kMaxBlocks) return fail(who, "too many tokens for one call");
+  const bool w = wide(table, table_stride, dtype) && wide(out, out_stride, dtype);
+  with_dtype(dtype, [&](auto DT) {
+    with_bool(w, [&](auto W) {
+      with_bool(id_bytes == 8, [&](auto I8) {
+        using E = elem_t<decltype(DT)::value>;
+        using I = std::conditional_t<decltype(I8)::value, int64_t, int32_t>;
+        gather_kernel<decltype(DT)::value, decltype(W)::value, I>
+            <<<dim3((uint32_t)blocks), dim3(256), 0, (hipStream_t)stream>>>(
+                (const E*)table, table_stride, ids, (E*)out, out_stride, n_tokens, vocab, width,
+                vocab_start, scale, log2);
+      });
+    });
+  });
+  return launched(who);
+}
+
+extern "C" size_t zs_embed_backward_bytes(int64_t n_tokens, int64_t vocab, int64_t width) {
+  if (n_tokens < 0 || n_tokens > kMaxTokens || vocab < 1 || vocab > kMaxVocab || width < 1 ||
+      width > kMaxWidth)
+    return 0;
+  return layout(n_tokens, vocab, width).total;
+}
+
+extern "C" int zs_embed_backward(const void* grad_out, int64_t grad_stride, const void* ids,
+                                 void* grad_table, int64_t table_stride, int64_t n_tokens,
+                                 int64_t vocab, int64_t width, int64_t vocab_start, float scale,
+                                 int32_t dtype, int32_t table_dtype, int32_t id_bytes,
+                                 int32_t accumulate, void* workspace, size_t workspace_bytes,
+                                 void* stream) {
+  const char* who = "zs_embed_backward";
+  if (!good_dtype(dtype)) return fail(who, "unknown element type");
+  if (table_dtype != dtype && table_dtype != ZS_F32)
+    return fail(who, "the table's gradient has the gradient's type or fp32");
+  if (int rc = check_ids(who, ids, n_tokens, vocab, width, id_bytes, scale)) return rc;
+  if (table_stride < width || grad_stride < width)
+    return fail(who, "a row stride is below width");
+  if (!grad_table || (n_tokens && !grad_out)) return fail(who, "NULL buffer");
+  if (!al(grad_table, elem_bytes(table_dtype)) || !al(grad_out, elem_bytes(dtype)))
+    return fail(who, "a buffer is not aligned to its elements");
+  const Layout l = layout(n_tokens, vocab, width);
+  if (!workspace || !al(workspace, 256)) return fail(who, "the workspace is NULL or not 256-byte aligned");
+  if (workspace_bytes < l.total) return fail(who, "the workspace is too small");
+  const int64_t zero_items = accumulate ? 0 : (vocab + kZeroRows - 1) / kZeroRows;
+  const int64_t blocks = ((l.runs + zero_items) * l.slabs + 3) / 4;
+  const int64_t join_blocks = (l.runs * l.slabs + 3) / 4;
+  if (blocks > kMaxBlocks) return fail(who, "too many rows for one call");
+  if (blocks == 0) return ZS_OK;  // no tokens to add
+  uint8_t* ws = (uint8_t*)workspace;
+  int32_t *order = (int32_t*)(ws + l.order), *sorted = (int32_t*)(ws + l.sorted),
+          *first = (int32_t*)(ws + l.first), *count = (int32_t*)(ws + l.count),
+          *n_valid = (int32_t*)(ws + l.n_valid);
+  float* parts = (float*)(ws + l.parts);
+  hipStream_t s = (hipStream_t)stream;
+  with_bool(id_bytes == 8, [&](auto I8) {
+    using I = std::conditional_t<decltype(I8)::value, int64_t, int32_t>;
+    sort_kernel<I><<<dim3(1u << l.bucket_log2), dim3(kSortThreads), 0, s>>>(
+        ids, (int32_t)n_tokens, vocab, vocab_start, l.bucket_log2, order, sorted, first, count,
+        n_valid);
+  });
+  if (int rc = launched(who)) return rc;
+  const bool w = wide(grad_out, grad_stride, dtype), tw = wide(grad_table, table_stride, table_dtype);
+  auto go = [&](auto DT, auto TT) {
+    with_bool(w, [&](auto W) {
+      with_bool(tw, [&](auto TW) {
+        using E = elem_t<decltype(DT)::value>;
+        using T = elem_t<decltype(TT)::value>;
+        reduce_kernel<decltype(DT)::value, decltype(TT)::value, decltype(W)::value,
+                      decltype(TW)::value><<<dim3((uint32_t)blocks), dim3(256), 0, s>>>(
+            (const E*)grad_out, grad_stride, (T*)grad_table, table_stride, vocab, width, scale,
+            accumulate, order, sorted, first, count, n_valid, parts, l.part_stride, l.runs,
+            l.slabs);
+      });
+    });
+    if (l.runs > 1)
+      with_bool(tw, [&](auto TW) {
+        using T = elem_t<decltype(TT)::value>;
+        join_kernel<decltype(TT)::value, decltype(TW)::value>
+            <<<dim3((uint32_t)join_blocks), dim3(256), 0, s>>>(
+                (T*)grad_table, table_stride, width, scale, accumulate, sorted, first, count,
+                n_valid, parts, l.part_stride, l.runs, l.slabs);
+      });
+  };
+  if (table_dtype == dtype)
+    with_dtype(dtype, [&](auto DT) { go(DT, DT); });
+  else
+    with_dtype(dtype, [&](auto DT) { go(DT, std::integral_constant<int, ZS_F32>()); });
+  return launched(who);
+}

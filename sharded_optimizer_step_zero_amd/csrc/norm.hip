@@ -1,0 +1,336 @@
+// norm.hip -- root-mean-square norm with the residual's addition and an 8-bit
+// output, and its gradient.
+//
+// Forward, a row at a time: s = x + r (rounded and stored), rstd = 1 /
+// sqrt(mean(s^2) + eps), y = s * rstd * w.  The row stays in registers between
+// the sum of squares and the output, so every array is read or written once; 8
+// elements a lane, a row over a workgroup (or a part of one for narrow rows).
+// A group's largest magnitude is a maximum over 4, 8 or 16 neighbouring lanes, so
+// the 8-bit output needs neither LDS nor a second pass.
+//
+// Backward: with h = s * rstd, dx = rstd * (w dy - h * mean(w dy h)) + ds.  dw =
+// sum over rows of dy h: a workgroup takes every n-th row and keeps its part of dw
+// in registers; a second kernel adds the parts in a fixed order.
+//
+// Both are bound by HBM.  Sums, means and rstd are fp32.
+#include "ops.h"
+
+namespace zs {
+namespace ops {
+namespace {
+
+constexpr int64_t kMaxWidth = 65536;
+constexpr int64_t kMaxBlocks = 0x7fffff;
+constexpr int kBackwardGroups = 512;  // parts of dw, for rows wider than 512
+
+// How a row is spread: `lanes` threads with nc chunks of 8 each; rows up to 512
+// wide share a workgroup of 256.
+struct Shape {
+  int lanes, nc, threads;
+};
+Shape shape(int64_t width) {
+  const int64_t chunks = (width + 7) / 8;
+  if (chunks <= 64) {
+    int lanes = 16;
+    while (lanes < chunks) lanes *= 2;
+    return {lanes, 1, 256};
+  }
+  if (chunks <= 128) return {128, 1, 128};
+  int nc = 1, lanes = 256;
+  while (nc < 8 && nc * lanes < chunks) nc *= 2;
+  while (nc * lanes < chunks) lanes *= 2;
+  return {lanes, nc, lanes};
+}
+
+// Sum over the row's threads: within a wave by shuffles, across waves through LDS
+// (each call its own slots, written before and read after one barrier).
+__device__ __forceinline__ float row_sum(float x, int lanes, float* slots) {
+  const int w = lanes < 64 ? lanes : 64;
+  for (int d = 1; d < w; d <<= 1) x += __shfl_xor(x, d, 64);
+  if (lanes <= 64) return x;
+  if ((threadIdx.x & 63) == 0) slots[threadIdx.x >> 6] = x;
+  __syncthreads();
+  float s = 0.0f;
+  for (int i = 0; i < lanes / 64; i++) s += slots[i];
+  return s;
+}
+
+template <int DT, bool WIDE, int NC, int CODE>
+__global__ __launch_bounds__(1024) void norm_kernel(
+    const elem_t<DT>* x, int64_t x_stride, const elem_t<DT>* residual, int64_t residual_stride,
+    const elem_t<DT>* __restrict__ weight, elem_t<DT>* sum, int64_t sum_stride,
+    elem_t<DT>* __restrict__ y, int64_t y_stride, uint8_t* __restrict__ codes,
+    uint8_t* __restrict__ scales, float* __restrict__ rstd, int64_t rows, int64_t width,
+    float eps, int lanes, int rows_per_block, int group_lanes) {
+  __shared__ float slots[16];
+  const int in_row = threadIdx.x & (lanes - 1);
+  const int64_t row = (int64_t)blockIdx.x * rows_per_block + (rows_per_block > 1 ? threadIdx.x / lanes : 0);
+  const bool live = row < rows;  // no early return: the shuffles and barriers are the workgroup's
+  f32x8 s[NC];
+  float sq = 0.0f;
+#pragma unroll
+  for (int k = 0; k < NC; k++) {
+    const int64_t c = (int64_t)(k * lanes + in_row) * 8, left = live ? width - c : 0;
+    s[k] = f32x8{};
+    if (left > 0) {
+      s[k] = load8<DT, WIDE>(x + row * x_stride + c, left);
+      if (residual) {
+        s[k] += load8<DT, WIDE>(residual + row * residual_stride + c, left);
+        // the stored, rounded sum is what is normalised
+        s[k] = __builtin_convertvector(__builtin_convertvector(s[k], typename Elem<DT>::vec), f32x8);
+        store8<DT, WIDE>(sum + row * sum_stride + c, left, s[k]);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < 8; i++) sq += s[k][i] * s[k][i];
+  }
+  const float total = row_sum(sq, lanes, slots);
+  const float r = 1.0f / __builtin_sqrtf(total / (float)width + eps);
+  if (live && in_row == 0) rstd[row] = r;
+  const int64_t groups = (width + group_lanes * 8 - 1) / (group_lanes * 8);
+#pragma unroll
+  for (int k = 0; k < NC; k++) {
+    const int64_t chunk = k * lanes + in_row, c = chunk * 8, left = live ? width - c : 0;
+    f32x8 v = {};
+    if (left > 0) {
+      v = s[k] * r * load8<DT, WIDE>(weight + c, left);
+      if (y) store8<DT, WIDE>(y + row * y_stride + c, left, v);
+    }
+    if (CODE >= 0) {
+      uint32_t byte;
+      const u32x2 w = quantise8<CODE < 0 ? 0 : CODE>(v, group_lanes, &byte);
+      if (left > 0) {
+        store_codes<WIDE>(codes + row * width + c, left, w);
+        if (chunk % group_lanes == 0) scales[row * groups + chunk / group_lanes] = (uint8_t)byte;
+      }
+    }
+  }
+}
+
+template <int DT, bool WIDE, int NC>
+__global__ __launch_bounds__(1024) void norm_grad_kernel(
+    const elem_t<DT>* dy, int64_t dy_stride, const elem_t<DT>* __restrict__ sum,
+    int64_t sum_stride, const elem_t<DT>* __restrict__ weight, const float* __restrict__ rstd,
+    const elem_t<DT>* ds, int64_t ds_stride, elem_t<DT>* dx, int64_t dx_stride,
+    float* __restrict__ parts, int64_t part_stride, int64_t rows, int64_t width, int lanes,
+    int rows_per_block) {
+  __shared__ float slots[2][16];
+  const int in_row = threadIdx.x & (lanes - 1);
+  const int sub = rows_per_block > 1 ? threadIdx.x / lanes : 0;
+  const int64_t step = (int64_t)gridDim.x * rows_per_block;
+  const float inv_width = 1.0f / (float)width;
+  f32x8 w[NC], dw[NC];
+#pragma unroll
+  for (int k = 0; k < NC; k++) {
+    const int64_t c = (int64_t)(k * lanes + in_row) * 8;
+    w[k] = width > c ? load8<DT, WIDE>(weight + c, width - c) : f32x8{};
+    dw[k] = f32x8{};
+  }
+  int turn = 0;
+  for (int64_t row0 = (int64_t)blockIdx.x * rows_per_block; row0 < rows; row0 += step, turn ^= 1) {
+    const int64_t row = row0 + sub;
+    const bool live = row < rows;
+    const float r = live ? rstd[row] : 0.0f;
+    f32x8 h[NC], g[NC];
+    float dot = 0.0f;
+#pragma unroll
+    for (int k = 0; k < NC; k++) {
+      const int64_t c = (int64_t)(k * lanes + in_row) * 8, left = live ? width - c : 0;
+      h[k] = g[k] = f32x8{};
+      if (left > 0) {
+        h[k] = load8<DT, WIDE>(sum + row * sum_stride + c, left);
+        g[k] = load8<DT, WIDE>(dy + row * dy_stride + c, left);
+#pragma unroll
+        for (int i = 0; i < 8; i++) {
+          h[k][i] *= r;
+          dw[k][i] += g[k][i] * h[k][i];
+          g[k][i] *= w[k][i];
+          dot += g[k][i] * h[k][i];
+        }
+      }
+    }
+    const float mean = row_sum(dot, lanes, slots[turn]) * inv_width;
+#pragma unroll
+    for (int k = 0; k < NC; k++) {
+      const int64_t c = (int64_t)(k * lanes + in_row) * 8, left = live ? width - c : 0;
+      if (left > 0) {
+        f32x8 v = (g[k] - h[k] * mean) * r;
+        if (ds) v += load8<DT, WIDE>(ds + row * ds_stride + c, left);
+        store8<DT, WIDE>(dx + row * dx_stride + c, left, v);
+      }
+    }
+  }
+  float* part = parts + ((int64_t)blockIdx.x * rows_per_block + sub) * part_stride;
+#pragma unroll
+  for (int k = 0; k < NC; k++) {
+    const int64_t c = (int64_t)(k * lanes + in_row) * 8;
+    if (c < width) store8<ZS_F32, true>(part + c, 8, dw[k]);
+  }
+}
+
+// dw[c] = the sum of the parts' column c: 16 slices of the parts a workgroup, each
+// in order, then the slices in order.
+template <int WT>
+__global__ __launch_bounds__(1024) void columns_kernel(const float* __restrict__ parts,
+                                                       int64_t part_stride, int64_t n_parts,
+                                                       elem_t<WT>* __restrict__ dw,
+                                                       int64_t width) {
+  __shared__ float slots[16][64];
+  const int lane = threadIdx.x & 63, slice = threadIdx.x >> 6;
+  const int64_t c = (int64_t)blockIdx.x * 64 + lane;
+  const int64_t per = (n_parts + 15) / 16, begin = slice * per;
+  const int64_t end = begin + per < n_parts ? begin + per : n_parts;
+  float s = 0.0f;
+  if (c < width) {
+#pragma unroll 8
+    for (int64_t p = begin; p < end; p++) s += parts[p * part_stride + c];
+  }
+  slots[slice][lane] = s;
+  __syncthreads();
+  if (slice == 0 && c < width) {
+    s = 0.0f;
+    for (int i = 0; i < 16; i++) s += slots[i][lane];
+    dw[c] = (elem_t<WT>)s;
+  }
+}
+
+template <typename F>
+void with_nc(int nc, F f) {
+  if (nc == 1)
+    f(std::integral_constant<int, 1>());
+  else if (nc == 2)
+    f(std::integral_constant<int, 2>());
+  else if (nc == 4)
+    f(std::integral_constant<int, 4>());
+  else
+    f(std::integral_constant<int, 8>());
+}
+
+// Workgroups of the backward pass, and parts of dw.
+int64_t grad_blocks(int64_t rows, const Shape& s) {
+  const int per = s.threads / s.lanes;
+  const int64_t need = (rows + per - 1) / per;
+  return need < kBackwardGroups ? need : kBackwardGroups;
+}
+
+int64_t part_stride_of(int64_t width) { return (width + 7) / 8 * 8; }
+
+}  // namespace
+}  // namespace ops
+}  // namespace zs
+
+using namespace zs::ops;
+
+extern "C" int zs_norm_forward(const void* x, int64_t x_stride, const void* residual,
+                               int64_t residual_stride, const void* weight, void* sum,
+                               int64_t sum_stride, void* y, int64_t y_stride, void* codes,
+                               void* scales, float* rstd, int64_t rows, int64_t width, float eps,
+                               int32_t dtype, int32_t code, int32_t group, void* stream) {
+  const char* who = "zs_norm_forward";
+  if (!good_dtype(dtype)) return fail(who, "unknown element type");
+  if (rows < 0 || rows > 0x7fffffff || width < 1 || width > kMaxWidth)
+    return fail(who, "a size is out of range");
+  if (!(eps >= 0.0f) || !__builtin_isfinite(eps)) return fail(who, "eps must be finite and not negative");
+  if ((codes == nullptr) != (scales == nullptr)) return fail(who, "codes and scales go together");
+  if ((residual == nullptr) != (sum == nullptr)) return fail(who, "residual and sum go together");
+  if (codes && ((code != ZS_E4M3 && code != ZS_E5M2) || !good_group(group)))
+    return fail(who, "the 8-bit form is e4m3 or e5m2 in groups of 32, 64 or 128");
+  if (x_stride < width || (residual && (residual_stride < width || sum_stride < width)) ||
+      (y && y_stride < width))
+    return fail(who, "a row stride is below width");
+  if (rows == 0) return ZS_OK;
+  if (!x || !weight || !rstd) return fail(who, "NULL buffer");
+  const int eb = elem_bytes(dtype);
+  if (!al(x, eb) || !al(residual, eb) || !al(weight, eb) || !al(sum, eb) || !al(y, eb) ||
+      !al(rstd, 4))
+    return fail(who, "a buffer is not aligned to its elements");
+  const Shape s = shape(width);
+  const int per = s.threads / s.lanes;
+  const int64_t blocks = (rows + per - 1) / per;
+  if (blocks > kMaxBlocks) return fail(who, "too many rows for one call");
+  const bool w = wide(x, x_stride, dtype) && al(weight, 16) &&
+                 (!residual || (wide(residual, residual_stride, dtype) && wide(sum, sum_stride, dtype))) &&
+                 (!y || wide(y, y_stride, dtype)) && (!codes || (width % 8 == 0 && al(codes, 8)));
+  const int group_lanes = codes ? group / 8 : 16;
+  with_dtype(dtype, [&](auto DT) {
+    with_bool(w, [&](auto W) {
+      with_nc(s.nc, [&](auto NC) {
+        auto go = [&](auto CODE) {
+          using E = elem_t<decltype(DT)::value>;
+          norm_kernel<decltype(DT)::value, decltype(W)::value, decltype(NC)::value,
+                      decltype(CODE)::value>
+              <<<dim3((uint32_t)blocks), dim3(s.threads), 0, (hipStream_t)stream>>>(
+                  (const E*)x, x_stride, (const E*)residual, residual_stride, (const E*)weight,
+                  (E*)sum, sum_stride, (E*)y, y_stride, (uint8_t*)codes, (uint8_t*)scales, rstd,
+                  rows, width, eps, s.lanes, per, group_lanes);
+        };
+        if (!codes)
+          go(std::integral_constant<int, -1>());
+        else
+          with_code(code, go);
+      });
+    });
+  });
+  return launched(who);
+}
+
+extern "C" size_t zs_norm_backward_bytes(int64_t rows, int64_t width) {
+  if (rows < 0 || rows > 0x7fffffff || width < 1 || width > kMaxWidth) return 0;
+  const Shape s = shape(width);
+  const size_t parts = (size_t)grad_blocks(rows, s) * (s.threads / s.lanes);
+  return up256(parts * part_stride_of(width) * 4) + 256;
+}
+
+extern "C" int zs_norm_backward(const void* dy, int64_t dy_stride, const void* sum,
+                                int64_t sum_stride, const void* weight, const float* rstd,
+                                const void* grad_sum, int64_t grad_sum_stride, void* grad_x,
+                                int64_t grad_x_stride, void* grad_weight, int64_t rows,
+                                int64_t width, int32_t dtype, int32_t weight_dtype,
+                                void* workspace, size_t workspace_bytes, void* stream) {
+  const char* who = "zs_norm_backward";
+  if (!good_dtype(dtype)) return fail(who, "unknown element type");
+  if (weight_dtype != dtype && weight_dtype != ZS_F32)
+    return fail(who, "the weight's gradient has the weight's type or fp32");
+  if (rows < 0 || rows > 0x7fffffff || width < 1 || width > kMaxWidth)
+    return fail(who, "a size is out of range");
+  if (dy_stride < width || sum_stride < width || grad_x_stride < width ||
+      (grad_sum && grad_sum_stride < width))
+    return fail(who, "a row stride is below width");
+  if (!weight || !grad_weight || (rows && (!dy || !sum || !rstd || !grad_x)))
+    return fail(who, "NULL buffer");
+  const int eb = elem_bytes(dtype);
+  if (!al(dy, eb) || !al(sum, eb) || !al(weight, eb) || !al(rstd, 4) || !al(grad_sum, eb) ||
+      !al(grad_x, eb) || !al(grad_weight, elem_bytes(weight_dtype)))
+    return fail(who, "a buffer is not aligned to its elements");
+  if (!workspace || !al(workspace, 256)) return fail(who, "the workspace is NULL or not 256-byte aligned");
+  if (workspace_bytes < zs_norm_backward_bytes(rows, width))
+    return fail(who, "the workspace is too small");
+  const Shape s = shape(width);
+  const int per = s.threads / s.lanes;
+  const int64_t blocks = grad_blocks(rows, s);
+  const int64_t stride = part_stride_of(width);
+  const bool w = wide(dy, dy_stride, dtype) && wide(sum, sum_stride, dtype) && al(weight, 16) &&
+                 wide(grad_x, grad_x_stride, dtype) &&
+                 (!grad_sum || wide(grad_sum, grad_sum_stride, dtype));
+  if (blocks)
+    with_dtype(dtype, [&](auto DT) {
+      with_bool(w, [&](auto W) {
+        with_nc(s.nc, [&](auto NC) {
+          using E = elem_t<decltype(DT)::value>;
+          norm_grad_kernel<decltype(DT)::value, decltype(W)::value, decltype(NC)::value>
+              <<<dim3((uint32_t)blocks), dim3(s.threads), 0, (hipStream_t)stream>>>(
+                  (const E*)dy, dy_stride, (const E*)sum, sum_stride, (const E*)weight, rstd,
+                  (const E*)grad_sum, grad_sum_stride, (E*)grad_x, grad_x_stride,
+                  (float*)workspace, stride, rows, width, s.lanes, per);
+        });
+      });
+    });
+  if (int rc = launched(who)) return rc;
+  with_dtype(weight_dtype, [&](auto WT) {
+    columns_kernel<decltype(WT)::value>
+        <<<dim3((uint32_t)((width + 63) / 64)), dim3(1024), 0, (hipStream_t)stream>>>(
+            (const float*)workspace, stride, blocks * per, (elem_t<decltype(WT)::value>*)grad_weight,
+            width);
+  });
+  return launched(who);
+}

@@ -1,0 +1,243 @@
+// ops.h -- what the model operators' kernels share: reading and writing rows of
+// any element type eight elements at a time, the 8-bit form, and argument checks.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include <string>
+#include <type_traits>
+
+#include "../../include/zeroshard.h"
+#include "../../include/zeroshard_ops.h"
+#include "abi_internal.h"
+
+namespace zs {
+namespace ops {
+
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+typedef float f32x2 __attribute__((ext_vector_type(2)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef float f32x8 __attribute__((ext_vector_type(8)));
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
+
+template <int DT>
+struct Elem;
+template <>
+struct Elem<ZS_F32> {
+  using type = float;
+  using vec = f32x8;
+};
+template <>
+struct Elem<ZS_BF16> {
+  using type = __bf16;
+  using vec = bf16x8;
+};
+template <>
+struct Elem<ZS_F16> {
+  using type = _Float16;
+  using vec = f16x8;
+};
+template <int DT>
+using elem_t = typename Elem<DT>::type;
+
+// Eight elements of a row from p on, as fp32; n of them exist (the rest read as
+// 0).  WIDE: p is 16-byte aligned, so a whole chunk is one or two wide loads.
+template <int DT, bool WIDE>
+__device__ __forceinline__ f32x8 load8(const elem_t<DT>* p, int64_t n) {
+  using V = typename Elem<DT>::vec;
+  f32x8 r;
+  if (WIDE && n >= 8) {
+    if constexpr (DT == ZS_F32) {  // 16-byte aligned only
+      const f32x4 a = *(const f32x4*)p, b = *(const f32x4*)(p + 4);
+      return __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7);
+    } else {
+      return __builtin_convertvector(*(const V*)p, f32x8);
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < 8; i++) r[i] = i < n ? (float)p[i] : 0.0f;
+  return r;
+}
+
+// Rounds to the element type (nearest, ties to even) and stores.
+template <int DT, bool WIDE>
+__device__ __forceinline__ void store8(elem_t<DT>* p, int64_t n, f32x8 x) {
+  using V = typename Elem<DT>::vec;
+  const V v = __builtin_convertvector(x, V);
+  if (WIDE && n >= 8) {
+    if constexpr (DT == ZS_F32) {
+      *(f32x4*)p = __builtin_shufflevector(v, v, 0, 1, 2, 3);
+      *(f32x4*)(p + 4) = __builtin_shufflevector(v, v, 4, 5, 6, 7);
+    } else {
+      *(V*)p = v;
+    }
+    return;
+  }
+#pragma unroll
+  for (int i = 0; i < 8; i++)
+    if (i < n) p[i] = v[i];
+}
+
+// ---------------------------------------------------------------- 8-bit form
+
+// The scale byte of a group with this largest magnitude.  1.75 * 2^top is the
+// format's largest value: a mantissa above .75 goes to the next power of two.
+template <int CODE>
+__device__ __forceinline__ uint32_t scale_byte(float amax) {
+  constexpr int top = CODE == ZS_E4M3 ? 8 : 15;
+  const uint32_t b = __float_as_uint(amax);
+  if (b >= 0x7f800000u) return 255u;
+  const int e = (int)((b + 0x1fffffu) >> 23) - top;  // biased by 127
+  return (uint32_t)(e < 0 ? 0 : e);
+}
+// 2^-e of a scale byte that is not 255 (byte 0: 2^127), and 2^e (255: NaN).
+__device__ __forceinline__ float scale_inverse(uint32_t byte) {
+  return __uint_as_float((254u - byte) << 23);
+}
+__device__ __forceinline__ float scale_value(uint32_t byte) {
+  if (byte == 255u) return __uint_as_float(0x7fc00000u);
+  return byte ? __uint_as_float(byte << 23) : __uint_as_float(0x00400000u);
+}
+
+template <int CODE>
+__device__ __forceinline__ u32x2 encode8(f32x8 x) {
+  u32x2 r;
+#pragma unroll
+  for (int h = 0; h < 2; h++) {
+    int w = 0;
+    if (CODE == ZS_E4M3) {
+      w = __builtin_amdgcn_cvt_pk_fp8_f32(x[4 * h], x[4 * h + 1], w, false);
+      w = __builtin_amdgcn_cvt_pk_fp8_f32(x[4 * h + 2], x[4 * h + 3], w, true);
+    } else {
+      w = __builtin_amdgcn_cvt_pk_bf8_f32(x[4 * h], x[4 * h + 1], w, false);
+      w = __builtin_amdgcn_cvt_pk_bf8_f32(x[4 * h + 2], x[4 * h + 3], w, true);
+    }
+    r[h] = (uint32_t)w;
+  }
+  return r;
+}
+template <int CODE>
+__device__ __forceinline__ f32x8 decode8(u32x2 w) {
+  f32x8 r;
+#pragma unroll
+  for (int h = 0; h < 2; h++) {
+    f32x2 a, b;
+    if (CODE == ZS_E4M3) {
+      a = __builtin_amdgcn_cvt_pk_f32_fp8((int)w[h], false);
+      b = __builtin_amdgcn_cvt_pk_f32_fp8((int)w[h], true);
+    } else {
+      a = __builtin_amdgcn_cvt_pk_f32_bf8((int)w[h], false);
+      b = __builtin_amdgcn_cvt_pk_f32_bf8((int)w[h], true);
+    }
+    r[4 * h] = a[0];
+    r[4 * h + 1] = a[1];
+    r[4 * h + 2] = b[0];
+    r[4 * h + 3] = b[1];
+  }
+  return r;
+}
+
+// Eight codes at p, n of them exist.  WIDE: p is 8-byte aligned.
+template <bool WIDE>
+__device__ __forceinline__ u32x2 load_codes(const uint8_t* p, int64_t n) {
+  if (WIDE && n >= 8) return *(const u32x2*)p;
+  u32x2 r = {0, 0};
+#pragma unroll
+  for (int i = 0; i < 8; i++)
+    if (i < n) r[i >> 2] |= (uint32_t)p[i] << (8 * (i & 3));
+  return r;
+}
+template <bool WIDE>
+__device__ __forceinline__ void store_codes(uint8_t* p, int64_t n, u32x2 w) {
+  if (WIDE && n >= 8) {
+    *(u32x2*)p = w;
+    return;
+  }
+#pragma unroll
+  for (int i = 0; i < 8; i++)
+    if (i < n) p[i] = (uint8_t)(w[i >> 2] >> (8 * (i & 3)));
+}
+
+// |x| as bits: integer order is the order of magnitudes, with NaN above
+// infinity, so a group's maximum also tells that it holds one.
+__device__ __forceinline__ uint32_t amax_bits(f32x8 x) {
+  uint32_t m = 0;
+#pragma unroll
+  for (int i = 0; i < 8; i++) {
+    const uint32_t b = __float_as_uint(x[i]) & 0x7fffffffu;
+    m = b > m ? b : m;
+  }
+  return m;
+}
+// The maximum over the 4, 8 or 16 neighbouring lanes (8 elements each) of a group.
+__device__ __forceinline__ float group_amax(f32x8 x, int lanes) {
+  uint32_t m = amax_bits(x);
+  for (int d = 1; d < lanes; d <<= 1) {
+    const uint32_t o = (uint32_t)__shfl_xor((int)m, d, 64);
+    m = o > m ? o : m;
+  }
+  return __uint_as_float(m);
+}
+// The group's codes and scale byte of the lane's eight elements.
+template <int CODE>
+__device__ __forceinline__ u32x2 quantise8(f32x8 x, int lanes, uint32_t* byte) {
+  const uint32_t b = scale_byte<CODE>(group_amax(x, lanes));
+  *byte = b;
+  const float inv = scale_inverse(b == 255u ? 127u : b);
+  f32x8 s;
+#pragma unroll
+  for (int i = 0; i < 8; i++) s[i] = x[i] * inv;
+  u32x2 w = encode8<CODE>(s);
+  if (b == 255u) w = u32x2{0, 0};
+  return w;
+}
+
+// ---------------------------------------------------------------- host side
+
+inline int fail(const char* who, const char* what) {
+  return einval((std::string(who) + ": " + what).c_str());
+}
+inline int elem_bytes(int32_t dtype) { return dtype == ZS_F32 ? 4 : 2; }
+inline bool good_dtype(int32_t d) { return d >= ZS_F32 && d <= ZS_F16; }
+inline bool good_group(int32_t g) { return g == 32 || g == 64 || g == 128; }
+inline bool al(const void* p, size_t n) { return ((uintptr_t)p % n) == 0; }
+// Rows that can be read 16 bytes at a time.
+inline bool wide(const void* p, int64_t stride, int32_t dtype) {
+  return al(p, 16) && (stride * elem_bytes(dtype)) % 16 == 0;
+}
+inline int launched(const char* who) {
+  const hipError_t e = hipGetLastError();
+  return e == hipSuccess ? ZS_OK : ehip(who, e);
+}
+inline size_t up256(size_t x) { return (x + 255) / 256 * 256; }
+
+// Calls f with the type as a constant.
+template <typename F>
+inline void with_dtype(int32_t dtype, F f) {
+  if (dtype == ZS_F32)
+    f(std::integral_constant<int, ZS_F32>());
+  else if (dtype == ZS_BF16)
+    f(std::integral_constant<int, ZS_BF16>());
+  else
+    f(std::integral_constant<int, ZS_F16>());
+}
+template <typename F>
+inline void with_bool(bool b, F f) {
+  if (b)
+    f(std::integral_constant<bool, true>());
+  else
+    f(std::integral_constant<bool, false>());
+}
+template <typename F>
+inline void with_code(int32_t code, F f) {
+  if (code == ZS_E4M3)
+    f(std::integral_constant<int, ZS_E4M3>());
+  else
+    f(std::integral_constant<int, ZS_E5M2>());
+}
+
+}  // namespace ops
+}  // namespace zs
