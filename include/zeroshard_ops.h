@@ -17,9 +17,8 @@
  * in zero_shard_last_error().  Calls queue kernels only and can be captured in a
  * graph.  Matrices are row-major with a row stride in elements (>= the width);
  * elements of a row are adjacent.  Nothing but element alignment is asked of data
- * pointers (rows at multiples of 16 bytes are read and written 16 bytes at a
- * time, others element by element); workspaces are 256-byte aligned.  Outputs
- * must not overlap inputs unless a call says so.  Sizes of zero are allowed where
+ * pointers; workspaces are 256-byte aligned.  Outputs must not overlap inputs
+ * unless a call says so.  Sizes of zero are allowed where
  * a call does not say otherwise, and null pointers for buffers of no elements.
  * Results do not depend on timing: every sum has a fixed order.
  *

@@ -47,7 +47,7 @@ __device__ __forceinline__ Place place(int lanes_log2, uint32_t per_row, int64_t
   return p;
 }
 
-template <int DT, bool WIDE, int CODE>
+template <int DT, bool NT, int CODE>
 __global__ __launch_bounds__(256) void pack_kernel(const elem_t<DT>* __restrict__ x,
                                                    int64_t x_stride, uint8_t* __restrict__ codes,
                                                    uint8_t* __restrict__ scales, int64_t rows,
@@ -56,15 +56,15 @@ __global__ __launch_bounds__(256) void pack_kernel(const elem_t<DT>* __restrict_
   const Place p = place(lanes_log2, per_row, rows, width);
   const int64_t c = p.chunk * 8, left = width - c;
   f32x8 v = {};
-  if (p.live) v = load8<DT, WIDE>(x + p.row * x_stride + c, left);
+  if (p.live) v = load8<DT, NT>(x + p.row * x_stride + c, left);
   uint32_t byte;
   const u32x2 w = quantise8<CODE>(v, group_lanes, &byte);
   if (!p.live) return;
-  store_codes<WIDE>(codes + p.row * width + c, left, w);
+  store_codes<NT>(codes + p.row * width + c, left, w);
   if (p.chunk % group_lanes == 0) scales[p.row * groups + p.chunk / group_lanes] = (uint8_t)byte;
 }
 
-template <int DT, bool WIDE, int CODE>
+template <int DT, bool NT, int CODE>
 __global__ __launch_bounds__(256) void unpack_kernel(const uint8_t* __restrict__ codes,
                                                      const uint8_t* __restrict__ scales,
                                                      elem_t<DT>* __restrict__ x, int64_t x_stride,
@@ -75,8 +75,8 @@ __global__ __launch_bounds__(256) void unpack_kernel(const uint8_t* __restrict__
   if (!p.live) return;
   const int64_t c = p.chunk * 8, left = width - c;
   const float s = scale_value(scales[p.row * groups + p.chunk / group_lanes]);
-  const f32x8 v = decode8<CODE>(load_codes<WIDE>(codes + p.row * width + c, left)) * s;
-  store8<DT, WIDE>(x + p.row * x_stride + c, left, v);
+  const f32x8 v = decode8<CODE>(load_codes<NT>(codes + p.row * width + c, left)) * s;
+  store8<DT, NT>(x + p.row * x_stride + c, left, v);
 }
 
 // 1 / (1 + e^-x): the hardware's exponential and reciprocal, each within an ulp or
@@ -102,7 +102,7 @@ __device__ __forceinline__ float activation(float x, float* slope) {
   return x * s;
 }
 
-template <int DT, bool WIDE, int ACT, int CODE>
+template <int DT, bool NT, int ACT, int CODE>
 __global__ __launch_bounds__(256) void glu_kernel(
     const elem_t<DT>* __restrict__ gate_up, int64_t gu_stride, elem_t<DT>* __restrict__ out,
     int64_t out_stride, uint8_t* __restrict__ codes, uint8_t* __restrict__ scales, int64_t rows,
@@ -112,15 +112,15 @@ __global__ __launch_bounds__(256) void glu_kernel(
   f32x8 g = {}, u = {};
   if (p.live) {
     const elem_t<DT>* src = gate_up + p.row * gu_stride + c;
-    g = load8<DT, WIDE>(src, left);
-    u = load8<DT, WIDE>(src + width, left);
+    g = load8<DT, NT>(src, left);
+    u = load8<DT, NT>(src + width, left);
     f32x8 o;
 #pragma unroll
     for (int i = 0; i < 8; i++) {
       float slope;
       o[i] = activation<ACT>(g[i], &slope) * u[i];
     }
-    store8<DT, WIDE>(out + p.row * out_stride + c, left, o);
+    store8<DT, NT>(out + p.row * out_stride + c, left, o);
   }
   if (CODE >= 0) {
     uint32_t gb, ub;
@@ -128,8 +128,8 @@ __global__ __launch_bounds__(256) void glu_kernel(
     const u32x2 uw = quantise8<CODE < 0 ? 0 : CODE>(u, group_lanes, &ub);
     if (!p.live) return;
     uint8_t* dst = codes + p.row * 2 * width + c;
-    store_codes<WIDE>(dst, left, gw);
-    store_codes<WIDE>(dst + width, left, uw);
+    store_codes<NT>(dst, left, gw);
+    store_codes<NT>(dst + width, left, uw);
     if (p.chunk % group_lanes == 0) {
       uint8_t* s = scales + p.row * 2 * groups + p.chunk / group_lanes;
       s[0] = (uint8_t)gb;
@@ -138,7 +138,7 @@ __global__ __launch_bounds__(256) void glu_kernel(
   }
 }
 
-template <int DT, bool WIDE, int ACT, int CODE>
+template <int DT, bool NT, int ACT, int CODE>
 __global__ __launch_bounds__(256) void glu_grad_kernel(
     const elem_t<DT>* __restrict__ dout, int64_t dout_stride, const uint8_t* __restrict__ codes,
     const uint8_t* __restrict__ scales, elem_t<DT>* __restrict__ dgu, int64_t dgu_stride,
@@ -149,9 +149,9 @@ __global__ __launch_bounds__(256) void glu_grad_kernel(
   const int64_t c = p.chunk * 8, left = width - c;
   const uint8_t* src = codes + p.row * 2 * width + c;
   const uint8_t* sc = scales + p.row * 2 * groups + p.chunk / group_lanes;
-  const f32x8 g = decode8<CODE>(load_codes<WIDE>(src, left)) * scale_value(sc[0]);
-  const f32x8 u = decode8<CODE>(load_codes<WIDE>(src + width, left)) * scale_value(sc[groups]);
-  const f32x8 d = load8<DT, WIDE>(dout + p.row * dout_stride + c, left);
+  const f32x8 g = decode8<CODE>(load_codes<NT>(src, left)) * scale_value(sc[0]);
+  const f32x8 u = decode8<CODE>(load_codes<NT>(src + width, left)) * scale_value(sc[groups]);
+  const f32x8 d = load8<DT, NT>(dout + p.row * dout_stride + c, left);
   f32x8 dg, du, o;
 #pragma unroll
   for (int i = 0; i < 8; i++) {
@@ -162,9 +162,9 @@ __global__ __launch_bounds__(256) void glu_grad_kernel(
     o[i] = a * u[i];
   }
   elem_t<DT>* dst = dgu + p.row * dgu_stride + c;
-  store8<DT, WIDE>(dst, left, dg);
-  store8<DT, WIDE>(dst + width, left, du);
-  if (out) store8<DT, WIDE>(out + p.row * out_stride + c, left, o);
+  store8<DT, NT>(dst, left, dg);
+  store8<DT, NT>(dst + width, left, du);
+  if (out) store8<DT, NT>(out + p.row * out_stride + c, left, o);
 }
 
 template <typename F>
@@ -205,11 +205,11 @@ extern "C" int zs_act8_pack(const void* x, int64_t x_stride, void* codes, void* 
   if (!x || !codes || !scales) return fail(who, "NULL buffer");
   if (!al(x, elem_bytes(dtype))) return fail(who, "a buffer is not aligned to its elements");
   const Spread s = spread(rows, width);
-  const bool w = wide(x, x_stride, dtype) && width % 8 == 0 && al(codes, 8);
+  const bool nt = streams(rows * width * (1 + elem_bytes(dtype)));
   with_dtype(dtype, [&](auto DT) {
-    with_bool(w, [&](auto W) {
+    with_bool(nt, [&](auto NT) {
       with_code(code, [&](auto CODE) {
-        pack_kernel<decltype(DT)::value, decltype(W)::value, decltype(CODE)::value>
+        pack_kernel<decltype(DT)::value, decltype(NT)::value, decltype(CODE)::value>
             <<<dim3((uint32_t)s.blocks), dim3(256), 0, (hipStream_t)stream>>>(
                 (const elem_t<decltype(DT)::value>*)x, x_stride, (uint8_t*)codes,
                 (uint8_t*)scales, rows, width, group / 8, (width + group - 1) / group,
@@ -231,11 +231,11 @@ extern "C" int zs_act8_unpack(const void* codes, const void* scales, void* x, in
   if (!x || !codes || !scales) return fail(who, "NULL buffer");
   if (!al(x, elem_bytes(dtype))) return fail(who, "a buffer is not aligned to its elements");
   const Spread s = spread(rows, width);
-  const bool w = wide(x, x_stride, dtype) && width % 8 == 0 && al(codes, 8);
+  const bool nt = streams(rows * width * (1 + elem_bytes(dtype)));
   with_dtype(dtype, [&](auto DT) {
-    with_bool(w, [&](auto W) {
+    with_bool(nt, [&](auto NT) {
       with_code(code, [&](auto CODE) {
-        unpack_kernel<decltype(DT)::value, decltype(W)::value, decltype(CODE)::value>
+        unpack_kernel<decltype(DT)::value, decltype(NT)::value, decltype(CODE)::value>
             <<<dim3((uint32_t)s.blocks), dim3(256), 0, (hipStream_t)stream>>>(
                 (const uint8_t*)codes, (const uint8_t*)scales,
                 (elem_t<decltype(DT)::value>*)x, x_stride, rows, width, group / 8,
@@ -264,15 +264,13 @@ extern "C" int zs_glu_forward(const void* gate_up, int64_t gate_up_stride, void*
   if (!al(gate_up, eb) || !al(out, eb)) return fail(who, "a buffer is not aligned to its elements");
   const Spread s = spread(rows, width);
   const int g = codes ? group : 128;
-  // gate and up start 16-byte aligned only where the width is a multiple of 16 bytes
-  const bool w = wide(gate_up, gate_up_stride, dtype) && wide(out, out_stride, dtype) &&
-                 width % 8 == 0 && (!codes || al(codes, 8));
+  const bool nt = streams(rows * width * (3 * eb + (codes ? 2 : 0)));
   with_dtype(dtype, [&](auto DT) {
-    with_bool(w, [&](auto W) {
+    with_bool(nt, [&](auto NT) {
       with_act(act, [&](auto ACT) {
         auto go = [&](auto CODE) {
           using E = elem_t<decltype(DT)::value>;
-          glu_kernel<decltype(DT)::value, decltype(W)::value, decltype(ACT)::value,
+          glu_kernel<decltype(DT)::value, decltype(NT)::value, decltype(ACT)::value,
                      decltype(CODE)::value>
               <<<dim3((uint32_t)s.blocks), dim3(256), 0, (hipStream_t)stream>>>(
                   (const E*)gate_up, gate_up_stride, (E*)out, out_stride, (uint8_t*)codes,
@@ -306,15 +304,13 @@ extern "C" int zs_glu_backward(const void* grad_out, int64_t grad_out_stride, co
   if (!al(grad_out, eb) || !al(grad_gate_up, eb) || !al(out, eb))
     return fail(who, "a buffer is not aligned to its elements");
   const Spread s = spread(rows, width);
-  const bool w = wide(grad_out, grad_out_stride, dtype) &&
-                 wide(grad_gate_up, grad_gate_up_stride, dtype) && width % 8 == 0 &&
-                 al(codes, 8) && (!out || wide(out, out_stride, dtype));
+  const bool nt = streams(rows * width * ((out ? 4 : 3) * eb + 2));
   with_dtype(dtype, [&](auto DT) {
-    with_bool(w, [&](auto W) {
+    with_bool(nt, [&](auto NT) {
       with_act(act, [&](auto ACT) {
         with_code(code, [&](auto CODE) {
           using E = elem_t<decltype(DT)::value>;
-          glu_grad_kernel<decltype(DT)::value, decltype(W)::value, decltype(ACT)::value,
+          glu_grad_kernel<decltype(DT)::value, decltype(NT)::value, decltype(ACT)::value,
                           decltype(CODE)::value>
               <<<dim3((uint32_t)s.blocks), dim3(256), 0, (hipStream_t)stream>>>(
                   (const E*)grad_out, grad_out_stride, (const uint8_t*)codes,

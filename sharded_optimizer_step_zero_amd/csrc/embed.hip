@@ -30,6 +30,7 @@ namespace {
 
 constexpr int kSortThreads = 1024;
 constexpr int kSortWaves = kSortThreads / 64;
+constexpr int kBatch = 16;       // ids that a lane holds
 constexpr int kMaxSlots = 512;   // ids of one bucket
 constexpr int kRun = 32;         // sorted tokens of one wave
 constexpr int kCols = 512;       // columns of one wave
@@ -40,7 +41,7 @@ __device__ __forceinline__ int64_t local_id(const void* ids, int64_t t, int64_t 
   return (int64_t)((const I*)ids)[t] - start;
 }
 
-template <int DT, bool WIDE, typename I>
+template <int DT, typename I>
 __global__ __launch_bounds__(256) void gather_kernel(
     const elem_t<DT>* __restrict__ table, int64_t table_stride, const void* __restrict__ ids,
     elem_t<DT>* __restrict__ out, int64_t out_stride, int64_t n, int64_t vocab, int64_t width,
@@ -54,8 +55,8 @@ __global__ __launch_bounds__(256) void gather_kernel(
   elem_t<DT>* dst = out + t * out_stride;
   for (int64_t c = (int64_t)(threadIdx.x & (lanes - 1)) * 8; c < width; c += lanes * 8) {
     f32x8 x = {};
-    if (in) x = load8<DT, WIDE>(src + c, width - c) * scale;
-    store8<DT, WIDE>(dst + c, width - c, x);
+    if (in) x = load8<DT>(src + c, width - c) * scale;
+    store8<DT>(dst + c, width - c, x);
   }
 }
 
@@ -73,16 +74,29 @@ __global__ __launch_bounds__(kSortThreads) void sort_kernel(
     ((int32_t*)cnt)[i] = 0;
   if (threadIdx.x == 0) lower = 0;
   __syncthreads();
-  // each wave has a stretch of the tokens, a multiple of 64
+  // each wave has a stretch of the tokens, a multiple of 64, and takes kBatch
+  // loads of it at a time; a stretch of one batch stays in registers
   const int64_t per = ((int64_t)n + kSortThreads - 1) / kSortThreads * 64;
   const int64_t begin = wave * per, end = begin + per < n ? begin + per : n;
+  int32_t held[kBatch];
+  auto load = [&](int64_t t0) {
+#pragma unroll
+    for (int i = 0; i < kBatch; i++) {
+      const int64_t t = t0 + i * 64 + lane;
+      const int64_t v = t < end ? local_id<I>(ids, t, start) : -1;
+      held[i] = v >= 0 && v < vocab ? (int32_t)v : -1;
+    }
+  };
   int32_t less = 0;
-  for (int64_t t = begin + lane; t < end; t += 64) {
-    const int64_t v = local_id<I>(ids, t, start);
-    if (v < 0 || v >= vocab) continue;
-    const uint32_t b = (uint32_t)v & (buckets - 1);
-    less += b < bucket;
-    if (b == bucket) atomicAdd(&cnt[wave][(uint32_t)v >> bucket_log2], 1);
+  for (int64_t t0 = begin; t0 < end; t0 += kBatch * 64) {
+    load(t0);
+#pragma unroll
+    for (int i = 0; i < kBatch; i++) {
+      const uint32_t b = (uint32_t)held[i] & (buckets - 1);
+      if (held[i] < 0) continue;
+      less += b < bucket;
+      if (b == bucket) atomicAdd(&cnt[wave][(uint32_t)held[i] >> bucket_log2], 1);
+    }
   }
   for (int d = 1; d < 64; d <<= 1) less += __shfl_xor(less, d, 64);
   if (lane == 0 && less) atomicAdd(&lower, less);
@@ -114,39 +128,40 @@ __global__ __launch_bounds__(kSortThreads) void sort_kernel(
   }
   if (bucket == buckets - 1 && threadIdx.x == kMaxSlots - 1) *n_valid = at + total;
   __syncthreads();
-  for (int64_t t0 = begin; t0 < end; t0 += 64) {
-    const int64_t t = t0 + lane;
-    int64_t v = -1;
-    if (t < end) v = local_id<I>(ids, t, start);
-    const bool mine = v >= 0 && v < vocab && ((uint32_t)v & (buckets - 1)) == bucket;
-    const int32_t slot = (int32_t)((uint32_t)v >> bucket_log2);
-    uint64_t todo = __ballot(mine);
-    while (todo) {  // one id of these 64 tokens at a time, its tokens in order
-      const int leader = __builtin_ctzll(todo);
-      const int32_t s = __builtin_amdgcn_readlane(slot, leader);
-      const bool same = mine && slot == s;
-      const uint64_t peers = __ballot(same);
-      if (same) {
-        const int32_t place =
-            cnt[wave][s] + (int32_t)__builtin_popcountll(peers & ((1ull << lane) - 1));
-        order[place] = (int32_t)t;
-        sorted[place] = (int32_t)v;
-        if (lane == leader) cnt[wave][s] += (int32_t)__builtin_popcountll(peers);
+  for (int64_t t0 = begin; t0 < end; t0 += kBatch * 64) {
+    if (per > kBatch * 64) load(t0);
+#pragma unroll
+    for (int i = 0; i < kBatch; i++) {
+      const bool mine = held[i] >= 0 && ((uint32_t)held[i] & (buckets - 1)) == bucket;
+      const int32_t slot = held[i] >> bucket_log2;
+      uint64_t todo = __ballot(mine);
+      while (todo) {  // one id of these 64 tokens at a time, its tokens in order
+        const int leader = __builtin_ctzll(todo);
+        const int32_t s = __builtin_amdgcn_readlane(slot, leader);
+        const bool same = mine && slot == s;
+        const uint64_t peers = __ballot(same);
+        if (same) {
+          const int32_t place =
+              cnt[wave][s] + (int32_t)__builtin_popcountll(peers & ((1ull << lane) - 1));
+          order[place] = (int32_t)(t0 + i * 64 + lane);
+          sorted[place] = held[i];
+          if (lane == leader) cnt[wave][s] += (int32_t)__builtin_popcountll(peers);
+        }
+        todo &= ~peers;
       }
-      todo &= ~peers;
     }
   }
 }
 
-template <int TT, bool TWIDE>
+template <int TT, bool NT>
 __device__ __forceinline__ void put_row(elem_t<TT>* p, int64_t n, f32x8 sum, float scale,
                                         bool add) {
   f32x8 x = sum * scale;
-  if (add) x += load8<TT, TWIDE>(p, n);
-  store8<TT, TWIDE>(p, n, x);
+  if (add) x += load8<TT>(p, n);
+  store8<TT, NT>(p, n, x);
 }
 
-template <int DT, int TT, bool WIDE, bool TWIDE>
+template <int DT, int TT, bool NT>
 __global__ __launch_bounds__(256) void reduce_kernel(
     const elem_t<DT>* __restrict__ grad, int64_t grad_stride, elem_t<TT>* __restrict__ table,
     int64_t table_stride, int64_t vocab, int64_t width, float scale, int accumulate,
@@ -164,7 +179,7 @@ __global__ __launch_bounds__(256) void reduce_kernel(
     const f32x8 zero = {};
     const int64_t v0 = (unit - run_items) * kZeroRows;
     for (int i = 0; i < kZeroRows && v0 + i < vocab; i++)
-      if (count[v0 + i] == 0) store8<TT, TWIDE>(table + (v0 + i) * table_stride + c, left, zero);
+      if (count[v0 + i] == 0) store8<TT, NT>(table + (v0 + i) * table_stride + c, left, zero);
     return;
   }
   const int64_t valid = *n_valid;
@@ -181,7 +196,7 @@ __global__ __launch_bounds__(256) void reduce_kernel(
     for (int j = 0; j < 4; j++) {
       const int k = i + j < n ? i + j : n - 1;
       const int64_t t = __builtin_amdgcn_readlane(my_t, k);
-      x[j] = left > 0 ? load8<DT, WIDE>(grad + t * grad_stride + c, left) : f32x8{};
+      x[j] = left > 0 ? load8<DT>(grad + t * grad_stride + c, left) : f32x8{};
     }
 #pragma unroll
     for (int j = 0; j < 4; j++) {
@@ -194,10 +209,10 @@ __global__ __launch_bounds__(256) void reduce_kernel(
       if (left > 0) {  // the id's last token, or the run's
         if (b >= p0 && next == e) {
           const int64_t v = __builtin_amdgcn_readlane(my_v, i + j);
-          put_row<TT, TWIDE>(table + v * table_stride + c, left, sum, scale, accumulate != 0);
+          put_row<TT, NT>(table + v * table_stride + c, left, sum, scale, accumulate != 0);
         } else {  // slot 0: the id came from the run before; slot 1: it begins here
           float* part = parts + (unit * 2 + (b >= p0)) * part_stride + c;
-          store8<ZS_F32, true>(part, 8, sum);
+          store8<ZS_F32>(part, 8, sum);
         }
       }
       sum = f32x8{};
@@ -205,7 +220,7 @@ __global__ __launch_bounds__(256) void reduce_kernel(
   }
 }
 
-template <int TT, bool TWIDE>
+template <int TT>
 __global__ __launch_bounds__(256) void join_kernel(
     elem_t<TT>* __restrict__ table, int64_t table_stride, int64_t width, float scale,
     int accumulate, const int32_t* __restrict__ sorted, const int32_t* __restrict__ first,
@@ -223,19 +238,19 @@ __global__ __launch_bounds__(256) void join_kernel(
   if (b < unit * kRun || e <= last + 1) return;  // the id begins earlier, or ends here
   const int64_t left = width - c;
   if (left <= 0) return;
-  f32x8 sum = load8<ZS_F32, true>(parts + (unit * 2 + 1) * part_stride + c, 8);
+  f32x8 sum = load8<ZS_F32>(parts + (unit * 2 + 1) * part_stride + c, 8);
   const int64_t end = (e - 1) / kRun;
   int64_t r = unit + 1;
   for (; r + 4 <= end + 1; r += 4) {
     f32x8 x[4];
 #pragma unroll
     for (int j = 0; j < 4; j++)
-      x[j] = load8<ZS_F32, true>(parts + (r + j) * 2 * part_stride + c, 8);
+      x[j] = load8<ZS_F32>(parts + (r + j) * 2 * part_stride + c, 8);
 #pragma unroll
     for (int j = 0; j < 4; j++) sum += x[j];
   }
-  for (; r <= end; r++) sum += load8<ZS_F32, true>(parts + r * 2 * part_stride + c, 8);
-  put_row<TT, TWIDE>(table + (int64_t)v * table_stride + c, left, sum, scale, accumulate != 0);
+  for (; r <= end; r++) sum += load8<ZS_F32>(parts + r * 2 * part_stride + c, 8);
+  put_row<TT, false>(table + (int64_t)v * table_stride + c, left, sum, scale, accumulate != 0);
 }
 
 struct Layout {
@@ -304,17 +319,14 @@ extern "C" int zs_embed_forward(const void* table, int64_t table_stride, const v
   while (log2 < 8 && (8ll << log2) < width) log2++;
   const int64_t blocks = (n_tokens + (256 >> log2) - 1) >> (8 - log2);
   if (blocks > kMaxBlocks) return fail(who, "too many tokens for one call");
-  const bool w = wide(table, table_stride, dtype) && wide(out, out_stride, dtype);
   with_dtype(dtype, [&](auto DT) {
-    with_bool(w, [&](auto W) {
-      with_bool(id_bytes == 8, [&](auto I8) {
-        using E = elem_t<decltype(DT)::value>;
-        using I = std::conditional_t<decltype(I8)::value, int64_t, int32_t>;
-        gather_kernel<decltype(DT)::value, decltype(W)::value, I>
-            <<<dim3((uint32_t)blocks), dim3(256), 0, (hipStream_t)stream>>>(
-                (const E*)table, table_stride, ids, (E*)out, out_stride, n_tokens, vocab, width,
-                vocab_start, scale, log2);
-      });
+    with_bool(id_bytes == 8, [&](auto I8) {
+      using E = elem_t<decltype(DT)::value>;
+      using I = std::conditional_t<decltype(I8)::value, int64_t, int32_t>;
+      gather_kernel<decltype(DT)::value, I>
+          <<<dim3((uint32_t)blocks), dim3(256), 0, (hipStream_t)stream>>>(
+              (const E*)table, table_stride, ids, (E*)out, out_stride, n_tokens, vocab, width,
+              vocab_start, scale, log2);
     });
   });
   return launched(who);
@@ -364,27 +376,21 @@ extern "C" int zs_embed_backward(const void* grad_out, int64_t grad_stride, cons
         n_valid);
   });
   if (int rc = launched(who)) return rc;
-  const bool w = wide(grad_out, grad_stride, dtype), tw = wide(grad_table, table_stride, table_dtype);
+  const bool nt = streams(vocab * width * elem_bytes(table_dtype));
   auto go = [&](auto DT, auto TT) {
-    with_bool(w, [&](auto W) {
-      with_bool(tw, [&](auto TW) {
-        using E = elem_t<decltype(DT)::value>;
-        using T = elem_t<decltype(TT)::value>;
-        reduce_kernel<decltype(DT)::value, decltype(TT)::value, decltype(W)::value,
-                      decltype(TW)::value><<<dim3((uint32_t)blocks), dim3(256), 0, s>>>(
-            (const E*)grad_out, grad_stride, (T*)grad_table, table_stride, vocab, width, scale,
-            accumulate, order, sorted, first, count, n_valid, parts, l.part_stride, l.runs,
-            l.slabs);
-      });
+    using E = elem_t<decltype(DT)::value>;
+    using T = elem_t<decltype(TT)::value>;
+    with_bool(nt, [&](auto NT) {
+      reduce_kernel<decltype(DT)::value, decltype(TT)::value, decltype(NT)::value>
+          <<<dim3((uint32_t)blocks), dim3(256), 0, s>>>(
+              (const E*)grad_out, grad_stride, (T*)grad_table, table_stride, vocab, width, scale,
+              accumulate, order, sorted, first, count, n_valid, parts, l.part_stride, l.runs,
+              l.slabs);
     });
     if (l.runs > 1)
-      with_bool(tw, [&](auto TW) {
-        using T = elem_t<decltype(TT)::value>;
-        join_kernel<decltype(TT)::value, decltype(TW)::value>
-            <<<dim3((uint32_t)join_blocks), dim3(256), 0, s>>>(
-                (T*)grad_table, table_stride, width, scale, accumulate, sorted, first, count,
-                n_valid, parts, l.part_stride, l.runs, l.slabs);
-      });
+      join_kernel<decltype(TT)::value><<<dim3((uint32_t)join_blocks), dim3(256), 0, s>>>(
+          (T*)grad_table, table_stride, width, scale, accumulate, sorted, first, count, n_valid,
+          parts, l.part_stride, l.runs, l.slabs);
   };
   if (table_dtype == dtype)
     with_dtype(dtype, [&](auto DT) { go(DT, DT); });

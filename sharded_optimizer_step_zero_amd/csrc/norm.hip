@@ -37,8 +37,9 @@ Shape shape(int64_t width) {
   }
   if (chunks <= 128) return {128, 1, 128};
   int nc = 1, lanes = 256;
-  while (nc < 8 && nc * lanes < chunks) nc *= 2;
-  while (nc * lanes < chunks) lanes *= 2;
+  while (nc < 4 && nc * lanes < chunks) nc *= 2;
+  while (lanes < 1024 && nc * lanes < chunks) lanes *= 2;
+  while (nc * lanes < chunks) nc *= 2;
   return {lanes, nc, lanes};
 }
 
@@ -55,8 +56,8 @@ __device__ __forceinline__ float row_sum(float x, int lanes, float* slots) {
   return s;
 }
 
-template <int DT, bool WIDE, int NC, int CODE>
-__global__ __launch_bounds__(1024) void norm_kernel(
+template <int DT, bool NT, int NC, int T, int CODE>
+__global__ __launch_bounds__(T) void norm_kernel(
     const elem_t<DT>* x, int64_t x_stride, const elem_t<DT>* residual, int64_t residual_stride,
     const elem_t<DT>* __restrict__ weight, elem_t<DT>* sum, int64_t sum_stride,
     elem_t<DT>* __restrict__ y, int64_t y_stride, uint8_t* __restrict__ codes,
@@ -73,12 +74,12 @@ __global__ __launch_bounds__(1024) void norm_kernel(
     const int64_t c = (int64_t)(k * lanes + in_row) * 8, left = live ? width - c : 0;
     s[k] = f32x8{};
     if (left > 0) {
-      s[k] = load8<DT, WIDE>(x + row * x_stride + c, left);
+      s[k] = load8<DT, NT>(x + row * x_stride + c, left);
       if (residual) {
-        s[k] += load8<DT, WIDE>(residual + row * residual_stride + c, left);
+        s[k] += load8<DT, NT>(residual + row * residual_stride + c, left);
         // the stored, rounded sum is what is normalised
         s[k] = __builtin_convertvector(__builtin_convertvector(s[k], typename Elem<DT>::vec), f32x8);
-        store8<DT, WIDE>(sum + row * sum_stride + c, left, s[k]);
+        store8<DT, NT>(sum + row * sum_stride + c, left, s[k]);
       }
     }
 #pragma unroll
@@ -93,22 +94,29 @@ __global__ __launch_bounds__(1024) void norm_kernel(
     const int64_t chunk = k * lanes + in_row, c = chunk * 8, left = live ? width - c : 0;
     f32x8 v = {};
     if (left > 0) {
-      v = s[k] * r * load8<DT, WIDE>(weight + c, left);
-      if (y) store8<DT, WIDE>(y + row * y_stride + c, left, v);
+      v = s[k] * r * load8<DT>(weight + c, left);
+      if (y) store8<DT, NT>(y + row * y_stride + c, left, v);
     }
     if (CODE >= 0) {
       uint32_t byte;
       const u32x2 w = quantise8<CODE < 0 ? 0 : CODE>(v, group_lanes, &byte);
       if (left > 0) {
-        store_codes<WIDE>(codes + row * width + c, left, w);
+        store_codes<NT>(codes + row * width + c, left, w);
         if (chunk % group_lanes == 0) scales[row * groups + chunk / group_lanes] = (uint8_t)byte;
       }
     }
   }
 }
 
-template <int DT, bool WIDE, int NC>
-__global__ __launch_bounds__(1024) void norm_grad_kernel(
+// The chunks of a row that the backward pass reads.
+template <int DT, int NC>
+struct GradRow {
+  Chunk<DT> s[NC], dy[NC], ds[NC];
+  float rstd;
+};
+
+template <int DT, bool NT, int NC, int T>
+__global__ __launch_bounds__(T) void norm_grad_kernel(
     const elem_t<DT>* dy, int64_t dy_stride, const elem_t<DT>* __restrict__ sum,
     int64_t sum_stride, const elem_t<DT>* __restrict__ weight, const float* __restrict__ rstd,
     const elem_t<DT>* ds, int64_t ds_stride, elem_t<DT>* dx, int64_t dx_stride,
@@ -123,48 +131,54 @@ __global__ __launch_bounds__(1024) void norm_grad_kernel(
 #pragma unroll
   for (int k = 0; k < NC; k++) {
     const int64_t c = (int64_t)(k * lanes + in_row) * 8;
-    w[k] = width > c ? load8<DT, WIDE>(weight + c, width - c) : f32x8{};
+    w[k] = load8<DT>(weight + c, width - c);
     dw[k] = f32x8{};
   }
-  int turn = 0;
-  for (int64_t row0 = (int64_t)blockIdx.x * rows_per_block; row0 < rows; row0 += step, turn ^= 1) {
-    const int64_t row = row0 + sub;
+  auto load = [&](int64_t row) {
+    GradRow<DT, NC> r;
     const bool live = row < rows;
-    const float r = live ? rstd[row] : 0.0f;
+    r.rstd = live ? rstd[row] : 0.0f;
+#pragma unroll
+    for (int k = 0; k < NC; k++) {
+      const int64_t c = (int64_t)(k * lanes + in_row) * 8, left = live ? width - c : 0;
+      r.s[k] = load_chunk<DT, NT>(sum + row * sum_stride + c, left);
+      r.dy[k] = load_chunk<DT, NT>(dy + row * dy_stride + c, left);
+      r.ds[k] = load_chunk<DT, NT>(ds + row * ds_stride + c, ds ? left : 0);
+    }
+    return r;
+  };
+  int turn = 0;
+  const int64_t first = (int64_t)blockIdx.x * rows_per_block;
+  GradRow<DT, NC> next = load(first + sub);
+  for (int64_t row0 = first; row0 < rows; row0 += step, turn ^= 1) {
+    const GradRow<DT, NC> now = next;
+    const int64_t row = row0 + sub;
+    // the next row is on its way while this one is worked on
+    if (row0 + step < rows) next = load(row + step);
     f32x8 h[NC], g[NC];
     float dot = 0.0f;
 #pragma unroll
     for (int k = 0; k < NC; k++) {
-      const int64_t c = (int64_t)(k * lanes + in_row) * 8, left = live ? width - c : 0;
-      h[k] = g[k] = f32x8{};
-      if (left > 0) {
-        h[k] = load8<DT, WIDE>(sum + row * sum_stride + c, left);
-        g[k] = load8<DT, WIDE>(dy + row * dy_stride + c, left);
+      h[k] = widen<DT>(now.s[k]) * now.rstd;
+      g[k] = widen<DT>(now.dy[k]);
+      dw[k] += g[k] * h[k];
+      g[k] *= w[k];
 #pragma unroll
-        for (int i = 0; i < 8; i++) {
-          h[k][i] *= r;
-          dw[k][i] += g[k][i] * h[k][i];
-          g[k][i] *= w[k][i];
-          dot += g[k][i] * h[k][i];
-        }
-      }
+      for (int i = 0; i < 8; i++) dot += g[k][i] * h[k][i];
     }
     const float mean = row_sum(dot, lanes, slots[turn]) * inv_width;
 #pragma unroll
     for (int k = 0; k < NC; k++) {
-      const int64_t c = (int64_t)(k * lanes + in_row) * 8, left = live ? width - c : 0;
-      if (left > 0) {
-        f32x8 v = (g[k] - h[k] * mean) * r;
-        if (ds) v += load8<DT, WIDE>(ds + row * ds_stride + c, left);
-        store8<DT, WIDE>(dx + row * dx_stride + c, left, v);
-      }
+      const int64_t c = (int64_t)(k * lanes + in_row) * 8, left = row < rows ? width - c : 0;
+      const f32x8 v = (g[k] - h[k] * mean) * now.rstd + widen<DT>(now.ds[k]);
+      store8<DT, NT>(dx + row * dx_stride + c, left, v);
     }
   }
-  float* part = parts + ((int64_t)blockIdx.x * rows_per_block + sub) * part_stride;
+  float* part = parts + (first + sub) * part_stride;
 #pragma unroll
   for (int k = 0; k < NC; k++) {
     const int64_t c = (int64_t)(k * lanes + in_row) * 8;
-    if (c < width) store8<ZS_F32, true>(part + c, 8, dw[k]);
+    if (c < width) store8<ZS_F32>(part + c, 8, dw[k]);
   }
 }
 
@@ -194,16 +208,22 @@ __global__ __launch_bounds__(1024) void columns_kernel(const float* __restrict__
   }
 }
 
+// Calls f with the chunks a thread and the largest workgroup as constants.
 template <typename F>
-void with_nc(int nc, F f) {
-  if (nc == 1)
-    f(std::integral_constant<int, 1>());
-  else if (nc == 2)
-    f(std::integral_constant<int, 2>());
-  else if (nc == 4)
-    f(std::integral_constant<int, 4>());
-  else
-    f(std::integral_constant<int, 8>());
+void with_shape(const Shape& s, F f) {
+  using std::integral_constant;
+  if (s.threads > 256) {
+    if (s.nc == 4)
+      f(integral_constant<int, 4>(), integral_constant<int, 1024>());
+    else
+      f(integral_constant<int, 8>(), integral_constant<int, 1024>());
+  } else if (s.nc == 1) {
+    f(integral_constant<int, 1>(), integral_constant<int, 256>());
+  } else if (s.nc == 2) {
+    f(integral_constant<int, 2>(), integral_constant<int, 256>());
+  } else {
+    f(integral_constant<int, 4>(), integral_constant<int, 256>());
+  }
 }
 
 // Workgroups of the backward pass, and parts of dw.
@@ -248,16 +268,15 @@ extern "C" int zs_norm_forward(const void* x, int64_t x_stride, const void* resi
   const int per = s.threads / s.lanes;
   const int64_t blocks = (rows + per - 1) / per;
   if (blocks > kMaxBlocks) return fail(who, "too many rows for one call");
-  const bool w = wide(x, x_stride, dtype) && al(weight, 16) &&
-                 (!residual || (wide(residual, residual_stride, dtype) && wide(sum, sum_stride, dtype))) &&
-                 (!y || wide(y, y_stride, dtype)) && (!codes || (width % 8 == 0 && al(codes, 8)));
+  const bool nt = streams(rows * width * ((residual ? 3 : 1) * eb + (y ? eb : 0) + (codes ? 1 : 0)));
   const int group_lanes = codes ? group / 8 : 16;
   with_dtype(dtype, [&](auto DT) {
-    with_bool(w, [&](auto W) {
-      with_nc(s.nc, [&](auto NC) {
+    with_bool(nt, [&](auto NT) {
+      with_shape(s, [&](auto NC, auto T) {
         auto go = [&](auto CODE) {
           using E = elem_t<decltype(DT)::value>;
-          norm_kernel<decltype(DT)::value, decltype(W)::value, decltype(NC)::value,
+          norm_kernel<decltype(DT)::value, decltype(NT)::value, decltype(NC)::value,
+                      decltype(T)::value,
                       decltype(CODE)::value>
               <<<dim3((uint32_t)blocks), dim3(s.threads), 0, (hipStream_t)stream>>>(
                   (const E*)x, x_stride, (const E*)residual, residual_stride, (const E*)weight,
@@ -309,15 +328,14 @@ extern "C" int zs_norm_backward(const void* dy, int64_t dy_stride, const void* s
   const int per = s.threads / s.lanes;
   const int64_t blocks = grad_blocks(rows, s);
   const int64_t stride = part_stride_of(width);
-  const bool w = wide(dy, dy_stride, dtype) && wide(sum, sum_stride, dtype) && al(weight, 16) &&
-                 wide(grad_x, grad_x_stride, dtype) &&
-                 (!grad_sum || wide(grad_sum, grad_sum_stride, dtype));
+  const bool nt = streams(rows * width * eb * (grad_sum ? 4 : 3));
   if (blocks)
     with_dtype(dtype, [&](auto DT) {
-      with_bool(w, [&](auto W) {
-        with_nc(s.nc, [&](auto NC) {
+      with_bool(nt, [&](auto NT) {
+        with_shape(s, [&](auto NC, auto T) {
           using E = elem_t<decltype(DT)::value>;
-          norm_grad_kernel<decltype(DT)::value, decltype(W)::value, decltype(NC)::value>
+          norm_grad_kernel<decltype(DT)::value, decltype(NT)::value, decltype(NC)::value,
+                      decltype(T)::value>
               <<<dim3((uint32_t)blocks), dim3(s.threads), 0, (hipStream_t)stream>>>(
                   (const E*)dy, dy_stride, (const E*)sum, sum_stride, (const E*)weight, rstd,
                   (const E*)grad_sum, grad_sum_stride, (E*)grad_x, grad_x_stride,

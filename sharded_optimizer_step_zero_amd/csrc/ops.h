@@ -43,37 +43,64 @@ struct Elem<ZS_F16> {
 template <int DT>
 using elem_t = typename Elem<DT>::type;
 
-// Eight elements of a row from p on, as fp32; n of them exist (the rest read as
-// 0).  WIDE: p is 16-byte aligned, so a whole chunk is one or two wide loads.
-template <int DT, bool WIDE>
-__device__ __forceinline__ f32x8 load8(const elem_t<DT>* p, int64_t n) {
-  using V = typename Elem<DT>::vec;
-  f32x8 r;
-  if (WIDE && n >= 8) {
-    if constexpr (DT == ZS_F32) {  // 16-byte aligned only
-      const f32x4 a = *(const f32x4*)p, b = *(const f32x4*)(p + 4);
-      return __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7);
-    } else {
-      return __builtin_convertvector(*(const V*)p, f32x8);
-    }
-  }
+// Wide accesses at any element's address: global memory is read and written
+// unaligned, so a row may start anywhere.
+typedef u32x4 u32x4_any __attribute__((aligned(2)));
+typedef u32x2 u32x2_any __attribute__((aligned(1)));
+
+// NT: the data passes once and does not fit the caches; it is kept out of them.
+template <bool NT>
+__device__ __forceinline__ u32x4 ld16(const void* p) {
+  if (NT) return __builtin_nontemporal_load((const u32x4_any*)p);
+  return *(const u32x4_any*)p;
+}
+template <bool NT>
+__device__ __forceinline__ void st16(void* p, u32x4 x) {
+  if (NT)
+    __builtin_nontemporal_store(x, (u32x4_any*)p);
+  else
+    *(u32x4_any*)p = x;
+}
+
+// Eight elements of a row as they lie in memory: a lane's chunk.
+template <int DT>
+struct Chunk {
+  static constexpr int kWords = DT == ZS_F32 ? 2 : 1;
+  u32x4 w[kWords];
+};
+// The chunk at p, n elements of which exist (the rest are 0).
+template <int DT, bool NT = false>
+__device__ __forceinline__ Chunk<DT> load_chunk(const elem_t<DT>* p, int64_t n) {
+  Chunk<DT> r;
+  if (n >= 8) {
 #pragma unroll
-  for (int i = 0; i < 8; i++) r[i] = i < n ? (float)p[i] : 0.0f;
+    for (int i = 0; i < Chunk<DT>::kWords; i++) r.w[i] = ld16<NT>((const u32x4_any*)p + i);
+    return r;
+  }
+  elem_t<DT> e[8];
+#pragma unroll
+  for (int i = 0; i < 8; i++) e[i] = i < n ? p[i] : (elem_t<DT>)0.0f;
+  __builtin_memcpy(&r, e, sizeof(r));
   return r;
+}
+template <int DT>
+__device__ __forceinline__ f32x8 widen(Chunk<DT> c) {
+  return __builtin_convertvector(__builtin_bit_cast(typename Elem<DT>::vec, c), f32x8);
+}
+// Eight elements as fp32.
+template <int DT, bool NT = false>
+__device__ __forceinline__ f32x8 load8(const elem_t<DT>* p, int64_t n) {
+  return widen<DT>(load_chunk<DT, NT>(p, n));
 }
 
 // Rounds to the element type (nearest, ties to even) and stores.
-template <int DT, bool WIDE>
+template <int DT, bool NT = false>
 __device__ __forceinline__ void store8(elem_t<DT>* p, int64_t n, f32x8 x) {
-  using V = typename Elem<DT>::vec;
-  const V v = __builtin_convertvector(x, V);
-  if (WIDE && n >= 8) {
-    if constexpr (DT == ZS_F32) {
-      *(f32x4*)p = __builtin_shufflevector(v, v, 0, 1, 2, 3);
-      *(f32x4*)(p + 4) = __builtin_shufflevector(v, v, 4, 5, 6, 7);
-    } else {
-      *(V*)p = v;
-    }
+  const typename Elem<DT>::vec v = __builtin_convertvector(x, typename Elem<DT>::vec);
+  if (n >= 8) {
+    const Chunk<DT> c = __builtin_bit_cast(Chunk<DT>, v);
+#pragma unroll
+    for (int i = 0; i < Chunk<DT>::kWords; i++) st16<NT>((u32x4_any*)p + i, c.w[i]);
     return;
   }
 #pragma unroll
@@ -140,20 +167,23 @@ __device__ __forceinline__ f32x8 decode8(u32x2 w) {
   return r;
 }
 
-// Eight codes at p, n of them exist.  WIDE: p is 8-byte aligned.
-template <bool WIDE>
+// Eight codes at p, n of them exist.
+template <bool NT = false>
 __device__ __forceinline__ u32x2 load_codes(const uint8_t* p, int64_t n) {
-  if (WIDE && n >= 8) return *(const u32x2*)p;
+  if (n >= 8) return NT ? __builtin_nontemporal_load((const u32x2_any*)p) : *(const u32x2_any*)p;
   u32x2 r = {0, 0};
 #pragma unroll
   for (int i = 0; i < 8; i++)
     if (i < n) r[i >> 2] |= (uint32_t)p[i] << (8 * (i & 3));
   return r;
 }
-template <bool WIDE>
+template <bool NT = false>
 __device__ __forceinline__ void store_codes(uint8_t* p, int64_t n, u32x2 w) {
-  if (WIDE && n >= 8) {
-    *(u32x2*)p = w;
+  if (n >= 8) {
+    if (NT)
+      __builtin_nontemporal_store(w, (u32x2_any*)p);
+    else
+      *(u32x2_any*)p = w;
     return;
   }
 #pragma unroll
@@ -208,6 +238,9 @@ inline bool al(const void* p, size_t n) { return ((uintptr_t)p % n) == 0; }
 inline bool wide(const void* p, int64_t stride, int32_t dtype) {
   return al(p, 16) && (stride * elem_bytes(dtype)) % 16 == 0;
 }
+// Whether a call's arrays together pass the last-level cache (256 MB), so that
+// what it writes is gone from there before it is read again.
+inline bool streams(int64_t bytes) { return bytes >= (256ll << 20); }
 inline int launched(const char* who) {
   const hipError_t e = hipGetLastError();
   return e == hipSuccess ? ZS_OK : ehip(who, e);

@@ -8,19 +8,32 @@
 //
 // Forward: one matrix product whose tiles end in the maximum and the sum of
 // exponentials of each token's part of the vocabulary (two floats a token and
-// 128 or 32 vocabulary entries); a second kernel joins them.  Backward: pieces of the
-// vocabulary; for each, the product again, its tiles ending in G (and G
-// transposed), and the two products that use it.  8 * tokens * vocab * width
-// operations in all, on the matrix cores: bound by their rate where there are
-// tokens enough, by reading W where there are few.
+// tile); a second kernel joins them.  Backward: pieces of the vocabulary; for each,
+// the product again, its tiles ending in G, and the two products that use it.
+// 8 * tokens * vocab * width operations in all, on the matrix cores: bound by
+// their rate where there are tokens enough, by reading W where there are few.
 //
-// All three products are one kernel, C[n][m] = sum_k A[m][k] B[n][k], both
-// operands with k adjacent, on 16x16x32 matrix instructions (16-bit in, fp32
-// sums).  Tiles of A and B go from global memory straight into LDS, 64 elements of
-// k at a time, two buffers deep; a 16-byte chunk of row r sits at chunk
-// position c ^ (r & 7), so that the 16 rows a matrix instruction's operand needs do
-// not meet on the same banks.  Rows past the edge and k past the width are read as
-// zeros by the buffer instructions' bounds check.
+// All three products are one kernel, C[n][m] = sum_k A[m][k] B[n][k], on 16x16x32
+// matrix instructions (16-bit in, fp32 sums).  An operand lies in memory with k
+// adjacent (H and W for the logits, G for dH) or with its rows adjacent (W for dH,
+// H and G for dW), so nothing is transposed on the way: the second kind goes
+// through the LDS reads that transpose.
+//
+// 256 x 256 tiles, four waves of 128 x 128 each: a wave reads 16 operand
+// fragments of LDS for 64 matrix instructions, which leaves the LDS less busy
+// than the matrix cores (eight waves of 128 x 64 would have both at their limit).
+// Tiles of 64 k, two in LDS, come from global memory straight into it.  A step
+// multiplies a tile's first 32 k while it reads the fragments of the second,
+// then the second while it reads the next tile's first, so no multiplication
+// waits for LDS; between the two halves is the step's one barrier, where the next
+// tile's loads, started a step before, have landed and this tile's buffer is free
+// for the loads of the one after.
+//
+// A row with k adjacent takes 128 bytes of LDS, a cache line of memory; its 16-byte
+// chunk c sits at c ^ (row & 7), so that 8 neighbouring rows' chunks lie on
+// different banks.  Where rows are adjacent, chunk c of k's line sits at c ^ 2 * ((k & 3) |
+// ((k >> 3) & 1) << 2): the lines that one transposing read meets differ.  Rows past
+// the edge and k past the end read as zeros by the buffer loads' bounds check.
 #include <algorithm>
 
 #include "ops.h"
@@ -30,21 +43,25 @@ namespace ops {
 namespace {
 
 typedef short s16x8 __attribute__((ext_vector_type(8)));
-typedef __attribute__((address_space(3))) void* lds_ptr;
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+#define ZS_LDS __attribute__((address_space(3)))
 
 constexpr int kRsrcWord3 = 0x00020000;  // raw 32-bit buffer, gfx9 family
-constexpr int BK = 64;            // k elements of one step: 128 bytes of a row
-constexpr int kRowBytes = BK * 2;
+constexpr int BK = 64;  // k elements of one step
 
+// what a tile ends in
 constexpr int kStats = 0;   // maximum, sum of exponentials and target logit
-constexpr int kGrad = 1;    // G and G transposed
+constexpr int kGrad = 1;    // G
 constexpr int kStore = 2;   // C, rounded
 constexpr int kAccum = 3;   // C in fp32, stored or added
+// how an operand lies
+constexpr int kByK = 0;     // [row][k]
+constexpr int kByRow = 1;   // [k][row]
 
 struct GemmArgs {
   const uint16_t *a, *b;
-  int64_t lda, ldb;      // row strides
-  int64_t m, n, k;       // rows of A and of B, and k (a multiple of 8)
+  int64_t lda, ldb;      // strides, multiples of 8; a line's last chunk is whole in memory
+  int64_t m, n, k;       // rows of A and of B, and k
   int32_t tiles_m, tiles_n;
   int64_t k_per_split;   // a multiple of BK; the split is blockIdx.y
   // kStats, kGrad
@@ -53,8 +70,8 @@ struct GemmArgs {
   int64_t vocab, v0;     // A's first row is vocabulary entry v0
   float *part_max, *part_sum, *target_logit;
   const float *lse, *gloss, *gmax;
-  uint16_t *g, *gt;      // G [n][ldg], G transposed [m][ldgt]
-  int64_t ldg, ldgt, n_pad;  // columns of gt up to n_pad are written
+  uint16_t* g;           // G [n][ldg], whole rows
+  int64_t ldg;
   // kStore, kAccum
   uint16_t* c;
   float* acc;
@@ -62,18 +79,35 @@ struct GemmArgs {
   int32_t add, c_wide;
 };
 
+// c += a b on the matrix cores, c held in the accumulation registers: left to
+// itself the compiler spreads 256 sums over both register files and moves them
+// to and fro.  It does not know how long the result takes, so settle() has to
+// come before anything else touches the sums: at the end of a loop's body, which
+// itself has matrix instructions only.
 template <int DT>
-__device__ __forceinline__ f32x4 mfma(s16x8 a, s16x8 b, f32x4 c) {
+__device__ __forceinline__ void mfma(f32x4& c, s16x8 a, s16x8 b) {
   if constexpr (DT == ZS_BF16)
-    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a),
-                                                   __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
+    asm volatile("v_mfma_f32_16x16x32_bf16 %0, %1, %2, %0" : "+a"(c) : "v"(a), "v"(b));
   else
-    return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, a),
-                                                  __builtin_bit_cast(f16x8, b), c, 0, 0, 0);
+    asm volatile("v_mfma_f32_16x16x32_f16 %0, %1, %2, %0" : "+a"(c) : "v"(a), "v"(b));
 }
+// The last matrix instruction's result is written (18 wait states after its issue).
+__device__ __forceinline__ void settle() { asm volatile("s_nop 15\n\ts_nop 3" ::: "memory"); }
 template <int DT>
 __device__ __forceinline__ uint16_t round16(float x) {
   return __builtin_bit_cast(uint16_t, (elem_t<DT>)x);
+}
+
+template <int DT>
+__device__ __forceinline__ u32x2 pack16(f32x4 x) {
+  typedef elem_t<DT> v4 __attribute__((ext_vector_type(4)));
+  return __builtin_bit_cast(u32x2, __builtin_convertvector(x, v4));
+}
+constexpr float kLog2E = 1.44269504f;
+// e^x / e^y with y times log2 e given; one fused step, so that the argument of the
+// power of two is rounded once.
+__device__ __forceinline__ float exp2_of(float x, float y) {
+  return __builtin_amdgcn_exp2f(__builtin_fmaf(x, kLog2E, -y));
 }
 
 __device__ __forceinline__ int64_t target_of(const GemmArgs& g, int64_t t) {
@@ -94,61 +128,121 @@ __device__ __forceinline__ void tile_of(const GemmArgs& g, int32_t* tm, int32_t*
   *tn = (int32_t)(band * 8 + in % wide);
 }
 
-template <int DT, int BM, int BN, int WM, int WN, int EPI>
+// One operand's way from memory through LDS into a wave's fragments: R rows a
+// tile, F fragments of 16 rows a wave, `threads` threads.
+template <int LAYOUT, int R, int F, int THREADS>
+struct Operand {
+  static constexpr int kBytes = R * BK * 2;
+  static constexpr int kLoads = kBytes / (THREADS * 16);  // of a thread, for a tile
+  static_assert(kBytes % (THREADS * 16) == 0, "whole loads");
+  static constexpr int kLine = LAYOUT == kByK ? BK * 2 : R * 2;  // bytes of a line in LDS
+  static constexpr int kChunks = kLine / 16;
+  static constexpr int kLinesPerLoad = THREADS / kChunks;
+  static_assert(LAYOUT == kByK || kLinesPerLoad % 4 == 0, "k & 3 does not depend on the load");
+
+  const uint8_t* base;   // the tile's first element at the split's first k
+  int64_t ld;            // bytes
+  int32_t rows, k_len;   // that exist
+  uint32_t off[kLoads];  // a thread's place in each load
+  int32_t chunk_k;       // kByK: the first k of the thread's chunk
+
+  __device__ __forceinline__ static int swizzle(int line) {
+    return LAYOUT == kByK ? line & 7 : ((line & 3) | ((line >> 3) & 1) << 2) * 2;
+  }
+  __device__ __forceinline__ Operand(const uint16_t* p, int64_t stride, int64_t row0,
+                                     int64_t n_rows, int64_t k0, int32_t k, int tid) {
+    ld = stride * 2;
+    base = (const uint8_t*)(LAYOUT == kByK ? p + row0 * stride + k0 : p + k0 * stride + row0);
+    rows = (int32_t)(n_rows - row0 < R ? n_rows - row0 : R);
+    k_len = k;
+    const int line = tid / kChunks, at = tid % kChunks;
+#pragma unroll
+    for (int i = 0; i < kLoads; i++) {
+      const int l = line + i * kLinesPerLoad;
+      off[i] = (uint32_t)(l * ld + (at ^ swizzle(l)) * 16);
+    }
+    // kLinesPerLoad is a multiple of 8 here: the chunk is the same in every load
+    chunk_k = (at ^ swizzle(line)) * 8;
+  }
+  // Buffer descriptor of step `step`'s tile: what lies past it reads as zeros.
+  __device__ __forceinline__ u32x4 descriptor(int step) const {
+    const int32_t left = k_len - step * BK;
+    const uint8_t* p = base + (LAYOUT == kByK ? (int64_t)step * BK * 2 : step * BK * ld);
+    const int32_t lines = left < BK ? left : BK;
+    // up to the end of the last line's last chunk, which the stride covers
+    const int64_t bytes = LAYOUT == kByK ? (rows - 1) * ld + ((left + 7) & ~7) * 2
+                                         : (int64_t)(lines - 1) * ld + ((rows + 7) & ~7) * 2;
+    const uint64_t q = (uint64_t)p;
+    const uint32_t end = left > 0 ? (uint32_t)bytes : 0u;
+    // the same in every lane, which the compiler does not always see
+    return u32x4{(uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)q),
+                 (uint32_t)__builtin_amdgcn_readfirstlane((int)(q >> 32)),
+                 (uint32_t)__builtin_amdgcn_readfirstlane((int)end), (uint32_t)kRsrcWord3};
+  }
+  // Before the loads of step `step`: k past the end would be the next row's, so in
+  // the last tile a thread whose chunk is past it reads out of bounds.
+  __device__ __forceinline__ void limit(int step) {
+    const int32_t left = k_len - step * BK;
+    if (LAYOUT == kByK && left < BK) {
+#pragma unroll
+      for (int i = 0; i < kLoads; i++) off[i] = chunk_k < left ? off[i] : 0xfffffff0u;
+    }
+  }
+  // Load i of the tile, into LDS at `lds` (the wave's part of the load).
+  __device__ __forceinline__ void load(u32x4 d, int i, uint32_t lds) const {
+    asm volatile(
+        "s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds" ::"s"(
+            lds + i * THREADS * 16),
+        "v"(off[i]), "s"(d)
+        : "memory");
+  }
+  // Fragment f of the tile's half `half`, for the wave whose first row is `row0`: 16
+  // rows and 32 k; a lane has 8 k of one row.
+  __device__ __forceinline__ static s16x8 fragment(const uint8_t* tile, int half, int f, int row0,
+                                                   int lane) {
+    if constexpr (LAYOUT == kByK) {
+      const int row = row0 + (lane & 15), chunk = (half * 4 + (lane >> 4)) ^ swizzle(row);
+      // 16 rows on, the swizzle is the same
+      return *(const s16x8*)(tile + row * kLine + chunk * 16 + f * 16 * kLine);
+    } else {
+      // 16 lanes read 4 lines of k, 16 rows each, and get a row's 4 k each
+      const int k = half * 32 + (lane >> 4) * 8 + ((lane & 15) >> 2);
+      const int row = row0 + f * 16 + (lane & 3) * 4;
+      const int chunk = (row >> 3) ^ swizzle(k);
+      const uint8_t* p = tile + k * kLine + chunk * 16 + (row & 4) * 2;
+      const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((ZS_LDS s16x4*)p);
+      const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((ZS_LDS s16x4*)(p + 4 * kLine));
+      return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
+    }
+  }
+};
+
+template <int DT, int LA, int LB, int BM, int BN, int WM, int WN, int kBuffers, int EPI>
 __device__ __forceinline__ void gemm(const GemmArgs& g) {
   constexpr int kThreads = WM * WN * 64;
-  constexpr int kPass = kThreads / 8;  // rows that one load of all threads covers
-  constexpr int PA = BM / kPass, PB = BN / kPass;
   constexpr int FM = BM / WM / 16, FN = BN / WN / 16;
-  constexpr int kTile = (BM + BN) * kRowBytes;
-  static_assert(BM % kPass == 0 && BN % kPass == 0, "whole passes");
-  constexpr int kOut = EPI == kGrad || EPI == kStore ? BM * BN * 2 : 0;
-  constexpr int kLds = 2 * kTile > kOut ? 2 * kTile : kOut;
-  __shared__ __attribute__((aligned(1024))) uint8_t lds[kLds];
+  using OpA = Operand<LA, BM, FM, kThreads>;
+  using OpB = Operand<LB, BN, FN, kThreads>;
+  constexpr int kTile = OpA::kBytes + OpB::kBytes;
+  constexpr int kLoads = OpA::kLoads + OpB::kLoads;
+  static_assert(kBuffers * kTile >= BM * BN * 2 && kBuffers * kTile >= WM * BN * 8,
+                "the epilogue's tile fits");
+  __shared__ __attribute__((aligned(1024))) uint8_t lds[kBuffers * kTile];
 
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wm = wave / WN, wn = wave % WN;
   int32_t tm, tn;
   tile_of(g, &tm, &tn);
   const int64_t m0 = (int64_t)tm * BM, n0 = (int64_t)tn * BN;
   const int64_t k_begin = blockIdx.y * g.k_per_split;
   const int64_t k_end = k_begin + g.k_per_split < g.k ? k_begin + g.k_per_split : g.k;
-  const int nk = k_end > k_begin ? (int)((k_end - k_begin + BK - 1) / BK) : 0;
+  const int32_t k_len = k_end > k_begin ? (int32_t)(k_end - k_begin) : 0;
+  const int steps = (k_len + BK - 1) / BK;
 
-  // the rows of this tile that exist, from the split's first k on; a lane's
-  // offsets beyond them read zeros
-  const int rows_a = (int)(g.m - m0 < BM ? g.m - m0 : BM);
-  const int rows_b = (int)(g.n - n0 < BN ? g.n - n0 : BN);
-  const int k_len = (int)(k_end - k_begin);
-  const auto ra = __builtin_amdgcn_make_buffer_rsrc(
-      (void*)(g.a + m0 * g.lda + k_begin), 0, (uint32_t)(((rows_a - 1) * g.lda + k_len) * 2),
-      kRsrcWord3);
-  const auto rb = __builtin_amdgcn_make_buffer_rsrc(
-      (void*)(g.b + n0 * g.ldb + k_begin), 0, (uint32_t)(((rows_b - 1) * g.ldb + k_len) * 2),
-      kRsrcWord3);
-  const int lr = tid >> 3;                      // row within a pass
-  const int lc = (tid & 7) ^ (lr & 7);          // the 16-byte chunk that belongs there
-  uint32_t off_a[PA], off_b[PB];
-#pragma unroll
-  for (int p = 0; p < PA; p++) off_a[p] = (uint32_t)(((lr + p * kPass) * g.lda + lc * 8) * 2);
-#pragma unroll
-  for (int p = 0; p < PB; p++) off_b[p] = (uint32_t)(((lr + p * kPass) * g.ldb + lc * 8) * 2);
-
-  auto load = [&](int step, int buf) {
-    // k past the end would be the next row's: such chunks go out of bounds
-    const bool in = step * BK + lc * 8 < k_len;
-    const uint32_t ko = (uint32_t)step * kRowBytes;
-    uint8_t* base = lds + buf * kTile + wave * 8 * kRowBytes;
-#pragma unroll
-    for (int p = 0; p < PA; p++)
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(ra, (lds_ptr)(base + p * kPass * kRowBytes), 16,
-                                               in ? off_a[p] + ko : 0xfffffff0u, 0, 0, 0);
-#pragma unroll
-    for (int p = 0; p < PB; p++)
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(
-          rb, (lds_ptr)(base + (BM + p * kPass) * kRowBytes), 16,
-          in ? off_b[p] + ko : 0xfffffff0u, 0, 0, 0);
-  };
+  OpA a(g.a, g.lda, m0, g.m, k_begin, k_len, tid);
+  OpB b(g.b, g.ldb, n0, g.n, k_begin, k_len, tid);
+  const uint32_t lds_at = (uint32_t)(uintptr_t)(ZS_LDS uint8_t*)lds + wave * 1024;
 
   f32x4 acc[FM][FN];
 #pragma unroll
@@ -156,71 +250,154 @@ __device__ __forceinline__ void gemm(const GemmArgs& g) {
 #pragma unroll
     for (int j = 0; j < FN; j++) acc[i][j] = f32x4{};
 
-  const int row_a = wm * (BM / WM) + (lane & 15), row_b = wn * (BN / WN) + (lane & 15);
-  auto compute = [&](int buf) {
-    const uint8_t* ta = lds + buf * kTile;
-    const uint8_t* tb = ta + BM * kRowBytes;
+  const int ra = wm * (BM / WM), rb = wn * (BN / WN);
+
+  // the loads of a step's tile, past the last step too (zeros), so that their
+  // number is always the same
+  auto load = [&](int buffer, int i, u32x4 da, u32x4 db) {
+    const uint32_t to = lds_at + buffer * kTile;
+    if (i < OpA::kLoads)
+      a.load(da, i, to);
+    else
+      b.load(db, i - OpA::kLoads, to + OpA::kBytes);
+  };
+  // Multiplies fragments fa, fb while half `half` of the tile at `tile` is read into
+  // ga, gb, and (loads) starts the loads of step `ahead` into `buffer`.  Reads, in the
+  // order in which the next half needs them, and loads are dealt out between
+  // pairs of matrix instructions, which take longer than issuing them; the last
+  // eighth has none, so that the last reads have arrived.
+  auto multiply = [&](s16x8 (&fa)[FM], s16x8 (&fb)[FN], s16x8 (&ga)[FM], s16x8 (&gb)[FN],
+                      const uint8_t* tile, int half, bool loads, int buffer, int ahead) {
+    u32x4 da = {}, db = {};
+    if (loads) {
+      a.limit(ahead);
+      b.limit(ahead);
+      da = a.descriptor(ahead);
+      db = b.descriptor(ahead);
+    }
+    constexpr int kPairs = FM * FN / 2, kSpan = kPairs * 7 / 8, kReads = FM + FN;
+    const int n_loads = loads ? kLoads : 0;
 #pragma unroll
-    for (int kk = 0; kk < BK / 32; kk++) {
-      const int ch = ((kk * 4 + (lane >> 4)) ^ (lane & 7)) * 16;  // row & 7 == lane & 7
-      s16x8 fa[FM], fb[FN];
+    for (int x = 0; x < kPairs; x++) {
 #pragma unroll
-      for (int i = 0; i < FM; i++)
-        fa[i] = *(const s16x8*)(ta + (row_a + i * 16) * kRowBytes + ch);
+      for (int e = (x * kReads + kSpan - 1) / kSpan;
+           e < ((x + 1) * kReads + kSpan - 1) / kSpan && e < kReads; e++) {
+        if (e == 0)
+          ga[0] = OpA::fragment(tile, half, 0, ra, lane);
+        else if (e <= FN)
+          gb[e - 1] = OpB::fragment(tile + OpA::kBytes, half, e - 1, rb, lane);
+        else
+          ga[e - FN] = OpA::fragment(tile, half, e - FN, ra, lane);
+      }
 #pragma unroll
-      for (int j = 0; j < FN; j++)
-        fb[j] = *(const s16x8*)(tb + (row_b + j * 16) * kRowBytes + ch);
+      for (int e = (x * n_loads + kSpan - 1) / kSpan;
+           e < ((x + 1) * n_loads + kSpan - 1) / kSpan && e < n_loads; e++)
+        load(buffer, e, da, db);
 #pragma unroll
-      for (int i = 0; i < FM; i++)
-#pragma unroll
-        for (int j = 0; j < FN; j++) acc[i][j] = mfma<DT>(fa[i], fb[j], acc[i][j]);
+      for (int y = 2 * x; y < 2 * x + 2; y++) {
+        // to and fro, so that a turn keeps both a row's and a column's operand
+        const int i = y / FN, j = i & 1 ? FN - 1 - y % FN : y % FN;
+        mfma<DT>(acc[i][j], fa[i], fb[j]);
+      }
+      __builtin_amdgcn_sched_barrier(0);
     }
   };
 
-  if (nk > 0) load(0, 0);
-  for (int step = 0; step < nk; step++) {
-    // this step's tile has arrived for every wave, and the other buffer is read out
-    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-    __syncthreads();
-    if (step + 1 < nk) load(step + 1, (step + 1) & 1);
-    compute(step & 1);
+  if (steps > 0) {
+#pragma unroll
+    for (int t = 0; t < kBuffers; t++) {
+      a.limit(t);
+      b.limit(t);
+      const u32x4 da = a.descriptor(t), db = b.descriptor(t);
+#pragma unroll
+      for (int l = 0; l < kLoads; l++) load(t, l, da, db);
+    }
+    asm volatile("s_waitcnt vmcnt(%0)\n\ts_barrier" ::"n"((kBuffers - 1) * kLoads) : "memory");
+    s16x8 fa[FM], fb[FN], ga[FM], gb[FN];
+#pragma unroll
+    for (int i = 0; i < FM; i++) fa[i] = OpA::fragment(lds, 0, i, ra, lane);
+#pragma unroll
+    for (int j = 0; j < FN; j++) fb[j] = OpB::fragment(lds + OpA::kBytes, 0, j, rb, lane);
+    int buffer = 0;
+    for (int s = 0; s < steps; s++) {
+      const int next = buffer + 1 < kBuffers ? buffer + 1 : 0;
+      multiply(fa, fb, ga, gb, lds + buffer * kTile, 1, false, 0, 0);
+      // tile s + 1 has landed for every wave, and every wave has read tile s
+      asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"((kBuffers - 2) * kLoads)
+                   : "memory");
+      multiply(ga, gb, fa, fb, lds + next * kTile, 0, true, buffer, s + kBuffers);
+      settle();
+      buffer = next;
+    }
   }
+  // no load is on its way into LDS any more, and no wave reads it
+  asm volatile("s_waitcnt vmcnt(0)\n\ts_barrier" ::: "memory");
 
   // acc[i][j][r] is C at row m0 + wm*(BM/WM) + i*16 + (lane>>4)*4 + r of A and row
   // n0 + wn*(BN/WN) + j*16 + (lane&15) of B
   const int em = wm * (BM / WM) + (lane >> 4) * 4, en = wn * (BN / WN) + (lane & 15);
 
+  // entries past the vocabulary (the last tile's) take no part
+  if (EPI == kStats && m0 + BM > g.vocab) {
+    const int32_t left = (int32_t)(g.vocab - m0) - em;
+#pragma unroll
+    for (int i = 0; i < FM; i++)
+#pragma unroll
+      for (int r = 0; r < 4; r++)
+        if (i * 16 + r >= left) {
+#pragma unroll
+          for (int j = 0; j < FN; j++) acc[i][j][r] = -__builtin_inff();
+        }
+  }
+  // A token's target as i * 16 + r, where this lane has it; -1 elsewhere.
+  auto mine = [&](int64_t target) {
+    const int64_t at = target - (g.v0 + m0 + em);
+    return target < g.vocab && at >= 0 && at < FM * 16 && !(at & 12) ? (int)at : -1;
+  };
+
   if constexpr (EPI == kStats) {
+    f32x2* stats = (f32x2*)lds;
 #pragma unroll
     for (int j = 0; j < FN; j++) {
       const int64_t t = n0 + en + j * 16;
-      const int64_t target = t < g.n ? target_of(g, t) : -1;
+      const int at = t < g.n ? mine(target_of(g, t)) : -1;
+      if (at >= 0) {
+#pragma unroll
+        for (int i = 0; i < FM; i++)
+#pragma unroll
+          for (int r = 0; r < 4; r++)
+            if (at == i * 16 + r) g.target_logit[t] = acc[i][j][r];
+      }
       float top = -__builtin_inff();
 #pragma unroll
       for (int i = 0; i < FM; i++)
 #pragma unroll
-        for (int r = 0; r < 4; r++) {
-          const int64_t v = m0 + em + i * 16 + r;
-          if (v < g.vocab) top = __builtin_fmaxf(top, acc[i][j][r]);
-          if (v == target && v < g.vocab) g.target_logit[t] = acc[i][j][r];
-        }
+        for (int r = 0; r < 4; r++) top = __builtin_fmaxf(top, acc[i][j][r]);
       top = __builtin_fmaxf(top, __shfl_xor(top, 16, 64));
       top = __builtin_fmaxf(top, __shfl_xor(top, 32, 64));
-      const float from = top == -__builtin_inff() ? 0.0f : top;
+      const float from = top == -__builtin_inff() ? 0.0f : top * kLog2E;
       float sum = 0.0f;
 #pragma unroll
       for (int i = 0; i < FM; i++)
 #pragma unroll
-        for (int r = 0; r < 4; r++) {
-          const int64_t v = m0 + em + i * 16 + r;
-          if (v < g.vocab) sum += __builtin_amdgcn_exp2f((acc[i][j][r] - from) * 1.44269504f);
-        }
+        for (int r = 0; r < 4; r++) sum += exp2_of(acc[i][j][r], from);
       sum += __shfl_xor(sum, 16, 64);
       sum += __shfl_xor(sum, 32, 64);
-      if (lane < 16 && t < g.n) {
-        const int64_t at = (int64_t)(tm * WM + wm) * g.n + t;
-        g.part_max[at] = top;
-        g.part_sum[at] = sum;
+      if (lane < 16) stats[wm * BN + en + j * 16] = f32x2{top, sum};
+    }
+    __syncthreads();
+    for (int i = tid; i < BN; i += kThreads) {  // the waves of one token, in order
+      float top = stats[i][0];
+#pragma unroll
+      for (int w = 1; w < WM; w++) top = __builtin_fmaxf(top, stats[w * BN + i][0]);
+      const float from = top == -__builtin_inff() ? 0.0f : top * kLog2E;
+      float sum = 0.0f;
+#pragma unroll
+      for (int w = 0; w < WM; w++)
+        sum += stats[w * BN + i][1] * exp2_of(stats[w * BN + i][0], from);
+      if (n0 + i < g.n) {
+        g.part_max[tm * g.n + n0 + i] = top;
+        g.part_sum[tm * g.n + n0 + i] = sum;
       }
     }
   } else if constexpr (EPI == kAccum) {
@@ -239,43 +416,51 @@ __device__ __forceinline__ void gemm(const GemmArgs& g) {
     }
   } else {
     // the tile in 16 bits in LDS, [n][m], chunks of a row swizzled by the row
-    __syncthreads();
-    float factor = 1.0f;
-    if (EPI == kStore) factor = *g.gmax;
+    const float factor = *g.gmax;
+    auto to = [&](int row, int m) {
+      return lds + row * (BM * 2) + ((m >> 3) ^ (row & (BM / 8 - 1))) * 16 + (m & 7) * 2;
+    };
 #pragma unroll
     for (int j = 0; j < FN; j++) {
-      const int64_t t = n0 + en + j * 16;
-      float lse = 0.0f, scale = 0.0f;
-      int64_t target = -1;
-      bool counts = false;
-      if (EPI == kGrad && t < g.n) {
-        target = target_of(g, t);
+      const int row = en + j * 16;
+      const int64_t t = n0 + row;
+      float from = 0.0f, scale = factor;
+      bool counts = true;
+      int at = -1;
+      if (EPI == kGrad) {
+        const int64_t target = t < g.n ? target_of(g, t) : -1;
         counts = target >= 0 && target < g.vocab;
-        lse = g.lse[t];
-        const float top = *g.gmax;
-        scale = top > 0.0f ? g.gloss[t] / top : g.gloss[t];
+        if (counts) {
+          from = g.lse[t] * kLog2E;
+          scale = g.gloss[t] / factor;
+          at = mine(target);
+        }
       }
 #pragma unroll
       for (int i = 0; i < FM; i++) {
-        uint16_t h[4];
+        f32x4 x;
 #pragma unroll
-        for (int r = 0; r < 4; r++) {
-          float x = acc[i][j][r];
-          if (EPI == kGrad) {
-            const int64_t v = g.v0 + m0 + em + i * 16 + r;
-            x = __builtin_amdgcn_exp2f((x - lse) * 1.44269504f);
-            x = scale * (v == target ? x - 1.0f : x);
-            if (!counts || v >= g.vocab) x = 0.0f;
-          } else {
-            x *= factor;
-          }
-          h[r] = round16<DT>(x);
-        }
-        const int row = en + j * 16, m = em + i * 16;
-        const int ch = (m >> 3) ^ (row & (BM / 8 - 1));
-        *(u32x2*)(lds + row * (BM * 2) + ch * 16 + (m & 4) * 2) =
-            u32x2{h[0] | (uint32_t)h[1] << 16, h[2] | (uint32_t)h[3] << 16};
+        for (int r = 0; r < 4; r++)
+          x[r] = (EPI == kGrad ? exp2_of(acc[i][j][r], from) : acc[i][j][r]) * scale;
+        u32x2 w = pack16<DT>(x);
+        if (EPI == kGrad && !counts) w = u32x2{0, 0};
+        *(u32x2*)to(row, em + i * 16) = w;
       }
+      if (EPI == kGrad && at >= 0) {  // this lane wrote that place
+#pragma unroll
+        for (int i = 0; i < FM; i++)
+#pragma unroll
+          for (int r = 0; r < 4; r++)
+            if (at == i * 16 + r)
+              *(uint16_t*)to(row, em + at) =
+                  round16<DT>((exp2_of(acc[i][j][r], from) - 1.0f) * scale);
+      }
+    }
+    if (EPI == kGrad && g.v0 + m0 + BM > g.vocab) {  // zeros past the vocabulary
+      __syncthreads();
+      const int first = (int)(g.vocab - g.v0 - m0);
+      for (int x = tid; x < BM * BN; x += kThreads)
+        if (x % BM >= first) *(uint16_t*)to(x / BM, x % BM) = 0;
     }
     __syncthreads();
     uint16_t* out = EPI == kGrad ? g.g : g.c;
@@ -297,60 +482,43 @@ __device__ __forceinline__ void gemm(const GemmArgs& g) {
           if (m + i < m_end) p[i] = (uint16_t)(w[i >> 1] >> (16 * (i & 1)));
       }
     }
-    if (EPI == kGrad && g.gt) {
-      for (int x = tid; x < BN / 8 * BM; x += kThreads) {
-        const int c = x % (BN / 8), m = x / (BN / 8);
-        if (m0 + m >= g.m || n0 + c * 8 >= g.n_pad) continue;
-        u32x4 w = {};
-#pragma unroll
-        for (int i = 0; i < 8; i++) {
-          const int row = c * 8 + i;
-          const uint16_t h = *(const uint16_t*)(lds + row * (BM * 2) +
-                                                ((m >> 3) ^ (row & (BM / 8 - 1))) * 16 + (m & 7) * 2);
-          w[i >> 1] |= (uint32_t)h << (16 * (i & 1));
-        }
-        *(u32x4*)(g.gt + (m0 + m) * g.ldgt + n0 + c * 8) = w;
-      }
-    }
   }
 }
 
-template <int DT, int BM, int BN, int WM, int WN, int EPI>
-__global__ __launch_bounds__(WM* WN * 64) void gemm_kernel(GemmArgs g) {
-  gemm<DT, BM, BN, WM, WN, EPI>(g);
+template <int DT, int LA, int LB, int BM, int BN, int WM, int WN, int kBuffers, int EPI>
+__global__ __launch_bounds__(WM* WN * 64, 1) void gemm_kernel(GemmArgs g) {
+  gemm<DT, LA, LB, BM, BN, WM, WN, kBuffers, EPI>(g);
 }
 
-// Joins a token's partial maxima and sums: 16 threads a token, each over every
-// 16th part, then over the threads in order.
-__global__ __launch_bounds__(256) void join_stats_kernel(
+// Joins a token's partial maxima and sums: 64 threads a token, each over every
+// 64th part in order, then over the threads in order.
+__global__ __launch_bounds__(1024) void join_stats_kernel(
     const float* __restrict__ part_max, const float* __restrict__ part_sum,
     const float* __restrict__ target_logit, const void* __restrict__ targets,
     int32_t target_bytes, int64_t tokens, int64_t vocab, int32_t parts, float* __restrict__ loss,
     float* __restrict__ lse) {
-  __shared__ float tops[16][16], sums[16][16];
+  __shared__ float tops[64][16], sums[64][16];
   const int tt = threadIdx.x & 15, s = threadIdx.x >> 4;
   const int64_t t = (int64_t)blockIdx.x * 16 + tt;
+  // a part of nothing but -infinity, and no part at all, has the sum 0
+  auto join = [](float& top, float& sum, float m, float x) {
+    const float next = __builtin_fmaxf(top, m);
+    const float from = next == -__builtin_inff() ? 0.0f : next;
+    sum = sum * __builtin_amdgcn_exp2f((top - from) * 1.44269504f) +
+          x * __builtin_amdgcn_exp2f((m - from) * 1.44269504f);
+    top = next;
+  };
   float top = -__builtin_inff(), sum = 0.0f;
-  bool nan = false;
   if (t < tokens) {
-    for (int p = s; p < parts; p += 16) top = __builtin_fmaxf(top, part_max[p * tokens + t]);
-    for (int p = s; p < parts; p += 16) {
-      const float m = part_max[p * tokens + t], x = part_sum[p * tokens + t];
-      nan |= x != x;
-      if (m != -__builtin_inff()) sum += x * __builtin_amdgcn_exp2f((m - top) * 1.44269504f);
-    }
+#pragma unroll 4
+    for (int p = s; p < parts; p += 64)
+      join(top, sum, part_max[p * tokens + t], part_sum[p * tokens + t]);
   }
-  if (nan) sum = __builtin_nanf("");
   tops[s][tt] = top;
   sums[s][tt] = sum;
   __syncthreads();
   if (s != 0 || t >= tokens) return;
-  top = -__builtin_inff();
-  for (int i = 0; i < 16; i++) top = __builtin_fmaxf(top, tops[i][tt]);
-  sum = 0.0f;
-  for (int i = 0; i < 16; i++)
-    if (tops[i][tt] != -__builtin_inff() || sums[i][tt] != sums[i][tt])
-      sum += sums[i][tt] * __builtin_amdgcn_exp2f((tops[i][tt] - top) * 1.44269504f);
+  for (int i = 1; i < 64; i++) join(top, sum, tops[i][tt], sums[i][tt]);
   const float l = sum == 0.0f ? -__builtin_inff() : __builtin_logf(sum) + top;
   const int64_t target =
       target_bytes == 8 ? ((const int64_t*)targets)[t] : ((const int32_t*)targets)[t];
@@ -358,61 +526,45 @@ __global__ __launch_bounds__(256) void join_stats_kernel(
   loss[t] = target >= 0 && target < vocab ? l - target_logit[t] : 0.0f;
 }
 
-// out[j][i] = in[i][j] for i < rows (0 for rows whose target does not count, and
-// up to rows_pad), j < cols: 64 x 64 tiles through LDS.
-__global__ __launch_bounds__(256) void transpose_kernel(const uint16_t* __restrict__ in,
-                                                        int64_t in_stride, int64_t rows,
-                                                        int64_t cols, uint16_t* __restrict__ out,
-                                                        int64_t out_stride, int64_t rows_pad,
-                                                        const void* __restrict__ targets,
-                                                        int32_t target_bytes, int64_t vocab) {
-  __shared__ uint16_t tile[64][66];
-  const int64_t r0 = (int64_t)blockIdx.x * 64, c0 = (int64_t)blockIdx.y * 64;
-  const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
-  for (int i = w; i < 64; i += 4) {
-    const int64_t r = r0 + i, c = c0 + lane;
-    bool in_range = r < rows && c < cols;
-    if (in_range && targets) {
-      const int64_t t = target_bytes == 8 ? ((const int64_t*)targets)[r] : ((const int32_t*)targets)[r];
-      in_range = t >= 0 && t < vocab;
-    }
-    tile[i][lane] = in_range ? in[r * in_stride + c] : (uint16_t)0;
-  }
-  __syncthreads();
-  for (int i = w; i < 64; i += 4) {
-    const int64_t c = c0 + i, r = r0 + lane;
-    if (c < cols && r < rows_pad) out[c * out_stride + r] = tile[lane][i];
-  }
-}
-
 // Rows copied to a stride that is a multiple of 8 elements, zeros past the width.
-__global__ __launch_bounds__(256) void copy_rows_kernel(const uint16_t* __restrict__ in,
-                                                        int64_t in_stride, int64_t rows,
-                                                        int64_t width, uint16_t* __restrict__ out,
-                                                        int64_t out_stride) {
-  for (int64_t r = blockIdx.x; r < rows; r += gridDim.x)
-    for (int64_t c = threadIdx.x; c < out_stride; c += 256)
-      out[r * out_stride + c] = c < width ? in[r * in_stride + c] : (uint16_t)0;
-}
-
-// The largest finite |grad_loss| of the tokens that count.
-__global__ __launch_bounds__(1024) void gmax_kernel(const float* __restrict__ gloss,
-                                                    const void* __restrict__ targets,
-                                                    int32_t target_bytes, int64_t tokens,
-                                                    int64_t vocab, float* __restrict__ out) {
-  __shared__ float slots[16];
-  float top = 0.0f;
-  for (int64_t t = threadIdx.x; t < tokens; t += 1024) {
-    const int64_t v = target_bytes == 8 ? ((const int64_t*)targets)[t] : ((const int32_t*)targets)[t];
-    const float x = __builtin_fabsf(gloss[t]);
-    if (v >= 0 && v < vocab && x < __builtin_inff()) top = __builtin_fmaxf(top, x);
+// With targets: zeros for the rows of tokens that do not count, whatever they hold,
+// and one more workgroup finds the largest finite |grad_loss| of those that do (1
+// where that is 0).
+__global__ __launch_bounds__(256) void copy_rows_kernel(
+    const uint16_t* __restrict__ in, int64_t in_stride, int64_t rows, int64_t width,
+    uint16_t* __restrict__ out, int64_t out_stride, const void* __restrict__ targets,
+    int32_t target_bytes, int64_t vocab, const float* __restrict__ gloss,
+    float* __restrict__ gmax) {
+  auto counts = [&](int64_t r) {
+    const int64_t t =
+        target_bytes == 8 ? ((const int64_t*)targets)[r] : ((const int32_t*)targets)[r];
+    return t >= 0 && t < vocab;
+  };
+  if (gmax && blockIdx.x == 0) {
+    __shared__ float slots[4];
+    float top = 0.0f;
+#pragma unroll 4
+    for (int64_t t = threadIdx.x; t < rows; t += 256) {
+      const float x = __builtin_fabsf(gloss[t]);
+      if (counts(t) && x < __builtin_inff()) top = __builtin_fmaxf(top, x);
+    }
+    for (int d = 1; d < 64; d <<= 1) top = __builtin_fmaxf(top, __shfl_xor(top, d, 64));
+    if ((threadIdx.x & 63) == 0) slots[threadIdx.x >> 6] = top;
+    __syncthreads();
+    if (threadIdx.x == 0) {
+      for (int i = 1; i < 4; i++) top = __builtin_fmaxf(top, slots[i]);
+      *gmax = top > 0.0f ? top : 1.0f;
+    }
+    return;
   }
-  for (int d = 1; d < 64; d <<= 1) top = __builtin_fmaxf(top, __shfl_xor(top, d, 64));
-  if ((threadIdx.x & 63) == 0) slots[threadIdx.x >> 6] = top;
-  __syncthreads();
-  if (threadIdx.x == 0) {
-    for (int i = 1; i < 16; i++) top = __builtin_fmaxf(top, slots[i]);
-    *out = top > 0.0f ? top : 1.0f;
+  const int64_t skip = gmax ? 1 : 0;
+  for (int64_t r = blockIdx.x - skip; r < rows; r += gridDim.x - skip) {
+    const bool kept = !targets || counts(r);
+    for (int64_t c = threadIdx.x * 8; c < out_stride; c += 256 * 8) {
+      const Chunk<ZS_BF16> x =
+          load_chunk<ZS_BF16>((const __bf16*)in + r * in_stride + c, kept ? width - c : 0);
+      *(u32x4*)(out + r * out_stride + c) = x.w[0];
+    }
   }
 }
 
@@ -437,8 +589,8 @@ __global__ __launch_bounds__(256) void finish_kernel(const float* __restrict__ a
 // ---------------------------------------------------------------- host side
 
 constexpr int64_t kMaxWidth = 65536, kMaxStride = 1 << 21, kMaxRows = 0x7fffffff - 512;
-// G and its transpose of one piece together: within the 256 MB of the last-level cache
-constexpr int64_t kPieceElems = 64ll << 20;
+// G of one piece: 256 MB
+constexpr int64_t kPieceElems = 128ll << 20;
 constexpr int64_t up(int64_t x, int64_t m) { return (x + m - 1) / m * m; }
 
 bool needs_copy(const void* p, int64_t stride, int64_t width) {
@@ -451,22 +603,22 @@ struct Plan {
   bool small;         // few tokens: tiles of 64 tokens
   int64_t bm, bn;     // tile of the products that end in tokens
   int64_t parts;      // partial statistics a token (forward)
-  int64_t tp;         // tokens padded for G transposed
   int64_t piece;      // vocabulary entries a piece (backward)
   int32_t splits;     // of k in the product for grad_hidden
-  size_t h, w, pmax, psum, tlogit, gmax, ht, wt, g, gt, acc, total;
+  size_t h, w, pmax, psum, tlogit, gmax, g, acc, total;
 };
 
 Plan plan(const void* hidden, int64_t h_stride, const void* weight, int64_t w_stride,
           int64_t tokens, int64_t vocab, int64_t width, bool backward) {
   Plan p{};
   p.wp = up(width, 8);
-  p.copy_h = needs_copy(hidden, h_stride, width);
+  // the backward pass reads a copy whose rows that do not count are zeros
+  p.copy_h = backward || needs_copy(hidden, h_stride, width);
   p.copy_w = needs_copy(weight, w_stride, width);
   p.small = tokens <= 128;
   p.bm = p.small ? 128 : 256;
   p.bn = p.small ? 64 : 256;
-  p.parts = up(vocab, p.bm) / p.bm * (p.small ? 4 : 2);
+  p.parts = up(vocab, p.bm) / p.bm;
   size_t at = 0;
   auto take = [&](int64_t bytes) {
     const size_t q = at;
@@ -480,19 +632,16 @@ Plan plan(const void* hidden, int64_t h_stride, const void* weight, int64_t w_st
     p.psum = take(p.parts * tokens * 4);
     p.tlogit = take(tokens * 4);
   } else {
-    p.tp = up(std::max<int64_t>(tokens, 1), 64);
-    const int64_t most = std::max<int64_t>(kPieceElems / p.tp / 256 * 256, 256);
+    const int64_t t = std::max<int64_t>(tokens, 1);
+    const int64_t most = std::max<int64_t>(kPieceElems / up(t, 64) / 256 * 256, 256);
     const int64_t pieces = (vocab + most - 1) / most;
     p.piece = up((vocab + pieces - 1) / pieces, 256);
     // few tokens leave few tiles of grad_hidden: the piece's entries are divided
     // until the tiles cover the card, each part at least 512 long
-    const int64_t tiles = up(width, p.bm) / p.bm * (up(std::max<int64_t>(tokens, 1), p.bn) / p.bn);
-    p.splits = (int32_t)std::max<int64_t>(1, std::min<int64_t>(512 / tiles, p.piece / 512));
+    const int64_t tiles = up(width, p.bm) / p.bm * (up(t, p.bn) / p.bn);
+    p.splits = (int32_t)std::max<int64_t>(1, std::min<int64_t>(256 / tiles, p.piece / 512));
     p.gmax = take(4);
-    p.ht = take(width * p.tp * 2);
-    p.wt = take(width * p.piece * 2);
     p.g = take(tokens * p.piece * 2);
-    p.gt = take(p.piece * p.tp * 2);
     p.acc = take(p.splits * tokens * p.wp * 4);
   }
   p.total = std::max<size_t>(at, 256);
@@ -516,15 +665,18 @@ int check(const char* who, const void* hidden, int64_t hidden_stride, const void
   return ZS_OK;
 }
 
-template <int EPI>
+template <int EPI, int LA, int LB>
 void launch(const GemmArgs& a, bool small, int dtype, int splits, hipStream_t s) {
   const dim3 grid((uint32_t)(a.tiles_m * a.tiles_n), (uint32_t)splits);
   auto go = [&](auto DT) {
     constexpr int D = decltype(DT)::value;
-    if (small)
-      gemm_kernel<D, 128, 64, 4, 1, EPI><<<grid, dim3(256), 0, s>>>(a);
-    else
-      gemm_kernel<D, 256, 256, 2, 4, EPI><<<grid, dim3(512), 0, s>>>(a);
+    if constexpr (EPI != kStore) {
+      if (small) {
+        gemm_kernel<D, LA, LB, 128, 64, 4, 1, 3, EPI><<<grid, dim3(256), 0, s>>>(a);
+        return;
+      }
+    }
+    gemm_kernel<D, LA, LB, 256, 256, 2, 2, 2, EPI><<<grid, dim3(256), 0, s>>>(a);
   };
   if (dtype == ZS_BF16)
     go(std::integral_constant<int, ZS_BF16>());
@@ -548,8 +700,9 @@ bool shape(GemmArgs* a, bool small, int64_t m, int64_t n, int64_t k, int splits)
 void copy_rows(const void* in, int64_t stride, int64_t rows, int64_t width, void* out,
                int64_t wp, hipStream_t s) {
   if (rows)
-    copy_rows_kernel<<<dim3((uint32_t)std::min<int64_t>(rows, 4096)), dim3(256), 0, s>>>(
-        (const uint16_t*)in, stride, rows, width, (uint16_t*)out, wp);
+    copy_rows_kernel<<<dim3((uint32_t)std::min<int64_t>(rows, 8192)), dim3(256), 0, s>>>(
+        (const uint16_t*)in, stride, rows, width, (uint16_t*)out, wp, nullptr, 8, 0, nullptr,
+        nullptr);
 }
 
 }  // namespace
@@ -608,9 +761,9 @@ extern "C" int zs_xent_forward(const void* hidden, int64_t hidden_stride, const 
   a.part_max = (float*)(ws + p.pmax);
   a.part_sum = (float*)(ws + p.psum);
   a.target_logit = (float*)(ws + p.tlogit);
-  launch<kStats>(a, p.small, dtype, 1, s);
+  launch<kStats, kByK, kByK>(a, p.small, dtype, 1, s);
   if (int rc = launched(who)) return rc;
-  join_stats_kernel<<<dim3((uint32_t)((tokens + 15) / 16)), dim3(256), 0, s>>>(
+  join_stats_kernel<<<dim3((uint32_t)((tokens + 15) / 16)), dim3(1024), 0, s>>>(
       a.part_max, a.part_sum, a.target_logit, targets, target_bytes, tokens, vocab,
       (int32_t)p.parts, loss, lse);
   return launched(who);
@@ -646,27 +799,19 @@ extern "C" int zs_xent_backward(const void* hidden, int64_t hidden_stride, const
   if (!grad_hidden && !grad_weight) return ZS_OK;
   hipStream_t s = (hipStream_t)stream;
   uint8_t* ws = (uint8_t*)workspace;
-  const uint16_t *h = (const uint16_t*)hidden, *w = (const uint16_t*)weight;
-  int64_t ldh = hidden_stride, ldw = weight_stride;
+  const uint16_t *h = (const uint16_t*)(ws + p.h), *w = (const uint16_t*)weight;
+  int64_t ldw = weight_stride;
   float* gmax = (float*)(ws + p.gmax);
-  uint16_t *ht = (uint16_t*)(ws + p.ht), *wt = (uint16_t*)(ws + p.wt), *g = (uint16_t*)(ws + p.g),
-           *gt = (uint16_t*)(ws + p.gt);
+  uint16_t* g = (uint16_t*)(ws + p.g);
   float* acc = (float*)(ws + p.acc);
   if (p.copy_w) {
     copy_rows(weight, weight_stride, vocab, width, ws + p.w, p.wp, s);
     w = (const uint16_t*)(ws + p.w);
     ldw = p.wp;
   }
-  if (p.copy_h) {
-    copy_rows(hidden, hidden_stride, tokens, width, ws + p.h, p.wp, s);
-    h = (const uint16_t*)(ws + p.h);
-    ldh = p.wp;
-  }
-  gmax_kernel<<<dim3(1), dim3(1024), 0, s>>>(grad_loss, targets, target_bytes, tokens, vocab, gmax);
-  const uint32_t wt_cols = (uint32_t)((width + 63) / 64);
-  if (grad_weight)
-    transpose_kernel<<<dim3((uint32_t)(p.tp / 64), wt_cols), dim3(256), 0, s>>>(
-        h, ldh, tokens, width, ht, p.tp, p.tp, targets, target_bytes, vocab);
+  copy_rows_kernel<<<dim3((uint32_t)std::min<int64_t>(tokens, 8192) + 1), dim3(256), 0, s>>>(
+      (const uint16_t*)hidden, hidden_stride, tokens, width, (uint16_t*)(ws + p.h), p.wp, targets,
+      target_bytes, vocab, grad_loss, gmax);
   if (int rc = launched(who)) return rc;
   for (int64_t v0 = 0; v0 < vocab; v0 += p.piece) {
     const int64_t rows = std::min(p.piece, vocab - v0), cols = up(rows, 8);
@@ -676,7 +821,7 @@ extern "C" int zs_xent_backward(const void* hidden, int64_t hidden_stride, const
       a.a = w + v0 * ldw;
       a.lda = ldw;
       a.b = h;
-      a.ldb = ldh;
+      a.ldb = p.wp;
       a.targets = targets;
       a.target_bytes = target_bytes;
       a.vocab = vocab;
@@ -686,38 +831,33 @@ extern "C" int zs_xent_backward(const void* hidden, int64_t hidden_stride, const
       a.gmax = gmax;
       a.g = g;
       a.ldg = cols;
-      a.gt = grad_weight ? gt : nullptr;
-      a.ldgt = p.tp;
-      a.n_pad = p.tp;
-      launch<kGrad>(a, p.small, dtype, 1, s);
+      launch<kGrad, kByK, kByK>(a, p.small, dtype, 1, s);
     }
     if (grad_weight) {
       GemmArgs a{};
-      shape(&a, false, width, rows, tokens ? p.tp : 0, 1);
-      a.a = ht;
-      a.lda = p.tp;
-      a.b = gt;
-      a.ldb = p.tp;
+      shape(&a, false, width, rows, tokens, 1);
+      a.a = h;
+      a.lda = p.wp;
+      a.b = g;
+      a.ldb = cols;
       a.gmax = gmax;
       a.c = (uint16_t*)grad_weight + v0 * grad_weight_stride;
       a.ldc = grad_weight_stride;
       a.c_wide = wide(grad_weight, grad_weight_stride, dtype);
-      launch<kStore>(a, false, dtype, 1, s);
+      launch<kStore, kByRow, kByRow>(a, false, dtype, 1, s);
     }
     if (grad_hidden && tokens) {
-      transpose_kernel<<<dim3((uint32_t)((cols + 63) / 64), wt_cols), dim3(256), 0, s>>>(
-          w + v0 * ldw, ldw, rows, width, wt, cols, cols, nullptr, 8, vocab);
       GemmArgs a{};
-      shape(&a, p.small, width, tokens, cols, p.splits);
-      a.a = wt;
-      a.lda = cols;
+      shape(&a, p.small, width, tokens, rows, p.splits);
+      a.a = w + v0 * ldw;
+      a.lda = ldw;
       a.b = g;
       a.ldb = cols;
       a.acc = acc;
       a.ldc = p.wp;
       a.acc_split = tokens * p.wp;
       a.add = v0 > 0;
-      launch<kAccum>(a, p.small, dtype, p.splits, s);
+      launch<kAccum, kByRow, kByK>(a, p.small, dtype, p.splits, s);
     }
     if (int rc = launched(who)) return rc;
   }
