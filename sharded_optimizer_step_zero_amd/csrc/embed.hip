@@ -32,9 +32,16 @@ constexpr int kSortThreads = 1024;
 constexpr int kSortWaves = kSortThreads / 64;
 constexpr int kBatch = 16;       // ids that a lane holds
 constexpr int kMaxSlots = 512;   // ids of one bucket
-constexpr int kRun = 32;         // sorted tokens of one wave
+constexpr int kMaxRun = 32;      // sorted tokens of one wave at most
+constexpr int kAhead = 8;        // of whose rows are on their way at a time
 constexpr int kCols = 512;       // columns of one wave
+constexpr int kJoin = 16;        // parts that are read together
 constexpr int kZeroRows = 8;     // rows without tokens that one wave looks at
+
+// A run's last id, where it begins in the run and goes on, and the run it ends in.
+struct Crossing {
+  int32_t id, last_run;  // id -1: none
+};
 
 template <typename I>
 __device__ __forceinline__ int64_t local_id(const void* ids, int64_t t, int64_t start) {
@@ -70,8 +77,10 @@ __global__ __launch_bounds__(kSortThreads) void sort_kernel(
   __shared__ int32_t lower;
   const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
   const uint32_t bucket = blockIdx.x, buckets = 1u << bucket_log2;
-  for (int i = threadIdx.x; i < kSortWaves * kMaxSlots; i += kSortThreads)
-    ((int32_t*)cnt)[i] = 0;
+  const int slots = (int)((vocab + buckets - 1) >> bucket_log2);
+  for (int i = threadIdx.x; i < slots; i += kSortThreads)
+#pragma unroll
+    for (int w = 0; w < kSortWaves; w++) cnt[w][i] = 0;
   if (threadIdx.x == 0) lower = 0;
   __syncthreads();
   // each wave has a stretch of the tokens, a multiple of 64, and takes kBatch
@@ -83,8 +92,9 @@ __global__ __launch_bounds__(kSortThreads) void sort_kernel(
 #pragma unroll
     for (int i = 0; i < kBatch; i++) {
       const int64_t t = t0 + i * 64 + lane;
-      const int64_t v = t < end ? local_id<I>(ids, t, start) : -1;
-      held[i] = v >= 0 && v < vocab ? (int32_t)v : -1;
+      // past the end the last id is read again, so that all loads go out at once
+      const int64_t v = local_id<I>(ids, t < end ? t : end - 1, start);
+      held[i] = t < end && v >= 0 && v < vocab ? (int32_t)v : -1;
     }
   };
   int32_t less = 0;
@@ -102,13 +112,16 @@ __global__ __launch_bounds__(kSortThreads) void sort_kernel(
   if (lane == 0 && less) atomicAdd(&lower, less);
   __syncthreads();
   // a thread per id: its tokens before each wave, and all ids' before it
-  int32_t total = 0;
-  if (threadIdx.x < kMaxSlots)
-    for (int w = 0; w < kSortWaves; w++) {
-      const int32_t c = cnt[w][threadIdx.x];
-      cnt[w][threadIdx.x] = total;
-      total += c;
-    }
+  const bool owner = (int)threadIdx.x < slots;
+  int32_t total = 0, before[kSortWaves];
+#pragma unroll
+  for (int w = 0; w < kSortWaves; w++) before[w] = owner ? cnt[w][threadIdx.x] : 0;
+#pragma unroll
+  for (int w = 0; w < kSortWaves; w++) {
+    const int32_t c = before[w];
+    before[w] = total;
+    total += c;
+  }
   int32_t upto = total;
   for (int d = 1; d < 64; d <<= 1) {
     const int32_t o = __shfl_up(upto, d, 64);
@@ -118,15 +131,16 @@ __global__ __launch_bounds__(kSortThreads) void sort_kernel(
   __syncthreads();
   int32_t at = lower + upto - total;
   for (int w = 0; w < wave; w++) at += scan[w];
-  if (threadIdx.x < kMaxSlots) {
-    for (int w = 0; w < kSortWaves; w++) cnt[w][threadIdx.x] += at;
+  if (owner) {
+#pragma unroll
+    for (int w = 0; w < kSortWaves; w++) cnt[w][threadIdx.x] = at + before[w];
     const int64_t v = ((int64_t)threadIdx.x << bucket_log2) + bucket;
     if (v < vocab) {
       first[v] = at;
       count[v] = total;
     }
   }
-  if (bucket == buckets - 1 && threadIdx.x == kMaxSlots - 1) *n_valid = at + total;
+  if (bucket == buckets - 1 && threadIdx.x == kSortThreads - 1) *n_valid = at + total;
   __syncthreads();
   for (int64_t t0 = begin; t0 < end; t0 += kBatch * 64) {
     if (per > kBatch * 64) load(t0);
@@ -168,7 +182,7 @@ __global__ __launch_bounds__(256) void reduce_kernel(
     const int32_t* __restrict__ order, const int32_t* __restrict__ sorted,
     const int32_t* __restrict__ first, const int32_t* __restrict__ count,
     const int32_t* __restrict__ n_valid, float* __restrict__ parts, int64_t part_stride,
-    int64_t run_items, int64_t slabs) {
+    Crossing* __restrict__ crossings, int64_t run_items, int64_t slabs, int run) {
   const int lane = threadIdx.x & 63;
   const int64_t item = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
   const int64_t unit = item / slabs;
@@ -178,30 +192,43 @@ __global__ __launch_bounds__(256) void reduce_kernel(
     if (left <= 0 || accumulate) return;
     const f32x8 zero = {};
     const int64_t v0 = (unit - run_items) * kZeroRows;
-    for (int i = 0; i < kZeroRows && v0 + i < vocab; i++)
-      if (count[v0 + i] == 0) store8<TT, NT>(table + (v0 + i) * table_stride + c, left, zero);
+    int32_t tokens[kZeroRows];
+#pragma unroll
+    for (int i = 0; i < kZeroRows; i++) tokens[i] = count[v0 + i < vocab ? v0 + i : vocab - 1];
+#pragma unroll
+    for (int i = 0; i < kZeroRows; i++)
+      if (v0 + i < vocab && tokens[i] == 0)
+        store8<TT, NT>(table + (v0 + i) * table_stride + c, left, zero);
     return;
   }
   const int64_t valid = *n_valid;
-  const int64_t p0 = unit * kRun;
-  const int n = (int)(valid - p0 < kRun ? valid - p0 : kRun);
-  if (n <= 0) return;
+  const int64_t p0 = unit * run;
+  const int n = (int)(valid - p0 < run ? valid - p0 : run);
+  if (n <= 0) {
+    if (c == 0) crossings[unit] = {-1, 0};
+    return;
+  }
   const int64_t mine = p0 + (lane < n ? lane : n - 1);
   const int32_t my_t = order[mine], my_v = sorted[mine];
   const int32_t my_first = first[my_v], my_count = count[my_v];
+  if (c - lane * 8 == 0 && lane == n - 1) {  // the last token's id: does it begin here and go on?
+    const int64_t end = (int64_t)my_first + my_count;
+    const bool goes_on = my_first >= p0 && end > p0 + n;
+    crossings[unit] = {goes_on ? my_v : -1, (int32_t)((end - 1) / run)};
+  }
   f32x8 sum = {};
-  for (int i = 0; i < n; i += 4) {
-    f32x8 x[4];
+  for (int i = 0; i < n; i += kAhead) {
+    Chunk<DT> x[kAhead];
 #pragma unroll
-    for (int j = 0; j < 4; j++) {
+    for (int j = 0; j < kAhead; j++) {
       const int k = i + j < n ? i + j : n - 1;
       const int64_t t = __builtin_amdgcn_readlane(my_t, k);
-      x[j] = left > 0 ? load8<DT>(grad + t * grad_stride + c, left) : f32x8{};
+      x[j] = load_chunk<DT>(grad + t * grad_stride + c, left);
     }
 #pragma unroll
-    for (int j = 0; j < 4; j++) {
+    for (int j = 0; j < kAhead; j++) {
       if (i + j >= n) break;
-      sum += x[j];
+      sum += widen<DT>(x[j]);
       const int64_t b = __builtin_amdgcn_readlane(my_first, i + j);
       const int64_t e = b + __builtin_amdgcn_readlane(my_count, i + j);
       const int64_t next = p0 + i + j + 1;
@@ -223,40 +250,35 @@ __global__ __launch_bounds__(256) void reduce_kernel(
 template <int TT>
 __global__ __launch_bounds__(256) void join_kernel(
     elem_t<TT>* __restrict__ table, int64_t table_stride, int64_t width, float scale,
-    int accumulate, const int32_t* __restrict__ sorted, const int32_t* __restrict__ first,
-    const int32_t* __restrict__ count, const int32_t* __restrict__ n_valid,
-    const float* __restrict__ parts, int64_t part_stride, int64_t run_items, int64_t slabs) {
+    int accumulate, const Crossing* __restrict__ crossings, const float* __restrict__ parts,
+    int64_t part_stride, int64_t run_items, int64_t slabs) {
   const int lane = threadIdx.x & 63;
   const int64_t item = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
   const int64_t unit = item / slabs;
   const int64_t c = (item - unit * slabs) * kCols + lane * 8;
   if (unit >= run_items) return;
-  const int64_t last = unit * kRun + kRun - 1;
-  if (last + 1 >= *n_valid) return;  // nothing follows this run
-  const int32_t v = sorted[last];
-  const int64_t b = first[v], e = b + count[v];
-  if (b < unit * kRun || e <= last + 1) return;  // the id begins earlier, or ends here
+  const Crossing crossing = crossings[unit];
   const int64_t left = width - c;
-  if (left <= 0) return;
+  if (crossing.id < 0 || left <= 0) return;
+  const int64_t end = crossing.last_run;
   f32x8 sum = load8<ZS_F32>(parts + (unit * 2 + 1) * part_stride + c, 8);
-  const int64_t end = (e - 1) / kRun;
   int64_t r = unit + 1;
-  for (; r + 4 <= end + 1; r += 4) {
-    f32x8 x[4];
+  for (; r <= end; r += kJoin) {  // so many parts on their way at a time
+    f32x8 x[kJoin];
 #pragma unroll
-    for (int j = 0; j < 4; j++)
-      x[j] = load8<ZS_F32>(parts + (r + j) * 2 * part_stride + c, 8);
+    for (int j = 0; j < kJoin; j++)
+      x[j] = load8<ZS_F32>(parts + (r + j) * 2 * part_stride + c, r + j <= end ? 8 : 0);
 #pragma unroll
-    for (int j = 0; j < 4; j++) sum += x[j];
+    for (int j = 0; j < kJoin; j++)
+      if (r + j <= end) sum += x[j];
   }
-  for (; r <= end; r++) sum += load8<ZS_F32>(parts + r * 2 * part_stride + c, 8);
-  put_row<TT, false>(table + (int64_t)v * table_stride + c, left, sum, scale, accumulate != 0);
+  put_row<TT, false>(table + (int64_t)crossing.id * table_stride + c, left, sum, scale, accumulate != 0);
 }
 
 struct Layout {
-  int bucket_log2;
+  int bucket_log2, run;
   int64_t runs, slabs, part_stride;
-  size_t order, sorted, first, count, n_valid, parts, total;
+  size_t order, sorted, first, count, n_valid, crossings, parts, total;
 };
 constexpr int64_t kMaxVocab = 1 << 24, kMaxTokens = 0x7fffffff;
 
@@ -264,8 +286,10 @@ Layout layout(int64_t n, int64_t vocab, int64_t width) {
   Layout l{};
   l.bucket_log2 = 8;
   while (((vocab + (1ll << l.bucket_log2) - 1) >> l.bucket_log2) > kMaxSlots) l.bucket_log2++;
-  l.runs = (n + kRun - 1) / kRun;
   l.slabs = (width + kCols - 1) / kCols;
+  // short runs where there are few: a wave's rows come one batch after another
+  l.run = n * l.slabs <= 8 * 8192 ? 8 : kMaxRun;
+  l.runs = (n + l.run - 1) / l.run;
   l.part_stride = (width + 7) / 8 * 8;
   size_t at = 0;
   auto take = [&](size_t bytes) {
@@ -278,6 +302,7 @@ Layout layout(int64_t n, int64_t vocab, int64_t width) {
   l.first = take((size_t)vocab * 4);
   l.count = take((size_t)vocab * 4);
   l.n_valid = take(4);
+  l.crossings = take((size_t)l.runs * sizeof(Crossing));
   l.parts = take((size_t)l.runs * 2 * l.part_stride * 4);
   l.total = at;
   return l;
@@ -368,6 +393,7 @@ extern "C" int zs_embed_backward(const void* grad_out, int64_t grad_stride, cons
           *first = (int32_t*)(ws + l.first), *count = (int32_t*)(ws + l.count),
           *n_valid = (int32_t*)(ws + l.n_valid);
   float* parts = (float*)(ws + l.parts);
+  Crossing* crossings = (Crossing*)(ws + l.crossings);
   hipStream_t s = (hipStream_t)stream;
   with_bool(id_bytes == 8, [&](auto I8) {
     using I = std::conditional_t<decltype(I8)::value, int64_t, int32_t>;
@@ -376,7 +402,7 @@ extern "C" int zs_embed_backward(const void* grad_out, int64_t grad_stride, cons
         n_valid);
   });
   if (int rc = launched(who)) return rc;
-  const bool nt = streams(vocab * width * elem_bytes(table_dtype));
+  const bool nt = streams((n_tokens * elem_bytes(dtype) + vocab * elem_bytes(table_dtype)) * width);
   auto go = [&](auto DT, auto TT) {
     using E = elem_t<decltype(DT)::value>;
     using T = elem_t<decltype(TT)::value>;
@@ -384,13 +410,13 @@ extern "C" int zs_embed_backward(const void* grad_out, int64_t grad_stride, cons
       reduce_kernel<decltype(DT)::value, decltype(TT)::value, decltype(NT)::value>
           <<<dim3((uint32_t)blocks), dim3(256), 0, s>>>(
               (const E*)grad_out, grad_stride, (T*)grad_table, table_stride, vocab, width, scale,
-              accumulate, order, sorted, first, count, n_valid, parts, l.part_stride, l.runs,
-              l.slabs);
+              accumulate, order, sorted, first, count, n_valid, parts, l.part_stride, crossings,
+              l.runs, l.slabs, l.run);
     });
     if (l.runs > 1)
       join_kernel<decltype(TT)::value><<<dim3((uint32_t)join_blocks), dim3(256), 0, s>>>(
-          (T*)grad_table, table_stride, width, scale, accumulate, sorted, first, count, n_valid,
-          parts, l.part_stride, l.runs, l.slabs);
+          (T*)grad_table, table_stride, width, scale, accumulate, crossings, parts, l.part_stride,
+          l.runs, l.slabs);
   };
   if (table_dtype == dtype)
     with_dtype(dtype, [&](auto DT) { go(DT, DT); });

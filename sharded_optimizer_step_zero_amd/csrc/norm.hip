@@ -24,7 +24,9 @@ constexpr int64_t kMaxBlocks = 0x7fffff;
 constexpr int kBackwardGroups = 512;  // parts of dw, for rows wider than 512
 
 // How a row is spread: `lanes` threads with nc chunks of 8 each; rows up to 512
-// wide share a workgroup of 256.
+// wide share a workgroup of 256.  Two chunks a thread before more threads: at
+// 16384 rows of 8192, 512 threads with 2 chunks take 165 us, 256 with 4 173 and 1024
+// with 1 200.
 struct Shape {
   int lanes, nc, threads;
 };
@@ -36,8 +38,7 @@ Shape shape(int64_t width) {
     return {lanes, 1, 256};
   }
   if (chunks <= 128) return {128, 1, 128};
-  int nc = 1, lanes = 256;
-  while (nc < 4 && nc * lanes < chunks) nc *= 2;
+  int nc = chunks <= 256 ? 1 : 2, lanes = 256;
   while (lanes < 1024 && nc * lanes < chunks) lanes *= 2;
   while (nc * lanes < chunks) nc *= 2;
   return {lanes, nc, lanes};
@@ -54,6 +55,25 @@ __device__ __forceinline__ float row_sum(float x, int lanes, float* slots) {
   float s = 0.0f;
   for (int i = 0; i < lanes / 64; i++) s += slots[i];
   return s;
+}
+
+// Squares by fused steps, four sums of two, then in pairs: an output in 8 bits falls
+// on the other side of a border where rstd is off, so its error is kept small.
+__device__ __forceinline__ float sum_of_squares(f32x8 x) {
+  float q[4];
+#pragma unroll
+  for (int i = 0; i < 4; i++) q[i] = __builtin_fmaf(x[i + 4], x[i + 4], x[i] * x[i]);
+  return (q[0] + q[1]) + (q[2] + q[3]);
+}
+// 1 / sqrt(v), rounded about once: the hardware's estimate and a correction; the
+// estimate alone where the correction has no meaning (0, infinity, NaN).
+__device__ __forceinline__ float inverse_root(float v) {
+  const bool tiny = v < 0x1p-100f;  // the estimate takes subnormal numbers for 0
+  if (tiny) v *= 0x1p64f;
+  float r = __builtin_amdgcn_rsqf(v);
+  const float e = __builtin_fmaf(-v * r, r, 1.0f);
+  if (__builtin_fabsf(e) < 1.0f) r = __builtin_fmaf(r * e, 0.5f, r);
+  return tiny ? r * 0x1p32f : r;
 }
 
 template <int DT, bool NT, int NC, int T, int CODE>
@@ -82,11 +102,10 @@ __global__ __launch_bounds__(T) void norm_kernel(
         store8<DT, NT>(sum + row * sum_stride + c, left, s[k]);
       }
     }
-#pragma unroll
-    for (int i = 0; i < 8; i++) sq += s[k][i] * s[k][i];
+    sq += sum_of_squares(s[k]);
   }
   const float total = row_sum(sq, lanes, slots);
-  const float r = 1.0f / __builtin_sqrtf(total / (float)width + eps);
+  const float r = inverse_root(total / (float)width + eps);
   if (live && in_row == 0) rstd[row] = r;
   const int64_t groups = (width + group_lanes * 8 - 1) / (group_lanes * 8);
 #pragma unroll
@@ -212,17 +231,19 @@ __global__ __launch_bounds__(1024) void columns_kernel(const float* __restrict__
 template <typename F>
 void with_shape(const Shape& s, F f) {
   using std::integral_constant;
-  if (s.threads > 256) {
-    if (s.nc == 4)
-      f(integral_constant<int, 4>(), integral_constant<int, 1024>());
+  if (s.threads <= 256) {
+    if (s.nc == 1)
+      f(integral_constant<int, 1>(), integral_constant<int, 256>());
     else
-      f(integral_constant<int, 8>(), integral_constant<int, 1024>());
-  } else if (s.nc == 1) {
-    f(integral_constant<int, 1>(), integral_constant<int, 256>());
+      f(integral_constant<int, 2>(), integral_constant<int, 256>());
+  } else if (s.threads == 512) {
+    f(integral_constant<int, 2>(), integral_constant<int, 512>());
   } else if (s.nc == 2) {
-    f(integral_constant<int, 2>(), integral_constant<int, 256>());
+    f(integral_constant<int, 2>(), integral_constant<int, 1024>());
+  } else if (s.nc == 4) {
+    f(integral_constant<int, 4>(), integral_constant<int, 1024>());
   } else {
-    f(integral_constant<int, 4>(), integral_constant<int, 256>());
+    f(integral_constant<int, 8>(), integral_constant<int, 1024>());
   }
 }
 

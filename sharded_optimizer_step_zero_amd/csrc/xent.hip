@@ -188,12 +188,19 @@ struct Operand {
       for (int i = 0; i < kLoads; i++) off[i] = chunk_k < left ? off[i] : 0xfffffff0u;
     }
   }
+  // The same for one load, where the tiles do not come in order.
+  __device__ __forceinline__ uint32_t limited(int step, int i) const {
+    return LAYOUT == kByK && chunk_k >= k_len - step * BK ? 0xfffffff0u : off[i];
+  }
   // Load i of the tile, into LDS at `lds` (the wave's part of the load).
   __device__ __forceinline__ void load(u32x4 d, int i, uint32_t lds) const {
+    load(d, off[i], i, lds);
+  }
+  __device__ __forceinline__ void load(u32x4 d, uint32_t from, int i, uint32_t lds) const {
     asm volatile(
         "s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds" ::"s"(
             lds + i * THREADS * 16),
-        "v"(off[i]), "s"(d)
+        "v"(from), "s"(d)
         : "memory");
   }
   // Fragment f of the tile's half `half`, for the wave whose first row is `row0`: 16
@@ -220,6 +227,7 @@ struct Operand {
 template <int DT, int LA, int LB, int BM, int BN, int WM, int WN, int kBuffers, int EPI>
 __device__ __forceinline__ void gemm(const GemmArgs& g) {
   constexpr int kThreads = WM * WN * 64;
+  constexpr bool kTurned = BN == 64;
   constexpr int FM = BM / WM / 16, FN = BN / WN / 16;
   using OpA = Operand<LA, BM, FM, kThreads>;
   using OpB = Operand<LB, BN, FN, kThreads>;
@@ -254,12 +262,27 @@ __device__ __forceinline__ void gemm(const GemmArgs& g) {
 
   // the loads of a step's tile, past the last step too (zeros), so that their
   // number is always the same
-  auto load = [&](int buffer, int i, u32x4 da, u32x4 db) {
+  auto load = [&](int buffer, int step, int i, u32x4 da, u32x4 db) {
     const uint32_t to = lds_at + buffer * kTile;
-    if (i < OpA::kLoads)
+    const bool of_a = i < OpA::kLoads;
+    if (!of_a) i -= OpA::kLoads;
+    if (kTurned && of_a)
+      a.load(da, a.limited(step, i), i, to);
+    else if (kTurned)
+      b.load(db, b.limited(step, i), i, to + OpA::kBytes);
+    else if (of_a)
       a.load(da, i, to);
     else
-      b.load(db, i - OpA::kLoads, to + OpA::kBytes);
+      b.load(db, i, to + OpA::kBytes);
+  };
+  // The tile of step s.  With few tokens the products are bound by memory, and rows at a
+  // multiple of 4 KB would have all workgroups read one column, which few of the
+  // memory's channels hold: there every workgroup begins at a step of its own.
+  const int turn = kTurned && steps > 0 ? (int)((uint32_t)(tm + blockIdx.y) * 5u % (uint32_t)steps) : 0;
+  auto turned = [&](int s) {
+    if (!kTurned || s >= steps) return s;
+    const int at = s + turn;
+    return at < steps ? at : at - steps;
   };
   // Multiplies fragments fa, fb while half `half` of the tile at `tile` is read into
   // ga, gb, and (loads) starts the loads of step `ahead` into `buffer`.  Reads, in the
@@ -270,8 +293,11 @@ __device__ __forceinline__ void gemm(const GemmArgs& g) {
                       const uint8_t* tile, int half, bool loads, int buffer, int ahead) {
     u32x4 da = {}, db = {};
     if (loads) {
-      a.limit(ahead);
-      b.limit(ahead);
+      ahead = turned(ahead);
+      if (!kTurned) {
+        a.limit(ahead);
+        b.limit(ahead);
+      }
       da = a.descriptor(ahead);
       db = b.descriptor(ahead);
     }
@@ -292,7 +318,7 @@ __device__ __forceinline__ void gemm(const GemmArgs& g) {
 #pragma unroll
       for (int e = (x * n_loads + kSpan - 1) / kSpan;
            e < ((x + 1) * n_loads + kSpan - 1) / kSpan && e < n_loads; e++)
-        load(buffer, e, da, db);
+        load(buffer, ahead, e, da, db);
 #pragma unroll
       for (int y = 2 * x; y < 2 * x + 2; y++) {
         // to and fro, so that a turn keeps both a row's and a column's operand
@@ -306,11 +332,14 @@ __device__ __forceinline__ void gemm(const GemmArgs& g) {
   if (steps > 0) {
 #pragma unroll
     for (int t = 0; t < kBuffers; t++) {
-      a.limit(t);
-      b.limit(t);
-      const u32x4 da = a.descriptor(t), db = b.descriptor(t);
+      const int from = turned(t);
+      if (!kTurned) {
+        a.limit(from);
+        b.limit(from);
+      }
+      const u32x4 da = a.descriptor(from), db = b.descriptor(from);
 #pragma unroll
-      for (int l = 0; l < kLoads; l++) load(t, l, da, db);
+      for (int l = 0; l < kLoads; l++) load(t, from, l, da, db);
     }
     asm volatile("s_waitcnt vmcnt(%0)\n\ts_barrier" ::"n"((kBuffers - 1) * kLoads) : "memory");
     s16x8 fa[FM], fb[FN], ga[FM], gb[FN];

@@ -185,8 +185,23 @@ def _group(group):
     return group
 
 
-def _stream(device):
-    return torch.cuda.current_stream(device).cuda_stream
+# The current stream's handle: the raw query, where torch has it, costs a
+# twentieth of making a Stream object, which a call on a few rows would notice.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+
+def _run(device, entry, *args):
+    """Calls a C entry point on torch's current stream of the device, with that
+    device current."""
+    index = device.index
+    if torch.cuda.current_device() == index:
+        rc = entry(*args, _raw_stream(index))
+    else:
+        with torch.cuda.device(index):
+            rc = entry(*args, _raw_stream(index))
+    if rc < 0:
+        _check(rc)
 
 
 def _workspace(given, nbytes, device):
@@ -212,11 +227,6 @@ def _ids(ids, device):
     return _ID_BYTES[ids.dtype]
 
 
-def _on(device):
-    """The device of the call made current, where it is not."""
-    return torch.cuda.device(device)
-
-
 # ---------------------------------------------------------------- embedding
 
 
@@ -235,9 +245,8 @@ def embed(table, ids, scale=1.0, vocab_start=0, out=None):
         out_stride = width
     else:
         out_stride = _matrix(out, "out", table.dtype, dev, n, width)
-    with _on(dev):
-        _check(_embed_forward(table.data_ptr(), stride, ids.data_ptr(), out.data_ptr(), out_stride,
-                              n, vocab, width, vocab_start, scale, dt, nb, _stream(dev)))
+    _run(dev, _embed_forward, table.data_ptr(), stride, ids.data_ptr(), out.data_ptr(), out_stride,
+         n, vocab, width, vocab_start, scale, dt, nb)
     return out
 
 
@@ -267,11 +276,9 @@ def embed_backward(grad_out, ids, vocab, scale=1.0, vocab_start=0, out=None, out
     if out.dtype not in (grad_out.dtype, torch.float32):
         raise ValueError(f"out: dtype {out.dtype}, expected {grad_out.dtype} or torch.float32")
     ws = _workspace(workspace, _embed_backward_bytes(n, vocab, width), dev)
-    with _on(dev):
-        _check(_embed_backward(grad_out.data_ptr(), stride, ids.data_ptr(), out.data_ptr(),
-                               out_stride, n, vocab, width, vocab_start, scale, dt,
-                               _DTYPES[out.dtype], nb, int(accumulate), ws.data_ptr(), ws.numel(),
-                               _stream(dev)))
+    _run(dev, _embed_backward, grad_out.data_ptr(), stride, ids.data_ptr(), out.data_ptr(),
+         out_stride, n, vocab, width, vocab_start, scale, dt, _DTYPES[out.dtype], nb,
+         int(accumulate), ws.data_ptr(), ws.numel())
     return out
 
 
@@ -312,14 +319,11 @@ def norm(x, weight, residual=None, eps=1e-6, code=None, group=128, want_y=True):
         codes = torch.empty(rows, width, dtype=ct, device=dev)
         scales = torch.empty(rows, -(-width // group), dtype=_SCALE, device=dev)
     if rows:
-        with _on(dev):
-            _check(_norm_forward(
-                x.data_ptr(), xs, residual.data_ptr() if residual is not None else None, rs,
-                weight.data_ptr(), s.data_ptr() if residual is not None else None, ss,
-                y.data_ptr() if want_y else None, width,
-                codes.data_ptr() if code is not None else None,
-                scales.data_ptr() if code is not None else None, rstd.data_ptr(), rows, width, eps,
-                dt, cd, group, _stream(dev)))
+        _run(dev, _norm_forward, x.data_ptr(), xs, residual.data_ptr() if residual is not None else
+             None, rs, weight.data_ptr(), s.data_ptr() if residual is not None else None, ss,
+             y.data_ptr() if want_y else None, width, codes.data_ptr() if code is not None else
+             None, scales.data_ptr() if code is not None else None, rstd.data_ptr(), rows, width,
+             eps, dt, cd, group)
     return NormOut(y, s, rstd, codes, scales)
 
 
@@ -353,12 +357,10 @@ def norm_backward(grad_y, sum, weight, rstd, grad_sum=None, out=None, weight_gra
         raise ValueError(f"weight_grad_dtype: {weight_grad_out.dtype}, expected {grad_y.dtype} or "
                          "torch.float32")
     ws = _workspace(workspace, _norm_backward_bytes(rows, width), dev)
-    with _on(dev):
-        _check(_norm_backward(grad_y.data_ptr(), gs, sum.data_ptr(), ss, weight.data_ptr(),
-                              rstd.data_ptr(), grad_sum.data_ptr() if ds else None, ds,
-                              out.data_ptr(), os_, weight_grad_out.data_ptr(), rows, width, dt,
-                              _DTYPES[weight_grad_out.dtype], ws.data_ptr(), ws.numel(),
-                              _stream(dev)))
+    _run(dev, _norm_backward, grad_y.data_ptr(), gs, sum.data_ptr(), ss, weight.data_ptr(),
+         rstd.data_ptr(), grad_sum.data_ptr() if ds else None, ds, out.data_ptr(), os_,
+         weight_grad_out.data_ptr(), rows, width, dt, _DTYPES[weight_grad_out.dtype], ws.data_ptr(),
+         ws.numel())
     return out, weight_grad_out
 
 
@@ -376,9 +378,8 @@ def pack8(x, code="e4m3", group=128):
     codes = torch.empty(rows, width, dtype=ct, device=dev)
     scales = torch.empty(rows, -(-width // group), dtype=_SCALE, device=dev)
     if rows:
-        with _on(dev):
-            _check(_act8_pack(x.data_ptr(), xs, codes.data_ptr(), scales.data_ptr(), rows, width,
-                              dt, cd, group, _stream(dev)))
+        _run(dev, _act8_pack, x.data_ptr(), xs, codes.data_ptr(), scales.data_ptr(), rows, width,
+             dt, cd, group)
     return codes, scales
 
 
@@ -416,9 +417,8 @@ def unpack8(codes, scales, dtype, group=128, out=None):
     else:
         stride = _matrix(out, "out", dtype, dev, rows, width)
     if rows:
-        with _on(dev):
-            _check(_act8_unpack(codes.data_ptr(), scales.data_ptr(), out.data_ptr(), stride, rows,
-                                width, dt, cd, group, _stream(dev)))
+        _run(dev, _act8_unpack, codes.data_ptr(), scales.data_ptr(), out.data_ptr(), stride, rows,
+             width, dt, cd, group)
     return out
 
 
@@ -443,11 +443,9 @@ def glu(gate_up, act="silu", code="e4m3", group=128):
         codes = torch.empty(rows, both, dtype=ct, device=dev)
         scales = torch.empty(rows, 2, -(-width // group), dtype=_SCALE, device=dev)
     if rows:
-        with _on(dev):
-            _check(_glu_forward(gate_up.data_ptr(), gs, out.data_ptr(), width,
-                                codes.data_ptr() if code is not None else None,
-                                scales.data_ptr() if code is not None else None, rows, width, dt,
-                                a, cd, group, _stream(dev)))
+        _run(dev, _glu_forward, gate_up.data_ptr(), gs, out.data_ptr(), width, codes.data_ptr() if
+             code is not None else None, scales.data_ptr() if code is not None else None, rows,
+             width, dt, a, cd, group)
     return out, codes, scales
 
 
@@ -471,10 +469,9 @@ def glu_backward(grad_out, codes, scales, act="silu", group=128, want_out=False,
         os_ = _matrix(out, "out", grad_out.dtype, dev, rows, 2 * width)
     again = torch.empty(rows, width, dtype=grad_out.dtype, device=dev) if want_out else None
     if rows:
-        with _on(dev):
-            _check(_glu_backward(grad_out.data_ptr(), gs, codes.data_ptr(), scales.data_ptr(),
-                                 out.data_ptr(), os_, again.data_ptr() if want_out else None,
-                                 width, rows, width, dt, a, cd, group, _stream(dev)))
+        _run(dev, _glu_backward, grad_out.data_ptr(), gs, codes.data_ptr(), scales.data_ptr(),
+             out.data_ptr(), os_, again.data_ptr() if want_out else None, width, rows, width, dt, a,
+             cd, group)
     return out, again
 
 
@@ -502,10 +499,8 @@ def linear_xent(hidden, weight, targets, workspace=None):
     h, w = hidden.data_ptr(), weight.data_ptr()
     ws = _workspace(workspace, _xent_workspace_bytes(h, hs, w, wstride, tokens, vocab, width, 0),
                     dev)
-    with _on(dev):
-        _check(_xent_forward(h, hs, w, wstride, targets.data_ptr(), loss.data_ptr(),
-                             lse.data_ptr(), tokens, vocab, width, dt, nb, ws.data_ptr(),
-                             ws.numel(), _stream(dev)))
+    _run(dev, _xent_forward, h, hs, w, wstride, targets.data_ptr(), loss.data_ptr(), lse.data_ptr(),
+         tokens, vocab, width, dt, nb, ws.data_ptr(), ws.numel())
     return loss, lse
 
 
@@ -536,9 +531,7 @@ def linear_xent_backward(hidden, weight, targets, lse, grad_loss, out=None, weig
     h, w = hidden.data_ptr(), weight.data_ptr()
     ws = _workspace(workspace, _xent_workspace_bytes(h, hs, w, wstride, tokens, vocab, width, 1),
                     dev)
-    with _on(dev):
-        _check(_xent_backward(h, hs, w, wstride, targets.data_ptr(), lse.data_ptr(),
-                              grad_loss.data_ptr(), gh.data_ptr() if want_hidden else None, ghs,
-                              gw.data_ptr() if want_weight else None, gws, tokens, vocab, width,
-                              dt, nb, ws.data_ptr(), ws.numel(), _stream(dev)))
+    _run(dev, _xent_backward, h, hs, w, wstride, targets.data_ptr(), lse.data_ptr(),
+         grad_loss.data_ptr(), gh.data_ptr() if want_hidden else None, ghs, gw.data_ptr() if
+         want_weight else None, gws, tokens, vocab, width, dt, nb, ws.data_ptr(), ws.numel())
     return gh, gw
