@@ -628,6 +628,7 @@ bool needs_copy(const void* p, int64_t stride, int64_t width) {
 
 struct Plan {
   int64_t wp;         // width in whole chunks of 8
+  int64_t cs;         // row stride of the copies: whole cache lines
   bool copy_h, copy_w;
   bool small;         // few tokens: tiles of 64 tokens
   int64_t bm, bn;     // tile of the products that end in tokens
@@ -641,6 +642,7 @@ Plan plan(const void* hidden, int64_t h_stride, const void* weight, int64_t w_st
           int64_t tokens, int64_t vocab, int64_t width, bool backward) {
   Plan p{};
   p.wp = up(width, 8);
+  p.cs = up(width, 64);
   // the backward pass reads a copy whose rows that do not count are zeros
   p.copy_h = backward || needs_copy(hidden, h_stride, width);
   p.copy_w = needs_copy(weight, w_stride, width);
@@ -654,8 +656,8 @@ Plan plan(const void* hidden, int64_t h_stride, const void* weight, int64_t w_st
     at += up256((size_t)bytes);
     return q;
   };
-  if (p.copy_h) p.h = take(tokens * p.wp * 2);
-  if (p.copy_w) p.w = take(vocab * p.wp * 2);
+  if (p.copy_h) p.h = take(tokens * p.cs * 2);
+  if (p.copy_w) p.w = take(vocab * p.cs * 2);
   if (!backward) {
     p.pmax = take(p.parts * tokens * 4);
     p.psum = take(p.parts * tokens * 4);
@@ -775,14 +777,14 @@ extern "C" int zs_xent_forward(const void* hidden, int64_t hidden_stride, const 
   a.b = (const uint16_t*)hidden;
   a.ldb = hidden_stride;
   if (p.copy_w) {
-    copy_rows(weight, weight_stride, vocab, width, ws + p.w, p.wp, s);
+    copy_rows(weight, weight_stride, vocab, width, ws + p.w, p.cs, s);
     a.a = (const uint16_t*)(ws + p.w);
-    a.lda = p.wp;
+    a.lda = p.cs;
   }
   if (p.copy_h) {
-    copy_rows(hidden, hidden_stride, tokens, width, ws + p.h, p.wp, s);
+    copy_rows(hidden, hidden_stride, tokens, width, ws + p.h, p.cs, s);
     a.b = (const uint16_t*)(ws + p.h);
-    a.ldb = p.wp;
+    a.ldb = p.cs;
   }
   a.targets = targets;
   a.target_bytes = target_bytes;
@@ -834,12 +836,12 @@ extern "C" int zs_xent_backward(const void* hidden, int64_t hidden_stride, const
   uint16_t* g = (uint16_t*)(ws + p.g);
   float* acc = (float*)(ws + p.acc);
   if (p.copy_w) {
-    copy_rows(weight, weight_stride, vocab, width, ws + p.w, p.wp, s);
+    copy_rows(weight, weight_stride, vocab, width, ws + p.w, p.cs, s);
     w = (const uint16_t*)(ws + p.w);
-    ldw = p.wp;
+    ldw = p.cs;
   }
   copy_rows_kernel<<<dim3((uint32_t)std::min<int64_t>(tokens, 8192) + 1), dim3(256), 0, s>>>(
-      (const uint16_t*)hidden, hidden_stride, tokens, width, (uint16_t*)(ws + p.h), p.wp, targets,
+      (const uint16_t*)hidden, hidden_stride, tokens, width, (uint16_t*)(ws + p.h), p.cs, targets,
       target_bytes, vocab, grad_loss, gmax);
   if (int rc = launched(who)) return rc;
   for (int64_t v0 = 0; v0 < vocab; v0 += p.piece) {
@@ -850,7 +852,7 @@ extern "C" int zs_xent_backward(const void* hidden, int64_t hidden_stride, const
       a.a = w + v0 * ldw;
       a.lda = ldw;
       a.b = h;
-      a.ldb = p.wp;
+      a.ldb = p.cs;
       a.targets = targets;
       a.target_bytes = target_bytes;
       a.vocab = vocab;
@@ -866,7 +868,7 @@ extern "C" int zs_xent_backward(const void* hidden, int64_t hidden_stride, const
       GemmArgs a{};
       shape(&a, false, width, rows, tokens, 1);
       a.a = h;
-      a.lda = p.wp;
+      a.lda = p.cs;
       a.b = g;
       a.ldb = cols;
       a.gmax = gmax;

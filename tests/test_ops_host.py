@@ -5,6 +5,7 @@ agree with differences of their own forward passes."""
 import ctypes
 import os
 import re
+import subprocess
 
 import pytest
 import torch
@@ -25,6 +26,13 @@ def test_library_exports_every_declared_operator():
     for n in names:
         assert hasattr(lib, n) and callable(getattr(ops, n)), n
     assert sorted(ops.EXPORTED) == names
+
+
+def test_header_is_plain_c(tmp_path):
+    src = tmp_path / "t.c"
+    src.write_text('#include "zeroshard_ops.h"\nint main(void) { return ZS_F32 + ZS_E4M3 + ZS_SILU; }\n')
+    subprocess.run(["gcc", "-std=c99", "-Wall", "-Wextra", "-Werror", "-pedantic", "-fsyntax-only",
+                    "-I", os.path.join(ROOT, "include"), str(src)], check=True)
 
 
 def refused(call, *args):
