@@ -21,19 +21,28 @@
 //
 // 256 x 256 tiles, four waves of 128 x 128 each: a wave reads 16 operand
 // fragments of LDS for 64 matrix instructions, which leaves the LDS less busy
-// than the matrix cores (eight waves of 128 x 64 would have both at their limit).
-// Tiles of 64 k, two in LDS, come from global memory straight into it.  A step
-// multiplies a tile's first 32 k while it reads the fragments of the second,
-// then the second while it reads the next tile's first, so no multiplication
-// waits for LDS; between the two halves is the step's one barrier, where the next
-// tile's loads, started a step before, have landed and this tile's buffer is free
-// for the loads of the one after.
+// than the matrix cores (eight waves of 128 x 64, with W, H and G transposed on the
+// way, took 8.3 ms where this takes 6.7).  Tiles of 64 k, two in LDS, come from
+// global memory straight into it.  A step multiplies a tile's first 32 k while it reads
+// the fragments of the second, then the second while it reads the next tile's
+// first, so no multiplication waits for LDS; between the two halves is the step's
+// one barrier, where the next tile's loads, started a step before, have landed and
+// this tile's buffer is free for the loads of the one after.  Few tokens, or few
+// tiles, take 128 x 64 tiles of four waves and three buffers instead.
 //
-// A row with k adjacent takes 128 bytes of LDS, a cache line of memory; its 16-byte
-// chunk c sits at c ^ (row & 7), so that 8 neighbouring rows' chunks lie on
-// different banks.  Where rows are adjacent, chunk c of k's line sits at c ^ 2 * ((k & 3) |
-// ((k >> 3) & 1) << 2): the lines that one transposing read meets differ.  Rows past
-// the edge and k past the end read as zeros by the buffer loads' bounds check.
+// A row with k adjacent takes 128 bytes of LDS, a cache line of memory (with 64 bytes a
+// row and four buffers: 7.06 against 6.85 ms); its 16-byte chunk c sits at c ^ (row
+// & 7), so that 8 neighbouring rows' chunks lie on different banks.  Where rows are
+// adjacent, chunk c of k's line sits at c ^ 2 * ((k & 3) | ((k >> 3) & 1) << 2): the
+// lines that one transposing read meets differ (no bank conflicts counted in the
+// loops).  Rows past the edge and k past the end read as zeros by the buffer loads'
+// bounds check.
+//
+// Measured, 8192 tokens x 4096 x 32000 bf16: loss 1.65 ms (1300 TFLOP/s), loss and
+// gradients 6.7 ms (1280 TFLOP/s of the 8 tokens vocab width operations done; the
+// library's bare product 1370 to 1430).  The clock gives way under the load: on
+// zeros the same loop runs at 1650.  32x32x16 instructions are faster on zeros (1745) and
+// slower on data (1190).  64 x 2048 x 50304: 46 us of reading W at 4.5 TB/s, and 6 joining.
 #include <algorithm>
 
 #include "ops.h"
@@ -147,7 +156,8 @@ struct Operand {
   int32_t chunk_k;       // kByK: the first k of the thread's chunk
 
   __device__ __forceinline__ static int swizzle(int line) {
-    return LAYOUT == kByK ? line & 7 : ((line & 3) | ((line >> 3) & 1) << 2) * 2;
+    if (LAYOUT == kByK) return line & 7;
+    return ((line & 3) | ((line >> 3) & 1) << 2) * 2 & (kChunks - 1);
   }
   __device__ __forceinline__ Operand(const uint16_t* p, int64_t stride, int64_t row0,
                                      int64_t n_rows, int64_t k0, int32_t k, int tid) {
@@ -626,12 +636,24 @@ bool needs_copy(const void* p, int64_t stride, int64_t width) {
   return !al(p, 16) || stride % 8 || width % 8;
 }
 
+constexpr int64_t kCus = 256;
+int64_t tiles(int64_t m, int64_t n, bool small) {
+  return small ? up(m, 128) / 128 * (up(n, 64) / 64) : up(m, 256) / 256 * (up(n, 256) / 256);
+}
+// Whether a product takes the small tiles: where few rows of B leave a large one
+// mostly empty, and where large ones leave much of the card idle.  Loss and gradients
+// at 512 tokens x 1024 x 8000 take 77 us so and 138 with large tiles only; where
+// large tiles nearly fill the card they are better (2048 x 2048 x 8000, 250 tiles: 269
+// against 358 us).
+bool few(int64_t m, int64_t n, int64_t splits) {
+  return n <= 128 || tiles(m, n, false) * splits <= 192;
+}
+
 struct Plan {
   int64_t wp;         // width in whole chunks of 8
   int64_t cs;         // row stride of the copies: whole cache lines
   bool copy_h, copy_w;
-  bool small;         // few tokens: tiles of 64 tokens
-  int64_t bm, bn;     // tile of the products that end in tokens
+  bool small, small_h, small_w;  // tiles of 128 x 64: for the logits, grad_hidden, grad_weight
   int64_t parts;      // partial statistics a token (forward)
   int64_t piece;      // vocabulary entries a piece (backward)
   int32_t splits;     // of k in the product for grad_hidden
@@ -646,10 +668,6 @@ Plan plan(const void* hidden, int64_t h_stride, const void* weight, int64_t w_st
   // the backward pass reads a copy whose rows that do not count are zeros
   p.copy_h = backward || needs_copy(hidden, h_stride, width);
   p.copy_w = needs_copy(weight, w_stride, width);
-  p.small = tokens <= 128;
-  p.bm = p.small ? 128 : 256;
-  p.bn = p.small ? 64 : 256;
-  p.parts = up(vocab, p.bm) / p.bm;
   size_t at = 0;
   auto take = [&](int64_t bytes) {
     const size_t q = at;
@@ -659,6 +677,8 @@ Plan plan(const void* hidden, int64_t h_stride, const void* weight, int64_t w_st
   if (p.copy_h) p.h = take(tokens * p.cs * 2);
   if (p.copy_w) p.w = take(vocab * p.cs * 2);
   if (!backward) {
+    p.small = few(vocab, tokens, 1);
+    p.parts = up(vocab, p.small ? 128 : 256) / (p.small ? 128 : 256);
     p.pmax = take(p.parts * tokens * 4);
     p.psum = take(p.parts * tokens * 4);
     p.tlogit = take(tokens * 4);
@@ -667,10 +687,15 @@ Plan plan(const void* hidden, int64_t h_stride, const void* weight, int64_t w_st
     const int64_t most = std::max<int64_t>(kPieceElems / up(t, 64) / 256 * 256, 256);
     const int64_t pieces = (vocab + most - 1) / most;
     p.piece = up((vocab + pieces - 1) / pieces, 256);
+    p.small = few(p.piece, tokens, 1);
+    p.small_w = few(width, p.piece, 1);
     // few tokens leave few tiles of grad_hidden: the piece's entries are divided
     // until the tiles cover the card, each part at least 512 long
-    const int64_t tiles = up(width, p.bm) / p.bm * (up(t, p.bn) / p.bn);
-    p.splits = (int32_t)std::max<int64_t>(1, std::min<int64_t>(256 / tiles, p.piece / 512));
+    auto splits = [&](bool small) {
+      return std::max<int64_t>(1, std::min(kCus / tiles(width, t, small), p.piece / 512));
+    };
+    p.small_h = few(width, tokens, splits(false));
+    p.splits = (int32_t)splits(p.small_h);
     p.gmax = take(4);
     p.g = take(tokens * p.piece * 2);
     p.acc = take(p.splits * tokens * p.wp * 4);
@@ -701,13 +726,10 @@ void launch(const GemmArgs& a, bool small, int dtype, int splits, hipStream_t s)
   const dim3 grid((uint32_t)(a.tiles_m * a.tiles_n), (uint32_t)splits);
   auto go = [&](auto DT) {
     constexpr int D = decltype(DT)::value;
-    if constexpr (EPI != kStore) {
-      if (small) {
-        gemm_kernel<D, LA, LB, 128, 64, 4, 1, 3, EPI><<<grid, dim3(256), 0, s>>>(a);
-        return;
-      }
-    }
-    gemm_kernel<D, LA, LB, 256, 256, 2, 2, 2, EPI><<<grid, dim3(256), 0, s>>>(a);
+    if (small)
+      gemm_kernel<D, LA, LB, 128, 64, 4, 1, 3, EPI><<<grid, dim3(256), 0, s>>>(a);
+    else
+      gemm_kernel<D, LA, LB, 256, 256, 2, 2, 2, EPI><<<grid, dim3(256), 0, s>>>(a);
   };
   if (dtype == ZS_BF16)
     go(std::integral_constant<int, ZS_BF16>());
@@ -823,8 +845,8 @@ extern "C" int zs_xent_backward(const void* hidden, int64_t hidden_stride, const
   GemmArgs lg{}, gw{}, gh{};
   const int64_t per_row = (p.wp / 4 + 255) / 256;
   if (!shape(&lg, p.small, p.piece, std::max<int64_t>(tokens, 1), p.wp, 1) ||
-      !shape(&gw, false, width, p.piece, std::max<int64_t>(tokens, 8), 1) ||
-      !shape(&gh, p.small, width, std::max<int64_t>(tokens, 1), p.piece, p.splits) ||
+      !shape(&gw, p.small_w, width, p.piece, std::max<int64_t>(tokens, 8), 1) ||
+      !shape(&gh, p.small_h, width, std::max<int64_t>(tokens, 1), p.piece, p.splits) ||
       per_row * tokens > 0xffffff)
     return fail(who, "too many rows for one call");
   if (!grad_hidden && !grad_weight) return ZS_OK;
@@ -866,7 +888,7 @@ extern "C" int zs_xent_backward(const void* hidden, int64_t hidden_stride, const
     }
     if (grad_weight) {
       GemmArgs a{};
-      shape(&a, false, width, rows, tokens, 1);
+      shape(&a, p.small_w, width, rows, tokens, 1);
       a.a = h;
       a.lda = p.cs;
       a.b = g;
@@ -875,11 +897,11 @@ extern "C" int zs_xent_backward(const void* hidden, int64_t hidden_stride, const
       a.c = (uint16_t*)grad_weight + v0 * grad_weight_stride;
       a.ldc = grad_weight_stride;
       a.c_wide = wide(grad_weight, grad_weight_stride, dtype);
-      launch<kStore, kByRow, kByRow>(a, false, dtype, 1, s);
+      launch<kStore, kByRow, kByRow>(a, p.small_w, dtype, 1, s);
     }
     if (grad_hidden && tokens) {
       GemmArgs a{};
-      shape(&a, p.small, width, tokens, rows, p.splits);
+      shape(&a, p.small_h, width, tokens, rows, p.splits);
       a.a = w + v0 * ldw;
       a.lda = ldw;
       a.b = g;
@@ -888,7 +910,7 @@ extern "C" int zs_xent_backward(const void* hidden, int64_t hidden_stride, const
       a.ldc = p.wp;
       a.acc_split = tokens * p.wp;
       a.add = v0 > 0;
-      launch<kAccum, kByRow, kByK>(a, p.small, dtype, p.splits, s);
+      launch<kAccum, kByRow, kByK>(a, p.small_h, dtype, p.splits, s);
     }
     if (int rc = launched(who)) return rc;
   }
