@@ -60,7 +60,7 @@ __global__ __launch_bounds__(256) void pack_kernel(const elem_t<DT>* __restrict_
   f32x8 v = {};
   if (p.live) v = load8<DT, NT>(x + p.row * x_stride + c, left);
   uint32_t byte;
-  const u32x2 w = quantise8<CODE>(v, group_lanes, &byte);
+  const u32x2 w = quantise8<CODE>(v, group_amax(v, group_lanes), &byte);
   if (!p.live) return;
   store_codes<NT>(codes + p.row * width + c, left, w);
   if (p.chunk % group_lanes == 0) scales[p.row * groups + p.chunk / group_lanes] = (uint8_t)byte;
@@ -126,8 +126,8 @@ __global__ __launch_bounds__(256) void glu_kernel(
   }
   if (CODE >= 0) {
     uint32_t gb, ub;
-    const u32x2 gw = quantise8<CODE < 0 ? 0 : CODE>(g, group_lanes, &gb);
-    const u32x2 uw = quantise8<CODE < 0 ? 0 : CODE>(u, group_lanes, &ub);
+    const u32x2 gw = quantise8<CODE < 0 ? 0 : CODE>(g, group_amax(g, group_lanes), &gb);
+    const u32x2 uw = quantise8<CODE < 0 ? 0 : CODE>(u, group_amax(u, group_lanes), &ub);
     if (!p.live) return;
     uint8_t* dst = codes + p.row * 2 * width + c;
     store_codes<NT>(dst, left, gw);

@@ -12,9 +12,14 @@
 // sum over rows of dy h: a workgroup takes every n-th row and keeps its part of dw
 // in registers; a second kernel adds the parts in a fixed order.
 // The next row's loads are under way while one is worked on.
-// Both are bound by HBM.  Sums, means and rstd are fp32.  Measured, bf16: forward at
-// 16384 x 8192 with residual and codes 157 us for 939 MB (6.0 TB/s), backward at 8192 x 4096
-// 46 + 5 us for 268 MB (5.4 TB/s; 97 us without the prefetch).
+//
+// Both are bound by HBM.  Where a group's largest lies next to the border at which the
+// scale steps, the last bit decides a factor of two; so the forward joins its
+// squares and takes the root in fp64, rounds rstd once, and looks at such groups
+// again in fp64.  (All products in two parts of fp32 took 172 us for 161.)  The
+// backward sums in fp32.  Measured, bf16: forward at 16384 x 8192 with residual and
+// codes 163 us for 939 MB (5.8 TB/s), backward at 8192 x 4096 46 + 5 us for 268 MB (5.4
+// TB/s; 97 us without the prefetch).
 #include "ops.h"
 
 namespace zs {
@@ -53,34 +58,27 @@ Shape shape(int64_t width) {
 
 // Sum over the row's threads: within a wave by shuffles, across waves through LDS
 // (each call its own slots, written before and read after one barrier).
-__device__ __forceinline__ float row_sum(float x, int lanes, float* slots) {
+template <typename F>
+__device__ __forceinline__ F row_sum(F x, int lanes, F* slots) {
   const int w = lanes < 64 ? lanes : 64;
   for (int d = 1; d < w; d <<= 1) x += __shfl_xor(x, d, 64);
   if (lanes <= 64) return x;
   if ((threadIdx.x & 63) == 0) slots[threadIdx.x >> 6] = x;
   __syncthreads();
-  float s = 0.0f;
+  F s = 0;
   for (int i = 0; i < lanes / 64; i++) s += slots[i];
   return s;
 }
 
-// Squares by fused steps, four sums of two, then in pairs: an output in 8 bits falls
-// on the other side of a border where rstd is off, so its error is kept small.
-__device__ __forceinline__ float sum_of_squares(f32x8 x) {
-  float q[4];
-#pragma unroll
-  for (int i = 0; i < 4; i++) q[i] = __builtin_fmaf(x[i + 4], x[i + 4], x[i] * x[i]);
-  return (q[0] + q[1]) + (q[2] + q[3]);
-}
-// 1 / sqrt(v), rounded about once: the hardware's estimate and a correction; the
-// estimate alone where the correction has no meaning (0, infinity, NaN).
-__device__ __forceinline__ float inverse_root(float v) {
-  const bool tiny = v < 0x1p-100f;  // the estimate takes subnormal numbers for 0
-  if (tiny) v *= 0x1p64f;
-  float r = __builtin_amdgcn_rsqf(v);
-  const float e = __builtin_fmaf(-v * r, r, 1.0f);
-  if (__builtin_fabsf(e) < 1.0f) r = __builtin_fmaf(r * e, 0.5f, r);
-  return tiny ? r * 0x1p32f : r;
+// 1 / sqrt(v) in fp64: the hardware's fp32 estimate, of v brought near 1, and a Newton
+// step; the estimate alone where the step has no meaning (0, infinity, NaN).
+__device__ __forceinline__ double inverse_root(double v) {
+  const bool tiny = v < 0x1p-100, huge = v > 0x1p100;
+  const float near = (float)(tiny ? v * 0x1p180 : huge ? v * 0x1p-180 : v);
+  double r = __builtin_amdgcn_rsqf(near);
+  if (!(r > 0.0 && r < __builtin_inf())) return r;
+  r *= tiny ? 0x1p90 : huge ? 0x1p-90 : 1.0;
+  return r * __builtin_fma(-0.5 * v * r, r, 1.5);
 }
 
 template <int DT, bool NT, int NC, int T, int CODE>
@@ -89,13 +87,13 @@ __global__ __launch_bounds__(T) void norm_kernel(
     const elem_t<DT>* __restrict__ weight, elem_t<DT>* sum, int64_t sum_stride,
     elem_t<DT>* __restrict__ y, int64_t y_stride, uint8_t* __restrict__ codes,
     uint8_t* __restrict__ scales, float* __restrict__ rstd, int64_t rows, int64_t width,
-    float eps, int lanes, int rows_per_block, int group_lanes) {
-  __shared__ float slots[16];
+    float eps, double inv_width, int lanes, int rows_per_block, int group_lanes) {
+  __shared__ double slots[16];
   const int in_row = threadIdx.x & (lanes - 1);
   const int64_t row = (int64_t)blockIdx.x * rows_per_block + (rows_per_block > 1 ? threadIdx.x / lanes : 0);
   const bool live = row < rows;  // no early return: the shuffles and barriers are the workgroup's
   f32x8 s[NC];
-  float sq = 0.0f;
+  double sq = 0.0;
 #pragma unroll
   for (int k = 0; k < NC; k++) {
     const int64_t c = (int64_t)(k * lanes + in_row) * 8, left = live ? width - c : 0;
@@ -109,10 +107,16 @@ __global__ __launch_bounds__(T) void norm_kernel(
         store8<DT, NT>(sum + row * sum_stride + c, left, s[k]);
       }
     }
-    sq += sum_of_squares(s[k]);
+    float q[4];
+#pragma unroll
+    for (int i = 0; i < 4; i++)
+      q[i] = __builtin_fmaf(s[k][i + 4], s[k][i + 4], s[k][i] * s[k][i]);
+    // eight squares' error in fp32 is one of many that cancel; their sum's is not
+    sq += (double)((q[0] + q[1]) + (q[2] + q[3]));
   }
-  const float total = row_sum(sq, lanes, slots);
-  const float r = inverse_root(total / (float)width + eps);
+  const double total = row_sum(sq, lanes, slots);
+  const double root = inverse_root(__builtin_fma(total, inv_width, (double)eps));
+  const float r = (float)root;
   if (live && in_row == 0) rstd[row] = r;
   const int64_t groups = (width + group_lanes * 8 - 1) / (group_lanes * 8);
 #pragma unroll
@@ -124,8 +128,19 @@ __global__ __launch_bounds__(T) void norm_kernel(
       if (y) store8<DT, NT>(y + row * y_stride + c, left, v);
     }
     if (CODE >= 0) {
+      float amax = group_amax(v, group_lanes);
+      if ((__float_as_uint(amax) & 0x7fffffu) - 0x5ffffeu <= 4u) {
+        // within two units of 1.75 times a power of two, where the scale steps: the
+        // group again with its products in fp64 (all of its lanes come here)
+        if (left > 0) {
+          const f32x8 wt = load8<DT>(weight + c, left);
+#pragma unroll
+          for (int i = 0; i < 8; i++) v[i] = (float)((double)s[k][i] * root * (double)wt[i]);
+        }
+        amax = group_amax(v, group_lanes);
+      }
       uint32_t byte;
-      const u32x2 w = quantise8<CODE < 0 ? 0 : CODE>(v, group_lanes, &byte);
+      const u32x2 w = quantise8<CODE < 0 ? 0 : CODE>(v, amax, &byte);
       if (left > 0) {
         store_codes<NT>(codes + row * width + c, left, w);
         if (chunk % group_lanes == 0) scales[row * groups + chunk / group_lanes] = (uint8_t)byte;
@@ -318,7 +333,7 @@ extern "C" int zs_norm_forward(const void* x, int64_t x_stride, const void* resi
               <<<dim3((uint32_t)blocks), dim3(s.threads), 0, (hipStream_t)stream>>>(
                   (const E*)x, x_stride, (const E*)residual, residual_stride, (const E*)weight,
                   (E*)sum, sum_stride, (E*)y, y_stride, (uint8_t*)codes, (uint8_t*)scales, rstd,
-                  rows, width, eps, s.lanes, per, group_lanes);
+                  rows, width, eps, 1.0 / (double)width, s.lanes, per, group_lanes);
         };
         if (!codes)
           go(std::integral_constant<int, -1>());

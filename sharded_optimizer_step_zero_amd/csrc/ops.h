@@ -211,10 +211,11 @@ __device__ __forceinline__ float group_amax(f32x8 x, int lanes) {
   }
   return __uint_as_float(m);
 }
-// The group's codes and scale byte of the lane's eight elements.
+// The codes of the lane's eight elements and their group's scale byte, given the
+// group's largest magnitude.
 template <int CODE>
-__device__ __forceinline__ u32x2 quantise8(f32x8 x, int lanes, uint32_t* byte) {
-  const uint32_t b = scale_byte<CODE>(group_amax(x, lanes));
+__device__ __forceinline__ u32x2 quantise8(f32x8 x, float amax, uint32_t* byte) {
+  const uint32_t b = scale_byte<CODE>(amax);
   *byte = b;
   const float inv = scale_inverse(b == 255u ? 127u : b);
   f32x8 s;
