@@ -85,8 +85,7 @@ int zs_embed_backward(const void *grad_out, int64_t grad_stride, const void *ids
  * x and `sum` must be NULL), rstd = 1 / sqrt(mean(s^2) + eps) in fp32, and
  * y = s * rstd * weight: in `dtype` to y (NULL: not wanted) and in 8 bits to
  * codes and scales (both NULL: not wanted; ceil(width / group) scale bytes a row,
- * codes rows of `width` bytes).  sum may be x or residual itself.  y rows have the
- * stride of x.  1 <= width <= 65536.
+ * codes rows of `width` bytes).  sum may be x or residual itself.  1 <= width <= 65536.
  */
 int zs_norm_forward(const void *x, int64_t x_stride, const void *residual,
                     int64_t residual_stride, const void *weight, void *sum, int64_t sum_stride,
