@@ -530,34 +530,42 @@ __global__ __launch_bounds__(WM* WN * 64, 1) void gemm_kernel(GemmArgs g) {
 }
 
 // Joins a token's partial maxima and sums: 64 threads a token, each over every
-// 64th part in order, then over the threads in order.
+// 64th part in order, then the threads in pairs.
 __global__ __launch_bounds__(1024) void join_stats_kernel(
     const float* __restrict__ part_max, const float* __restrict__ part_sum,
     const float* __restrict__ target_logit, const void* __restrict__ targets,
     int32_t target_bytes, int64_t tokens, int64_t vocab, int32_t parts, float* __restrict__ loss,
     float* __restrict__ lse) {
-  __shared__ float tops[64][16], sums[64][16];
+  __shared__ float tops[16][16], sums[16][16];
   const int tt = threadIdx.x & 15, s = threadIdx.x >> 4;
   const int64_t t = (int64_t)blockIdx.x * 16 + tt;
   // a part of nothing but -infinity, and no part at all, has the sum 0
   auto join = [](float& top, float& sum, float m, float x) {
     const float next = __builtin_fmaxf(top, m);
-    const float from = next == -__builtin_inff() ? 0.0f : next;
-    sum = sum * __builtin_amdgcn_exp2f((top - from) * 1.44269504f) +
-          x * __builtin_amdgcn_exp2f((m - from) * 1.44269504f);
+    const float from = next == -__builtin_inff() ? 0.0f : next * kLog2E;
+    sum = sum * exp2_of(top, from) + x * exp2_of(m, from);
     top = next;
   };
   float top = -__builtin_inff(), sum = 0.0f;
   if (t < tokens) {
-#pragma unroll 4
+#pragma unroll 8
     for (int p = s; p < parts; p += 64)
       join(top, sum, part_max[p * tokens + t], part_sum[p * tokens + t]);
   }
-  tops[s][tt] = top;
-  sums[s][tt] = sum;
+  for (int d = 16; d < 64; d <<= 1)  // the wave's four threads of the token
+    join(top, sum, __shfl_xor(top, d, 64), __shfl_xor(sum, d, 64));
+  if ((threadIdx.x & 63) < 16) {
+    tops[threadIdx.x >> 6][tt] = top;
+    sums[threadIdx.x >> 6][tt] = sum;
+  }
   __syncthreads();
+  if (threadIdx.x >= 64) return;
+  top = -__builtin_inff();
+  sum = 0.0f;
+#pragma unroll
+  for (int i = 0; i < 4; i++) join(top, sum, tops[s * 4 + i][tt], sums[s * 4 + i][tt]);
+  for (int d = 16; d < 64; d <<= 1) join(top, sum, __shfl_xor(top, d, 64), __shfl_xor(sum, d, 64));
   if (s != 0 || t >= tokens) return;
-  for (int i = 1; i < 64; i++) join(top, sum, tops[i][tt], sums[i][tt]);
   const float l = sum == 0.0f ? -__builtin_inff() : __builtin_logf(sum) + top;
   const int64_t target =
       target_bytes == 8 ? ((const int64_t*)targets)[t] : ((const int32_t*)targets)[t];
