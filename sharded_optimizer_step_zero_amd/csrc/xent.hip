@@ -72,7 +72,7 @@ struct GemmArgs {
   int64_t lda, ldb;      // strides, multiples of 8; a line's last chunk is whole in memory
   int64_t m, n, k;       // rows of A and of B, and k
   int32_t tiles_m, tiles_n;
-  int64_t k_per_split;   // a multiple of BK; the split is blockIdx.y
+  int64_t k_per_split;   // a multiple of BK
   // kStats, kGrad
   const void* targets;
   int32_t target_bytes;
@@ -123,13 +123,17 @@ __device__ __forceinline__ int64_t target_of(const GemmArgs& g, int64_t t) {
   return g.target_bytes == 8 ? ((const int64_t*)g.targets)[t] : ((const int32_t*)g.targets)[t];
 }
 
-// The tile of a workgroup.  Workgroups go round the 8 dies: each die takes a
-// contiguous part of the tiles, which run down a band of 8 tiles of B, so that the
-// tiles at work on a die share their rows of A and B in its L2.
-__device__ __forceinline__ void tile_of(const GemmArgs& g, int32_t* tm, int32_t* tn) {
-  const uint32_t total = (uint32_t)g.tiles_m * (uint32_t)g.tiles_n;
+// The tile of a workgroup, and its part of k.  Workgroups go round the 8 dies: each die
+// takes a contiguous part of the tiles of all splits, split by split, which run down
+// a band of 8 tiles of B, so that the tiles at work on a die share their rows of A
+// and B in its L2.
+__device__ __forceinline__ void tile_of(const GemmArgs& g, int32_t* tm, int32_t* tn,
+                                        int32_t* split) {
+  const uint32_t tiles = (uint32_t)g.tiles_m * (uint32_t)g.tiles_n, total = gridDim.x;
   const uint32_t die = blockIdx.x & 7, per = total >> 3, extra = total & 7;
-  const uint32_t id = die * per + (die < extra ? die : extra) + (blockIdx.x >> 3);
+  const uint32_t all = die * per + (die < extra ? die : extra) + (blockIdx.x >> 3);
+  *split = (int32_t)(all / tiles);
+  const uint32_t id = all - (uint32_t)*split * tiles;
   const uint32_t band = id / ((uint32_t)g.tiles_m * 8);
   const uint32_t in = id - band * (uint32_t)g.tiles_m * 8;
   const uint32_t wide = (uint32_t)g.tiles_n - band * 8 < 8 ? (uint32_t)g.tiles_n - band * 8 : 8;
@@ -250,10 +254,10 @@ __device__ __forceinline__ void gemm(const GemmArgs& g) {
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wm = wave / WN, wn = wave % WN;
-  int32_t tm, tn;
-  tile_of(g, &tm, &tn);
+  int32_t tm, tn, split;
+  tile_of(g, &tm, &tn, &split);
   const int64_t m0 = (int64_t)tm * BM, n0 = (int64_t)tn * BN;
-  const int64_t k_begin = blockIdx.y * g.k_per_split;
+  const int64_t k_begin = split * g.k_per_split;
   const int64_t k_end = k_begin + g.k_per_split < g.k ? k_begin + g.k_per_split : g.k;
   const int32_t k_len = k_end > k_begin ? (int32_t)(k_end - k_begin) : 0;
   const int steps = (k_len + BK - 1) / BK;
@@ -288,7 +292,7 @@ __device__ __forceinline__ void gemm(const GemmArgs& g) {
   // The tile of step s.  With few tokens the products are bound by memory, and rows at a
   // multiple of 4 KB would have all workgroups read one column, which few of the
   // memory's channels hold: there every workgroup begins at a step of its own.
-  const int turn = kTurned && steps > 0 ? (int)((uint32_t)(tm + blockIdx.y) * 5u % (uint32_t)steps) : 0;
+  const int turn = kTurned && steps > 0 ? (int)((uint32_t)(tm + split) * 5u % (uint32_t)steps) : 0;
   auto turned = [&](int s) {
     if (!kTurned || s >= steps) return s;
     const int at = s + turn;
@@ -440,7 +444,7 @@ __device__ __forceinline__ void gemm(const GemmArgs& g) {
       }
     }
   } else if constexpr (EPI == kAccum) {
-    float* out = g.acc + blockIdx.y * g.acc_split;
+    float* out = g.acc + split * g.acc_split;
 #pragma unroll
     for (int j = 0; j < FN; j++) {
       const int64_t n = n0 + en + j * 16;
@@ -732,7 +736,7 @@ int check(const char* who, const void* hidden, int64_t hidden_stride, const void
 
 template <int EPI, int LA, int LB>
 void launch(const GemmArgs& a, bool small, int dtype, int splits, hipStream_t s) {
-  const dim3 grid((uint32_t)(a.tiles_m * a.tiles_n), (uint32_t)splits);
+  const dim3 grid((uint32_t)a.tiles_m * (uint32_t)a.tiles_n * (uint32_t)splits);
   auto go = [&](auto DT) {
     constexpr int D = decltype(DT)::value;
     if (small)
@@ -756,7 +760,7 @@ bool shape(GemmArgs* a, bool small, int64_t m, int64_t n, int64_t k, int splits)
   a->tiles_m = (int32_t)tm;
   a->tiles_n = (int32_t)tn;
   a->k_per_split = std::max<int64_t>(up((k + splits - 1) / splits, BK), BK);
-  return tm * tn * 512 <= 0xffffffffll;
+  return tm * tn * splits * 512 <= 0xffffffffll;
 }
 
 void copy_rows(const void* in, int64_t stride, int64_t rows, int64_t width, void* out,
