@@ -207,7 +207,7 @@ extern "C" int zs_act8_pack(const void* x, int64_t x_stride, void* codes, void* 
   if (!x || !codes || !scales) return fail(who, "NULL buffer");
   if (!al(x, elem_bytes(dtype))) return fail(who, "a buffer is not aligned to its elements");
   const Spread s = spread(rows, width);
-  const bool nt = streams(rows * width * (1 + elem_bytes(dtype)));
+  const bool nt = dtype != ZS_F32 && streams(rows * width * (1 + elem_bytes(dtype)));
   with_dtype(dtype, [&](auto DT) {
     with_bool(nt, [&](auto NT) {
       with_code(code, [&](auto CODE) {
@@ -233,7 +233,7 @@ extern "C" int zs_act8_unpack(const void* codes, const void* scales, void* x, in
   if (!x || !codes || !scales) return fail(who, "NULL buffer");
   if (!al(x, elem_bytes(dtype))) return fail(who, "a buffer is not aligned to its elements");
   const Spread s = spread(rows, width);
-  const bool nt = streams(rows * width * (1 + elem_bytes(dtype)));
+  const bool nt = dtype != ZS_F32 && streams(rows * width * (1 + elem_bytes(dtype)));
   with_dtype(dtype, [&](auto DT) {
     with_bool(nt, [&](auto NT) {
       with_code(code, [&](auto CODE) {
@@ -266,7 +266,7 @@ extern "C" int zs_glu_forward(const void* gate_up, int64_t gate_up_stride, void*
   if (!al(gate_up, eb) || !al(out, eb)) return fail(who, "a buffer is not aligned to its elements");
   const Spread s = spread(rows, width);
   const int g = codes ? group : 128;
-  const bool nt = streams(rows * width * (3 * eb + (codes ? 2 : 0)));
+  const bool nt = dtype != ZS_F32 && streams(rows * width * (3 * eb + (codes ? 2 : 0)));
   with_dtype(dtype, [&](auto DT) {
     with_bool(nt, [&](auto NT) {
       with_act(act, [&](auto ACT) {
@@ -306,7 +306,7 @@ extern "C" int zs_glu_backward(const void* grad_out, int64_t grad_out_stride, co
   if (!al(grad_out, eb) || !al(grad_gate_up, eb) || !al(out, eb))
     return fail(who, "a buffer is not aligned to its elements");
   const Spread s = spread(rows, width);
-  const bool nt = streams(rows * width * ((out ? 4 : 3) * eb + 2));
+  const bool nt = dtype != ZS_F32 && streams(rows * width * ((out ? 4 : 3) * eb + 2));
   with_dtype(dtype, [&](auto DT) {
     with_bool(nt, [&](auto NT) {
       with_act(act, [&](auto ACT) {

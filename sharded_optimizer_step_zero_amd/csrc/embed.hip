@@ -237,12 +237,12 @@ __global__ __launch_bounds__(256) void reduce_kernel(
     for (int j = 0; j < kAhead; j++) {
       const int k = i + j < n ? i + j : n - 1;
       const int64_t t = __builtin_amdgcn_readlane(my_t, k);
-      x[j] = load_chunk<DT>(grad + t * grad_stride + c, left);
+      x[j] = load_row<DT>(grad + t * grad_stride, c, width);
     }
 #pragma unroll
     for (int j = 0; j < kAhead; j++) {
       if (i + j >= n) break;
-      sum += widen<DT>(x[j]);
+      sum += take8<DT>(x[j], left, width);
       const int64_t b = __builtin_amdgcn_readlane(my_first, i + j);
       const int64_t e = b + __builtin_amdgcn_readlane(my_count, i + j);
       const int64_t next = p0 + i + j + 1;

@@ -92,20 +92,25 @@ __global__ __launch_bounds__(T) void norm_kernel(
   const int in_row = threadIdx.x & (lanes - 1);
   const int64_t row = (int64_t)blockIdx.x * rows_per_block + (rows_per_block > 1 ? threadIdx.x / lanes : 0);
   const bool live = row < rows;  // no early return: the shuffles and barriers are the workgroup's
+  const int64_t from = live ? row : rows - 1;  // a row that exists
+  Chunk<DT> in[NC], add[NC];
+#pragma unroll
+  for (int k = 0; k < NC; k++) {
+    const int64_t c = (int64_t)(k * lanes + in_row) * 8;
+    in[k] = load_row<DT, NT>(x + from * x_stride, c, width);
+    if (residual) add[k] = load_row<DT, NT>(residual + from * residual_stride, c, width);
+  }
   f32x8 s[NC];
   double sq = 0.0;
 #pragma unroll
   for (int k = 0; k < NC; k++) {
     const int64_t c = (int64_t)(k * lanes + in_row) * 8, left = live ? width - c : 0;
-    s[k] = f32x8{};
-    if (left > 0) {
-      s[k] = load8<DT, NT>(x + row * x_stride + c, left);
-      if (residual) {
-        s[k] += load8<DT, NT>(residual + row * residual_stride + c, left);
-        // the stored, rounded sum is what is normalised
-        s[k] = __builtin_convertvector(__builtin_convertvector(s[k], typename Elem<DT>::vec), f32x8);
-        store8<DT, NT>(sum + row * sum_stride + c, left, s[k]);
-      }
+    s[k] = take8<DT>(in[k], left, width);
+    if (residual) {
+      s[k] += take8<DT>(add[k], left, width);
+      // the stored, rounded sum is what is normalised
+      s[k] = __builtin_convertvector(__builtin_convertvector(s[k], typename Elem<DT>::vec), f32x8);
+      store8<DT, NT>(sum + row * sum_stride + c, left, s[k]);
     }
     float q[4];
 #pragma unroll
@@ -177,14 +182,15 @@ __global__ __launch_bounds__(T) void norm_grad_kernel(
   }
   auto load = [&](int64_t row) {
     GradRow<DT, NC> r;
-    const bool live = row < rows;
-    r.rstd = live ? rstd[row] : 0.0f;
+    const int64_t from = row < rows ? row : rows - 1;  // a row that exists
+    r.rstd = rstd[from];
 #pragma unroll
     for (int k = 0; k < NC; k++) {
-      const int64_t c = (int64_t)(k * lanes + in_row) * 8, left = live ? width - c : 0;
-      r.s[k] = load_chunk<DT, NT>(sum + row * sum_stride + c, left);
-      r.dy[k] = load_chunk<DT, NT>(dy + row * dy_stride + c, left);
-      r.ds[k] = load_chunk<DT, NT>(ds + row * ds_stride + c, ds ? left : 0);
+      const int64_t c = (int64_t)(k * lanes + in_row) * 8;
+      r.s[k] = load_row<DT, NT>(sum + from * sum_stride, c, width);
+      r.dy[k] = load_row<DT, NT>(dy + from * dy_stride, c, width);
+      r.ds[k] = Chunk<DT>{};
+      if (ds) r.ds[k] = load_row<DT, NT>(ds + from * ds_stride, c, width);
     }
     return r;
   };
@@ -200,8 +206,9 @@ __global__ __launch_bounds__(T) void norm_grad_kernel(
     float dot = 0.0f;
 #pragma unroll
     for (int k = 0; k < NC; k++) {
-      h[k] = widen<DT>(now.s[k]) * now.rstd;
-      g[k] = widen<DT>(now.dy[k]);
+      const int64_t left = row < rows ? width - (int64_t)(k * lanes + in_row) * 8 : 0;
+      h[k] = take8<DT>(now.s[k], left, width) * now.rstd;
+      g[k] = take8<DT>(now.dy[k], left, width);
       dw[k] += g[k] * h[k];
       g[k] *= w[k];
 #pragma unroll
@@ -211,7 +218,7 @@ __global__ __launch_bounds__(T) void norm_grad_kernel(
 #pragma unroll
     for (int k = 0; k < NC; k++) {
       const int64_t c = (int64_t)(k * lanes + in_row) * 8, left = row < rows ? width - c : 0;
-      const f32x8 v = (g[k] - h[k] * mean) * now.rstd + widen<DT>(now.ds[k]);
+      const f32x8 v = (g[k] - h[k] * mean) * now.rstd + take8<DT>(now.ds[k], left, width);
       store8<DT, NT>(dx + row * dx_stride + c, left, v);
     }
   }
@@ -320,7 +327,7 @@ extern "C" int zs_norm_forward(const void* x, int64_t x_stride, const void* resi
   const int per = s.threads / s.lanes;
   const int64_t blocks = (rows + per - 1) / per;
   if (blocks > kMaxBlocks) return fail(who, "too many rows for one call");
-  const bool nt = streams(rows * width * ((residual ? 3 : 1) * eb + (y ? eb : 0) + (codes ? 1 : 0)));
+  const bool nt = dtype != ZS_F32 && streams(rows * width * ((residual ? 3 : 1) * eb + (y ? eb : 0) + (codes ? 1 : 0)));
   const int group_lanes = codes ? group / 8 : 16;
   with_dtype(dtype, [&](auto DT) {
     with_bool(nt, [&](auto NT) {
@@ -380,7 +387,7 @@ extern "C" int zs_norm_backward(const void* dy, int64_t dy_stride, const void* s
   const int per = s.threads / s.lanes;
   const int64_t blocks = grad_blocks(rows, width, s);
   const int64_t stride = part_stride_of(width);
-  const bool nt = streams(rows * width * eb * (grad_sum ? 4 : 3));
+  const bool nt = dtype != ZS_F32 && streams(rows * width * eb * (grad_sum ? 4 : 3));
   if (blocks)
     with_dtype(dtype, [&](auto DT) {
       with_bool(nt, [&](auto NT) {

@@ -87,6 +87,34 @@ template <int DT>
 __device__ __forceinline__ f32x8 widen(Chunk<DT> c) {
   return __builtin_convertvector(__builtin_bit_cast(typename Elem<DT>::vec, c), f32x8);
 }
+// The chunk of a row from element c on without a branch, so that loads under way are
+// not waited for where a row ends inside a wave: where the row ends before the
+// chunk does, its last eight elements, which take8() moves into place.  Rows
+// narrower than that are read element by element.
+template <int DT, bool NT = false>
+__device__ __forceinline__ Chunk<DT> load_row(const elem_t<DT>* row, int64_t c, int64_t width) {
+  if (width < 8) return load_chunk<DT>(row + c, width - c);
+  const elem_t<DT>* p = row + (c + 8 <= width ? c : width - 8);
+  Chunk<DT> r;
+#pragma unroll
+  for (int i = 0; i < Chunk<DT>::kWords; i++) r.w[i] = ld16<NT>((const u32x4_any*)p + i);
+  return r;
+}
+// load_row's chunk as fp32, n elements of it (of a row of `width`) in place and
+// zeros behind them; n <= 0: zeros.
+template <int DT>
+__device__ __forceinline__ f32x8 take8(Chunk<DT> x, int64_t n, int64_t width) {
+  const f32x8 v = widen<DT>(x);
+  f32x8 r = {};
+  if (n >= 8 || (width < 8 && n > 0)) return v;
+#pragma unroll
+  for (int k = 1; k < 8; k++)
+    if (n == k) {
+#pragma unroll
+      for (int i = 0; i < k; i++) r[i] = v[i + 8 - k];
+    }
+  return r;
+}
 // Eight elements as fp32.
 template <int DT, bool NT = false>
 __device__ __forceinline__ f32x8 load8(const elem_t<DT>* p, int64_t n) {
@@ -240,7 +268,9 @@ inline bool wide(const void* p, int64_t stride, int32_t dtype) {
   return al(p, 16) && (stride * elem_bytes(dtype)) % 16 == 0;
 }
 // Whether a call's arrays together pass the last-level cache (256 MB), so that
-// what it writes is gone from there before it is read again.
+// what it writes is gone from there before it is read again.  Streamed accesses gain 3
+// to 7% there in 16-bit types.  A chunk of fp32 takes two accesses, each half of every
+// line, and loses 10% (norm, 16384 x 8192: 432 against 478 us): its callers do without.
 inline bool streams(int64_t bytes) { return bytes >= (256ll << 20); }
 inline int launched(const char* who) {
   const hipError_t e = hipGetLastError();
