@@ -15,9 +15,9 @@
 //
 // Both are bound by HBM.  Where a group's largest lies next to the border at which the
 // scale steps, the last bit decides a factor of two; so the forward joins its
-// squares and takes the root in fp64, rounds rstd once, and looks at such groups
-// again in fp64.  (All products in two parts of fp32 took 172 us for 161.)  The
-// backward sums in fp32.  Measured, bf16: forward at 16384 x 8192 with residual and
+// squares and takes the root in fp64, rounds rstd once, and looks at such groups, and
+// at elements next to a tie of their code, again in fp64.  (All products in two parts
+// of fp32 took 172 us for 161.)  The backward sums in fp32.  Measured, bf16: forward at 16384 x 8192 with residual and
 // codes 163 us for 939 MB (5.8 TB/s), backward at 8192 x 4096 46 + 5 us for 268 MB (5.4
 // TB/s; 97 us without the prefetch).
 #include "ops.h"
@@ -144,8 +144,35 @@ __global__ __launch_bounds__(T) void norm_kernel(
         }
         amax = group_amax(v, group_lanes);
       }
-      uint32_t byte;
-      const u32x2 w = quantise8<CODE < 0 ? 0 : CODE>(v, amax, &byte);
+      constexpr int kCode = CODE < 0 ? 0 : CODE;
+      const uint32_t byte = scale_byte<kCode>(amax);
+      const float inv = scale_inverse(byte == 255u ? 127u : byte);
+      // the bits that a code drops, and half of its last place
+      constexpr uint32_t kDropped = kCode == ZS_E4M3 ? 0xfffffu : 0x1fffffu;
+      constexpr uint32_t kHalf = (kDropped + 1) / 2;
+      f32x8 z;
+      uint32_t near = ~0u;
+#pragma unroll
+      for (int i = 0; i < 8; i++) {
+        z[i] = v[i] * inv;
+        const uint32_t d = (__float_as_uint(z[i]) + kHalf + 2u) & kDropped;
+        near = d < near ? d : near;
+      }
+      if (near <= 4u && left > 0) {  // within two units of a tie: from products in fp64
+        const f32x8 wt = load8<DT>(weight + c, left);
+#pragma unroll
+        for (int i = 0; i < 8; i++) {
+          const double d = (double)s[k][i] * root * (double)wt[i] * (double)inv;
+          const float f = (float)d;
+          uint32_t u = __float_as_uint(f);
+          // a value that only fp32 puts on the tie keeps its side
+          if ((u & kDropped) == kHalf && (double)f != d)
+            u += __builtin_fabs(d) > __builtin_fabs((double)f) ? 1u : ~0u;
+          z[i] = __uint_as_float(u);
+        }
+      }
+      u32x2 w = encode8<kCode>(z);
+      if (byte == 255u) w = u32x2{0, 0};
       if (left > 0) {
         store_codes<NT>(codes + row * width + c, left, w);
         if (chunk % group_lanes == 0) scales[row * groups + chunk / group_lanes] = (uint8_t)byte;
