@@ -163,8 +163,9 @@ int zs_xent_forward(const void *hidden, int64_t hidden_stride, const void *weigh
  * (zero rows for tokens that do not count, whose hidden rows and grad_loss are not
  * used): grad_hidden = G weight and grad_weight = G^T hidden, each rounded once
  * to `dtype`; either may be NULL.  G is formed a piece of the vocabulary at a time,
- * divided by the largest finite |grad_loss| and rounded to `dtype` for the two products,
- * which sum in fp32; the factor comes back before the last rounding.
+ * divided by the largest finite |grad_loss| (and times 2^15 in fp16, whose digits end
+ * at 2^-14) and rounded to `dtype` for the two products, which sum in fp32; the factor
+ * comes back before the last rounding.
  * tokens <= 2^21 - 64.
  */
 int zs_xent_backward(const void *hidden, int64_t hidden_stride, const void *weight,

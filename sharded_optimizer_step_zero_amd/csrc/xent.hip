@@ -113,6 +113,12 @@ __device__ __forceinline__ u32x2 pack16(f32x4 x) {
   return __builtin_bit_cast(u32x2, __builtin_convertvector(x, v4));
 }
 constexpr float kLog2E = 1.44269504f;
+// G's largest magnitude.  Most of a softmax lies far below its targets, and fp16 has digits
+// down to 2^-14 only, but fifteen binades above 1 that nothing else would use: improbable
+// entries keep the digits they would lose, at no cost, as the factor comes back together
+// with grad_loss.  (A power of two: exact.  At 2^15 an error in p of any size below 1 still fits.)
+template <int DT>
+constexpr float kTopG = DT == ZS_F16 ? 0x1p15f : 1.0f;
 // e^x / e^y with y times log2 e given; one fused step, so that the argument of the
 // power of two is rounded once.
 __device__ __forceinline__ float exp2_of(float x, float y) {
@@ -475,7 +481,7 @@ __device__ __forceinline__ void gemm(const GemmArgs& g) {
         counts = target >= 0 && target < g.vocab;
         if (counts) {
           from = g.lse[t] * kLog2E;
-          scale = g.gloss[t] / factor;
+          scale = g.gloss[t] / factor * kTopG<DT>;
           at = mine(target);
         }
       }
@@ -484,7 +490,7 @@ __device__ __forceinline__ void gemm(const GemmArgs& g) {
         f32x4 x;
 #pragma unroll
         for (int r = 0; r < 4; r++)
-          x[r] = (EPI == kGrad ? exp2_of(acc[i][j][r], from) : acc[i][j][r]) * scale;
+          x[r] = (EPI == kGrad ? exp2_of(acc[i][j][r], from) : acc[i][j][r] / kTopG<DT>) * scale;
         u32x2 w = pack16<DT>(x);
         if (EPI == kGrad && !counts) w = u32x2{0, 0};
         *(u32x2*)to(row, em + i * 16) = w;
@@ -632,7 +638,7 @@ __global__ __launch_bounds__(256) void finish_kernel(const float* __restrict__ a
   if (row >= rows || c >= width) return;
   f32x4 s = {};
   for (int i = 0; i < splits; i++) s += *(const f32x4*)(acc + i * acc_split + row * acc_stride + c);
-  s *= *gmax;
+  s = s / kTopG<DT> * *gmax;
   for (int i = 0; i < 4; i++)
     if (c + i < width) out[row * out_stride + c + i] = (elem_t<DT>)s[i];
 }
