@@ -119,10 +119,29 @@ constexpr float kLog2E = 1.44269504f;
 // with grad_loss.  (A power of two: exact.  At 2^15 an error in p of any size below 1 still fits.)
 template <int DT>
 constexpr float kTopG = DT == ZS_F16 ? 0x1p15f : 1.0f;
-// e^x / e^y with y times log2 e given; one fused step, so that the argument of the
-// power of two is rounded once.
-__device__ __forceinline__ float exp2_of(float x, float y) {
-  return __builtin_amdgcn_exp2f(__builtin_fmaf(x, kLog2E, -y));
+// e^(x - y).  The difference comes first: where x is y the result is 1, so that a sum whose
+// maximum stays is joined unchanged however often.  (With y log2 e rounded beforehand, each
+// join multiplied by 1 + |y| 2^-24 or so: a token sure of its target was off by 20 units in
+// its lse, and p - 1 there could be positive.)
+__device__ __forceinline__ float exp_of(float x, float y) {
+  return __builtin_amdgcn_exp2f((x - y) * kLog2E);
+}
+// Many e^(x - y) of one y, in one fused step each, x log2 e - power, and what y log2 e lost
+// when it was rounded as a factor of them all.  (The difference first costs an instruction
+// an entry: 0.5% of the loss and gradients at 1003 x 1000 x 32003.)
+struct Under {
+  float power, factor;
+  __device__ __forceinline__ explicit Under(float y) {
+    power = y * kLog2E;
+    factor = __builtin_amdgcn_exp2f(-__builtin_fmaf(y, kLog2E, -power));
+  }
+  __device__ __forceinline__ float operator()(float x) const {  // e^(x - y) / factor
+    return __builtin_amdgcn_exp2f(__builtin_fmaf(x, kLog2E, -power));
+  }
+};
+// A maximum to take differences from, also where nothing has come yet: e^-infinity is 0.
+__device__ __forceinline__ float base_of(float top) {
+  return top == -__builtin_inff() ? 0.0f : top;
 }
 
 __device__ __forceinline__ int64_t target_of(const GemmArgs& g, int64_t t) {
@@ -424,14 +443,17 @@ __device__ __forceinline__ void gemm(const GemmArgs& g) {
         for (int r = 0; r < 4; r++) top = __builtin_fmaxf(top, acc[i][j][r]);
       top = __builtin_fmaxf(top, __shfl_xor(top, 16, 64));
       top = __builtin_fmaxf(top, __shfl_xor(top, 32, 64));
-      const float from = top == -__builtin_inff() ? 0.0f : top * kLog2E;
+      const Under under(base_of(top));
       float sum = 0.0f;
 #pragma unroll
       for (int i = 0; i < FM; i++)
 #pragma unroll
-        for (int r = 0; r < 4; r++) sum += exp2_of(acc[i][j][r], from);
+        for (int r = 0; r < 4; r++) sum += under(acc[i][j][r]);
       sum += __shfl_xor(sum, 16, 64);
       sum += __shfl_xor(sum, 32, 64);
+      sum *= under.factor;
+      // the maximum's own exponential is 1: what is below is rounding, and a loss is not negative
+      if (sum < 1.0f && top > -__builtin_inff()) sum = 1.0f;
       if (lane < 16) stats[wm * BN + en + j * 16] = f32x2{top, sum};
     }
     __syncthreads();
@@ -439,11 +461,10 @@ __device__ __forceinline__ void gemm(const GemmArgs& g) {
       float top = stats[i][0];
 #pragma unroll
       for (int w = 1; w < WM; w++) top = __builtin_fmaxf(top, stats[w * BN + i][0]);
-      const float from = top == -__builtin_inff() ? 0.0f : top * kLog2E;
       float sum = 0.0f;
 #pragma unroll
       for (int w = 0; w < WM; w++)
-        sum += stats[w * BN + i][1] * exp2_of(stats[w * BN + i][0], from);
+        sum += stats[w * BN + i][1] * exp_of(stats[w * BN + i][0], base_of(top));
       if (n0 + i < g.n) {
         g.part_max[tm * g.n + n0 + i] = top;
         g.part_sum[tm * g.n + n0 + i] = sum;
@@ -473,24 +494,26 @@ __device__ __forceinline__ void gemm(const GemmArgs& g) {
     for (int j = 0; j < FN; j++) {
       const int row = en + j * 16;
       const int64_t t = n0 + row;
-      float from = 0.0f, scale = factor;
+      float lse = 0.0f, scale = factor;
       bool counts = true;
       int at = -1;
       if (EPI == kGrad) {
         const int64_t target = t < g.n ? target_of(g, t) : -1;
         counts = target >= 0 && target < g.vocab;
         if (counts) {
-          from = g.lse[t] * kLog2E;
+          lse = g.lse[t];
           scale = g.gloss[t] / factor * kTopG<DT>;
           at = mine(target);
         }
       }
+      const Under under(lse);
+      const float each = EPI == kGrad ? scale * under.factor : scale;
 #pragma unroll
       for (int i = 0; i < FM; i++) {
         f32x4 x;
 #pragma unroll
         for (int r = 0; r < 4; r++)
-          x[r] = (EPI == kGrad ? exp2_of(acc[i][j][r], from) : acc[i][j][r] / kTopG<DT>) * scale;
+          x[r] = (EPI == kGrad ? under(acc[i][j][r]) : acc[i][j][r] / kTopG<DT>) * each;
         u32x2 w = pack16<DT>(x);
         if (EPI == kGrad && !counts) w = u32x2{0, 0};
         *(u32x2*)to(row, em + i * 16) = w;
@@ -502,7 +525,7 @@ __device__ __forceinline__ void gemm(const GemmArgs& g) {
           for (int r = 0; r < 4; r++)
             if (at == i * 16 + r)
               *(uint16_t*)to(row, em + at) =
-                  round16<DT>((exp2_of(acc[i][j][r], from) - 1.0f) * scale);
+                  round16<DT>((exp_of(acc[i][j][r], lse) - 1.0f) * scale);
       }
     }
     if (EPI == kGrad && g.v0 + m0 + BM > g.vocab) {  // zeros past the vocabulary
@@ -552,8 +575,7 @@ __global__ __launch_bounds__(1024) void join_stats_kernel(
   // a part of nothing but -infinity, and no part at all, has the sum 0
   auto join = [](float& top, float& sum, float m, float x) {
     const float next = __builtin_fmaxf(top, m);
-    const float from = next == -__builtin_inff() ? 0.0f : next * kLog2E;
-    sum = sum * exp2_of(top, from) + x * exp2_of(m, from);
+    sum = sum * exp_of(top, base_of(next)) + x * exp_of(m, base_of(next));
     top = next;
   };
   float top = -__builtin_inff(), sum = 0.0f;
@@ -576,11 +598,12 @@ __global__ __launch_bounds__(1024) void join_stats_kernel(
   for (int i = 0; i < 4; i++) join(top, sum, tops[s * 4 + i][tt], sums[s * 4 + i][tt]);
   for (int d = 16; d < 64; d <<= 1) join(top, sum, __shfl_xor(top, d, 64), __shfl_xor(sum, d, 64));
   if (s != 0 || t >= tokens) return;
-  const float l = sum == 0.0f ? -__builtin_inff() : __builtin_logf(sum) + top;
+  const float l = sum == 0.0f ? -__builtin_inff() : __builtin_logf(sum);
   const int64_t target =
       target_bytes == 8 ? ((const int64_t*)targets)[t] : ((const int32_t*)targets)[t];
-  lse[t] = l;
-  loss[t] = target >= 0 && target < vocab ? l - target_logit[t] : 0.0f;
+  lse[t] = l + top;
+  // not lse - logit: a small loss would be what lse's rounding leaves
+  loss[t] = target >= 0 && target < vocab ? l + (top - target_logit[t]) : 0.0f;
 }
 
 // Rows copied to a stride that is a multiple of 8 elements, zeros past the width.
