@@ -14,8 +14,9 @@
 // The next row's loads are under way while one is worked on.
 //
 // Both are bound by HBM.  Where a group's largest lies next to the border at which the
-// scale steps, the last bit decides a factor of two; so the forward joins its
-// squares and takes the root in fp64, rounds rstd once, and looks at such groups, and
+// scale steps, the last bit decides a factor of two; so the forward sums its
+// squares and takes the root in fp64, which also holds the squares of every finite
+// element, rounds rstd once, and looks at such groups, and
 // at elements next to a tie of their code, again in fp64.  (All products in two parts
 // of fp32 took 172 us for 161.)  The backward sums in fp32.  Measured, bf16: forward at 16384 x 8192 with residual and
 // codes 163 us for 939 MB (5.8 TB/s), backward at 8192 x 4096 46 + 5 us for 268 MB (5.4
@@ -70,15 +71,24 @@ __device__ __forceinline__ F row_sum(F x, int lanes, F* slots) {
   return s;
 }
 
-// 1 / sqrt(v) in fp64: the hardware's fp32 estimate, of v brought near 1, and a Newton
-// step; the estimate alone where the step has no meaning (0, infinity, NaN).
+// 1 / sqrt(v) in fp64: the hardware's fp32 estimate, of v brought within fp32's range (squares
+// reach from 2^-298 to 2^256, and their mean a little below), and two Newton steps; the
+// estimate alone where a step has no meaning (0, infinity, NaN).
 __device__ __forceinline__ double inverse_root(double v) {
   const bool tiny = v < 0x1p-100, huge = v > 0x1p100;
-  const float near = (float)(tiny ? v * 0x1p180 : huge ? v * 0x1p-180 : v);
-  double r = __builtin_amdgcn_rsqf(near);
+  v *= tiny ? 0x1p210 : huge ? 0x1p-180 : 1.0;
+  double r = __builtin_amdgcn_rsqf((float)v);
   if (!(r > 0.0 && r < __builtin_inf())) return r;
-  r *= tiny ? 0x1p90 : huge ? 0x1p-90 : 1.0;
-  return r * __builtin_fma(-0.5 * v * r, r, 1.5);
+  r *= __builtin_fma(-0.5 * v * r, r, 1.5);
+  r *= __builtin_fma(-0.5 * v * r, r, 1.5);
+  return r * (tiny ? 0x1p105 : huge ? 0x1p-90 : 1.0);
+}
+
+// x in fp64, made anew: a branch that is hardly ever taken must not have the values that the
+// squares were made of held for it (34 registers more: 196 us for 158 at 16384 x 8192).
+__device__ __forceinline__ double widen_again(float x) {
+  asm("" : "+v"(x));
+  return (double)x;
 }
 
 template <int DT, bool NT, int NC, int T, int CODE>
@@ -112,12 +122,9 @@ __global__ __launch_bounds__(T) void norm_kernel(
       s[k] = __builtin_convertvector(__builtin_convertvector(s[k], typename Elem<DT>::vec), f32x8);
       store8<DT, NT>(sum + row * sum_stride + c, left, s[k]);
     }
-    float q[4];
+    // a square of 24 bits is exact in fp64, and finite whatever the element
 #pragma unroll
-    for (int i = 0; i < 4; i++)
-      q[i] = __builtin_fmaf(s[k][i + 4], s[k][i + 4], s[k][i] * s[k][i]);
-    // eight squares' error in fp32 is one of many that cancel; their sum's is not
-    sq += (double)((q[0] + q[1]) + (q[2] + q[3]));
+    for (int i = 0; i < 8; i++) sq = __builtin_fma((double)s[k][i], (double)s[k][i], sq);
   }
   const double total = row_sum(sq, lanes, slots);
   const double root = inverse_root(__builtin_fma(total, inv_width, (double)eps));
@@ -140,7 +147,7 @@ __global__ __launch_bounds__(T) void norm_kernel(
         if (left > 0) {
           const f32x8 wt = load8<DT>(weight + c, left);
 #pragma unroll
-          for (int i = 0; i < 8; i++) v[i] = (float)((double)s[k][i] * root * (double)wt[i]);
+          for (int i = 0; i < 8; i++) v[i] = (float)(widen_again(s[k][i]) * root * (double)wt[i]);
         }
         amax = group_amax(v, group_lanes);
       }
@@ -162,7 +169,7 @@ __global__ __launch_bounds__(T) void norm_kernel(
         const f32x8 wt = load8<DT>(weight + c, left);
 #pragma unroll
         for (int i = 0; i < 8; i++) {
-          const double d = (double)s[k][i] * root * (double)wt[i] * (double)inv;
+          const double d = widen_again(s[k][i]) * root * (double)wt[i] * (double)inv;
           const float f = (float)d;
           uint32_t u = __float_as_uint(f);
           // a value that only fp32 puts on the tie keeps its side
