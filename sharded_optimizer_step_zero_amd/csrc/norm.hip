@@ -16,9 +16,9 @@
 // Both are bound by HBM.  Where a group's largest lies next to the border at which the
 // scale steps, the last bit decides a factor of two; so the forward sums its
 // squares and takes the root in fp64, which also holds the squares of every finite
-// element, rounds rstd once, and looks at such groups, and
-// at elements next to a tie of their code, again in fp64.  (All products in two parts
-// of fp32 took 172 us for 161.)  The backward sums in fp32.  Measured, bf16: forward at 16384 x 8192 with residual and
+// element, rounds rstd once, and takes such groups, and elements next to a tie of their
+// code, from products in fp64.  (All products in two parts of fp32 took 172 us for
+// 161.)  The backward sums in fp32.  Measured, bf16: forward at 16384 x 8192 with residual and
 // codes 163 us for 939 MB (5.8 TB/s), backward at 8192 x 4096 46 + 5 us for 268 MB (5.4
 // TB/s; 97 us without the prefetch).
 #include "ops.h"
@@ -90,6 +90,14 @@ __device__ __forceinline__ double widen_again(float x) {
   asm("" : "+v"(x));
   return (double)x;
 }
+// d in fp32, cut and its last bit set where that lost anything (rounded to odd): it lies on the
+// same side of every value of fewer bits as d, so rounding it again rounds d.
+__device__ __forceinline__ float side_of(double d) {
+  const float f = (float)d;
+  uint32_t u = __float_as_uint(f);
+  if ((double)f != d && d == d) u = (u - (__builtin_fabs((double)f) > __builtin_fabs(d) ? 1u : 0u)) | 1u;
+  return __uint_as_float(u);
+}
 
 template <int DT, bool NT, int NC, int T, int CODE>
 __global__ __launch_bounds__(T) void norm_kernel(
@@ -141,44 +149,39 @@ __global__ __launch_bounds__(T) void norm_kernel(
     }
     if (CODE >= 0) {
       float amax = group_amax(v, group_lanes);
-      if ((__float_as_uint(amax) & 0x7fffffu) - 0x5ffffeu <= 4u) {
-        // within two units of 1.75 times a power of two, where the scale steps: the
-        // group again with its products in fp64 (all of its lanes come here)
+      if ((__float_as_uint(amax) & 0x7fffffu) - 0x5ffffdu <= 6u) {
+        // within three units (three roundings make two and a quarter there) of 1.75 times a
+        // power of two, where the scale steps: the group again with its products in fp64
+        // (all of its lanes come here)
         if (left > 0) {
           const f32x8 wt = load8<DT>(weight + c, left);
 #pragma unroll
-          for (int i = 0; i < 8; i++) v[i] = (float)(widen_again(s[k][i]) * root * (double)wt[i]);
+          for (int i = 0; i < 8; i++)
+            v[i] = side_of(widen_again(s[k][i]) * root * (double)wt[i]);
         }
         amax = group_amax(v, group_lanes);
       }
       constexpr int kCode = CODE < 0 ? 0 : CODE;
       const uint32_t byte = scale_byte<kCode>(amax);
       const float inv = scale_inverse(byte == 255u ? 127u : byte);
-      // the bits that a code drops, and half of its last place
-      constexpr uint32_t kDropped = kCode == ZS_E4M3 ? 0xfffffu : 0x1fffffu;
-      constexpr uint32_t kHalf = (kDropped + 1) / 2;
-      f32x8 z;
-      uint32_t near = ~0u;
+      // The products are off by three roundings, and these two by one more: where what lies
+      // 2^-21 (four units or more) below and above has one code, that is the element's, normal or subnormal.
+      const float below = inv * (1.0f - 0x1p-21f), above = inv * (1.0f + 0x1p-21f);
+      f32x8 lo, hi;
 #pragma unroll
       for (int i = 0; i < 8; i++) {
-        z[i] = v[i] * inv;
-        const uint32_t d = (__float_as_uint(z[i]) + kHalf + 2u) & kDropped;
-        near = d < near ? d : near;
+        lo[i] = v[i] * below;
+        hi[i] = v[i] * above;
       }
-      if (near <= 4u && left > 0) {  // within two units of a tie: from products in fp64
+      u32x2 w = encode8<kCode>(lo);
+      const u32x2 other = encode8<kCode>(hi);
+      if ((w[0] != other[0] || w[1] != other[1]) && left > 0) {  // from products in fp64
         const f32x8 wt = load8<DT>(weight + c, left);
 #pragma unroll
-        for (int i = 0; i < 8; i++) {
-          const double d = widen_again(s[k][i]) * root * (double)wt[i] * (double)inv;
-          const float f = (float)d;
-          uint32_t u = __float_as_uint(f);
-          // a value that only fp32 puts on the tie keeps its side
-          if ((u & kDropped) == kHalf && (double)f != d)
-            u += __builtin_fabs(d) > __builtin_fabs((double)f) ? 1u : ~0u;
-          z[i] = __uint_as_float(u);
-        }
+        for (int i = 0; i < 8; i++)
+          lo[i] = side_of(widen_again(s[k][i]) * root * (double)wt[i] * (double)inv);
+        w = encode8<kCode>(lo);
       }
-      u32x2 w = encode8<kCode>(z);
       if (byte == 255u) w = u32x2{0, 0};
       if (left > 0) {
         store_codes<NT>(codes + row * width + c, left, w);
