@@ -363,7 +363,9 @@ extern "C" int zs_norm_forward(const void* x, int64_t x_stride, const void* resi
   const Shape s = shape(width);
   const int per = s.threads / s.lanes;
   const int64_t blocks = (rows + per - 1) / per;
-  if (blocks > kMaxBlocks) return fail(who, "too many rows for one call");
+  // a launch has fewer than 2^32 threads
+  if (blocks > kMaxBlocks || blocks * s.threads > 0xffffffffll)
+    return fail(who, "too many rows for one call");
   const bool nt = dtype != ZS_F32 && streams(rows * width * ((residual ? 3 : 1) * eb + (y ? eb : 0) + (codes ? 1 : 0)));
   const int group_lanes = codes ? group / 8 : 16;
   with_dtype(dtype, [&](auto DT) {
