@@ -85,7 +85,8 @@ int zs_embed_backward(const void *grad_out, int64_t grad_stride, const void *ids
  * x and `sum` must be NULL), rstd = 1 / sqrt(mean(s^2) + eps) in fp32, and
  * y = s * rstd * weight: in `dtype` to y (NULL: not wanted) and in 8 bits to
  * codes and scales (both NULL: not wanted; ceil(width / group) scale bytes a row,
- * codes rows of `width` bytes).  sum may be x or residual itself.  1 <= width <= 65536.
+ * codes rows of `width` bytes).  sum may be x or residual itself.  1 <= width <= 65536,
+ * rows < 2^25 up to 512 columns, < 2^23 up to 8192, < 2^22 beyond (one launch's).
  */
 int zs_norm_forward(const void *x, int64_t x_stride, const void *residual,
                     int64_t residual_stride, const void *weight, void *sum, int64_t sum_stride,
@@ -150,7 +151,7 @@ size_t zs_xent_workspace_bytes(const void *hidden, int64_t hidden_stride, const 
  * stored: lse[t] = log sum_v exp logits[t][v] and loss[t] = lse[t] -
  * logits[t][targets[t]], both fp32.  A target outside [0, vocab) marks a token
  * that does not count: its loss is 0.  dtype: ZS_BF16 or ZS_F16.
- * 1 <= vocab < 2^31 - 512, 1 <= width <= 65536, tokens < 2^31 - 512, strides <= 2^21.
+ * 1 <= vocab < 2^31 - 512, 1 <= width <= 65536, tokens <= 2^26 - 16, strides <= 2^21.
  */
 int zs_xent_forward(const void *hidden, int64_t hidden_stride, const void *weight,
                     int64_t weight_stride, const void *targets, float *loss, float *lse,
@@ -166,7 +167,7 @@ int zs_xent_forward(const void *hidden, int64_t hidden_stride, const void *weigh
  * divided by the largest finite |grad_loss| (and times 2^15 in fp16, whose digits end
  * at 2^-14) and rounded to `dtype` for the two products, which sum in fp32; the factor
  * comes back before the last rounding.
- * tokens <= 2^21 - 64.
+ * tokens <= 2^21 - 64, and tokens * ceil(width / 1024) < 2^24.
  */
 int zs_xent_backward(const void *hidden, int64_t hidden_stride, const void *weight,
                      int64_t weight_stride, const void *targets, const float *lse,

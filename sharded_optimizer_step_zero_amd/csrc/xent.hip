@@ -761,7 +761,9 @@ extern "C" int zs_xent_forward(const void* hidden, int64_t hidden_stride, const 
   if (!workspace || !al(workspace, 256)) return fail(who, "the workspace is NULL or not 256-byte aligned");
   if (workspace_bytes < p.total) return fail(who, "the workspace is too small");
   GemmArgs a{};
-  if (!shape(&a, p.small, vocab, tokens, p.wp, 1)) return fail(who, "too many rows for one call");
+  const int64_t join_blocks = (tokens + 15) / 16;
+  if (!shape(&a, p.small, vocab, tokens, p.wp, 1) || join_blocks * 1024 > 0xffffffffll)
+    return fail(who, "too many rows for one call");
   hipStream_t s = (hipStream_t)stream;
   uint8_t* ws = (uint8_t*)workspace;
   a.a = (const uint16_t*)weight;
@@ -786,7 +788,7 @@ extern "C" int zs_xent_forward(const void* hidden, int64_t hidden_stride, const 
   a.target_logit = (float*)(ws + p.tlogit);
   launch<kStats, kByK, kByK>(a, p.small, dtype, 1, s);
   if (int rc = launched(who)) return rc;
-  join_stats_kernel<<<dim3((uint32_t)((tokens + 15) / 16)), dim3(1024), 0, s>>>(
+  join_stats_kernel<<<dim3((uint32_t)join_blocks), dim3(1024), 0, s>>>(
       a.part_max, a.part_sum, a.target_logit, targets, target_bytes, tokens, vocab,
       (int32_t)p.parts, loss, lse);
   return launched(who);
