@@ -190,7 +190,8 @@ __global__ __launch_bounds__(256) void glu_grad_kernel(
   for (int i = 0; i < 8; i++) {
     float slope;
     const float a = activation<DT, ACT>(g[i], &slope);
-    dg[i] = d[i] * u[i] * slope;
+    // the slope, of about 1 at most, first: d u alone may pass fp32 where the gradient does not
+    dg[i] = u[i] * slope * d[i];
     du[i] = d[i] * a;
     o[i] = a * u[i];
   }
