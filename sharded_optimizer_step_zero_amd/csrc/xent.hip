@@ -232,16 +232,23 @@ struct Operand {
   __device__ __forceinline__ uint32_t limited(int step, int i) const {
     return LAYOUT == kByK && chunk_k >= k_len - step * BK ? 0xfffffff0u : off[i];
   }
-  // Load i of the tile, into LDS at `lds` (the wave's part of the load).
+  // Load i of the tile, into LDS at `lds` (the wave's part of the load).  The compiler does not
+  // see a load here: a descriptor's scalar that a vector instruction wrote would have to be
+  // five wait states old.  Descriptors come from the scalar side; test_ops_assembly_hazards.py
+  // looks whether any build brings one closer (a wait here costs the loop 0.7%).
   __device__ __forceinline__ void load(u32x4 d, int i, uint32_t lds) const {
     load(d, off[i], i, lds);
   }
   __device__ __forceinline__ void load(u32x4 d, uint32_t from, int i, uint32_t lds) const {
+    // m0 is the compiler's own, which it warns of: it has to know that its value is gone
+#pragma clang diagnostic push
+#pragma clang diagnostic ignored "-Winline-asm"
     asm volatile(
         "s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds" ::"s"(
             lds + i * THREADS * 16),
         "v"(from), "s"(d)
-        : "memory");
+        : "memory", "m0");
+#pragma clang diagnostic pop
   }
   // Fragment f of the tile's half `half`, for the wave whose first row is `row0`: 16
   // rows and 32 k; a lane has 8 k of one row.
