@@ -158,12 +158,16 @@ __global__ __launch_bounds__(kSortThreads) void sort_kernel(
         const int32_t s = __builtin_amdgcn_readlane(slot, leader);
         const bool same = mine && slot == s;
         const uint64_t peers = __ballot(same);
+        // one lane takes the places of all: no lane reads what another wrote
+        int32_t first_place = 0;
+        if (lane == leader)
+          first_place = atomicAdd(&cnt[wave][s], (int32_t)__builtin_popcountll(peers));
+        first_place = __builtin_amdgcn_readlane(first_place, leader);
         if (same) {
           const int32_t place =
-              cnt[wave][s] + (int32_t)__builtin_popcountll(peers & ((1ull << lane) - 1));
+              first_place + (int32_t)__builtin_popcountll(peers & ((1ull << lane) - 1));
           order[place] = (int32_t)(t0 + i * 64 + lane);
           sorted[place] = held[i];
-          if (lane == leader) cnt[wave][s] += (int32_t)__builtin_popcountll(peers);
         }
         todo &= ~peers;
       }
