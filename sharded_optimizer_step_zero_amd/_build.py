@@ -48,7 +48,7 @@ def build(verbose: bool = False, extra_flags=None) -> str:
             if p.wait():
                 raise subprocess.CalledProcessError(p.returncode, cmd)
         # the objects go to the linker as they are (hipcc would read them as source)
-        cmd = ["hipcc", *HIPCC_FLAGS, "-shared", "-o", LIB + ".tmp",
+        cmd = ["hipcc", *HIPCC_FLAGS, *(extra_flags or []), "-shared", "-o", LIB + ".tmp",
                *[f"-Wl,{o}" for o in objs], "-pthread"]
         if verbose:
             print(" ".join(cmd), flush=True)
