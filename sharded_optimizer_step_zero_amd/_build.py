@@ -44,9 +44,10 @@ def build(verbose: bool = False, extra_flags=None) -> str:
                 print(" ".join(cmd), flush=True)
             running.append((cmd, subprocess.Popen(cmd)))
             objs.append(obj)
-        for cmd, p in running:
-            if p.wait():
-                raise subprocess.CalledProcessError(p.returncode, cmd)
+        # all of them end before the folder that they write to goes
+        failed = [(cmd, p) for cmd, p in running if p.wait()]
+        for cmd, p in failed:
+            raise subprocess.CalledProcessError(p.returncode, cmd)
         # the objects go to the linker as they are (hipcc would read them as source)
         cmd = ["hipcc", *HIPCC_FLAGS, *(extra_flags or []), "-shared", "-o", LIB + ".tmp",
                *[f"-Wl,{o}" for o in objs], "-pthread"]

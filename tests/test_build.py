@@ -44,3 +44,12 @@ def test_flags_reach_every_compiler_and_the_linker(builder):
     assert os.path.exists(builder.LIB)
     assert len(builder.commands) == 3 and all("-DEXTRA=1" in c for c in builder.commands)
     assert "-shared" in builder.commands[-1]
+
+
+def test_a_failing_source_leaves_nothing_running(builder, tmp_path):
+    builder.SOURCES = [str(tmp_path / f) for f in ("bad.cpp", "slow.cpp", "a.cpp")]
+    with pytest.raises(subprocess.CalledProcessError) as e:
+        builder.build()
+    assert any(c.endswith("bad.cpp") for c in e.value.cmd)
+    assert len(builder.started) == 3 and all(p.returncode is not None for p in builder.started)
+    assert not os.path.exists(builder.LIB) and not os.path.exists(builder.LIB + ".tmp")
