@@ -101,7 +101,7 @@ size_t zs_norm_backward_bytes(int64_t rows, int64_t width);
  * With h = s * rstd: grad_x = rstd * (weight*dy - h * mean(weight*dy*h)) +
  * grad_sum (NULL: nothing to add), which is the gradient of x and of the residual
  * alike, and grad_weight = sum over rows of dy * h (in `weight_dtype`: `dtype` or
- * ZS_F32).  Sums in fp32.  grad_x may be dy or grad_sum itself.
+ * ZS_F32).  Sums in fp32.  grad_x may be dy, sum or grad_sum itself.
  */
 int zs_norm_backward(const void *dy, int64_t dy_stride, const void *sum, int64_t sum_stride,
                      const void *weight, const float *rstd, const void *grad_sum,
@@ -163,10 +163,10 @@ int zs_xent_forward(const void *hidden, int64_t hidden_stride, const void *weigh
  * With G[t][v] = grad_loss[t] * (exp(logits[t][v] - lse[t]) - [v == targets[t]])
  * (zero rows for tokens that do not count, whose hidden rows and grad_loss are not
  * used): grad_hidden = G weight and grad_weight = G^T hidden, each rounded once
- * to `dtype`; either may be NULL.  G is formed a piece of the vocabulary at a time,
- * divided by the largest finite |grad_loss| (and times 2^15 in fp16, whose digits end
- * at 2^-14) and rounded to `dtype` for the two products, which sum in fp32; the factor
- * comes back before the last rounding.
+ * to `dtype`; either may be NULL.  grad_hidden may be hidden itself.  G is formed a
+ * piece of the vocabulary at a time, divided by the largest finite |grad_loss| (and times
+ * 2^15 in fp16, whose digits end at 2^-14) and rounded to `dtype` for the two products,
+ * which sum in fp32; the factor comes back before the last rounding.
  * tokens <= 2^21 - 64, and tokens * ceil(width / 1024) < 2^24.
  */
 int zs_xent_backward(const void *hidden, int64_t hidden_stride, const void *weight,

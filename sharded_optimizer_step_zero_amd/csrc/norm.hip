@@ -200,8 +200,8 @@ struct GradRow {
 
 template <int DT, bool NT, int NC, int T>
 __global__ __launch_bounds__(T) void norm_grad_kernel(
-    const elem_t<DT>* dy, int64_t dy_stride, const elem_t<DT>* __restrict__ sum,
-    int64_t sum_stride, const elem_t<DT>* __restrict__ weight, const float* __restrict__ rstd,
+    const elem_t<DT>* dy, int64_t dy_stride, const elem_t<DT>* sum, int64_t sum_stride,
+    const elem_t<DT>* __restrict__ weight, const float* __restrict__ rstd,
     const elem_t<DT>* ds, int64_t ds_stride, elem_t<DT>* dx, int64_t dx_stride,
     float* __restrict__ parts, int64_t part_stride, int64_t rows, int64_t width, int lanes,
     int rows_per_block) {

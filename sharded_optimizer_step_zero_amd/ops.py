@@ -9,11 +9,13 @@ below check what the kernels will stream over, allocate outputs and workspace
 with torch, and enqueue on torch's current stream of the tensors' device.
 
 There is no autograd here: forward and backward are separate calls, and what the
-backward reads is what the forward returned.  Matrices are 2-D with adjacent
+backward reads is what the forward returned.  Tensors that require a gradient are
+read like any other, and results carry no history.  Matrices are 2-D with adjacent
 elements in a row and any row stride of at least the width; ``out=`` arguments
 take such views too, so a gradient can be written straight into a contribution
-buffer of ZeroShard.  Arguments the kernels could not read are refused with
-ValueError before anything is enqueued.
+buffer of ZeroShard.  They must not overlap what the call reads or the call's other
+outputs, except where its description allows an input itself.  Arguments the kernels
+could not read or write so are refused with ValueError before anything is enqueued.
 
 The 8-bit form: codes as torch.float8_e4m3fn or torch.float8_e5m2, and one
 power-of-two scale (torch.float8_e8m0fnu) for each group of 32, 64 or 128
@@ -204,6 +206,42 @@ def _run(device, entry, *args):
         _check(rc)
 
 
+def _extent(t):
+    """(address, rows, bytes from row to row, bytes of a row) of a matrix, or of a
+    contiguous tensor as one row."""
+    e = t.element_size()
+    if t.dim() == 2 and t.shape[0] > 1:
+        return t.data_ptr(), t.shape[0], t.stride(0) * e, t.shape[1] * e
+    return t.data_ptr(), 1, t.numel() * e, t.numel() * e
+
+
+def _overlap(a, b):
+    """Whether two tensors share a byte: rows of views side by side in one buffer do not."""
+    pa, na, sa, wa = _extent(a)
+    pb, nb, sb, wb = _extent(b)
+    if not wa or not wb or pa + (na - 1) * sa + wa <= pb or pb + (nb - 1) * sb + wb <= pa:
+        return False
+    if na > nb:
+        pa, na, sa, wa, pb, nb, sb, wb = pb, nb, sb, wb, pa, na, sa, wa
+    if na == 1:
+        at = torch.tensor([pa - pb])
+    else:
+        at = torch.arange(na, dtype=torch.int64) * sa + (pa - pb)
+    # of each row of a: the first of b's rows that ends behind its beginning
+    row = torch.div(at - wb, sb, rounding_mode="floor").add_(1).clamp_(min=0)
+    return bool(((row < nb) & (row * sb < at + wa)).any())
+
+
+def _apart(out, name, allowed, others):
+    """Refuses an output that overlaps an input; it may be one of `allowed` itself."""
+    for t in allowed:
+        if t is not None and (t.data_ptr() != out.data_ptr() or t.stride() != out.stride()):
+            others = (*others, t)
+    for t in others:
+        if t is not None and _overlap(out, t):
+            raise ValueError(f"{name}: overlaps another buffer of the call")
+
+
 def _workspace(given, nbytes, device):
     if nbytes == 0:
         raise ValueError("a size is out of the range the operator takes")
@@ -245,6 +283,7 @@ def embed(table, ids, scale=1.0, vocab_start=0, out=None):
         out_stride = width
     else:
         out_stride = _matrix(out, "out", table.dtype, dev, n, width)
+        _apart(out, "out", (), (table, ids))
     _run(dev, _embed_forward, table.data_ptr(), stride, ids.data_ptr(), out.data_ptr(), out_stride,
          n, vocab, width, vocab_start, scale, dt, nb)
     return out
@@ -273,6 +312,7 @@ def embed_backward(grad_out, ids, vocab, scale=1.0, vocab_start=0, out=None, out
         out_stride = width
     else:
         out_stride = _matrix(out, "out", out_dtype, dev, vocab, width)
+        _apart(out, "out", (), (grad_out, ids))
     if out.dtype not in (grad_out.dtype, torch.float32):
         raise ValueError(f"out: dtype {out.dtype}, expected {grad_out.dtype} or torch.float32")
     ws = _workspace(workspace, _embed_backward_bytes(n, vocab, width), dev)
@@ -331,7 +371,8 @@ def norm_backward(grad_y, sum, weight, rstd, grad_sum=None, out=None, weight_gra
                   weight_grad_dtype=None, workspace=None):
     """(grad_x, grad_weight) of norm: grad_x is the gradient of x and of the residual
     alike, with grad_sum (the gradient that reaches s by the residual path) added.
-    grad_weight in the weight's dtype, or fp32 with weight_grad_dtype=torch.float32."""
+    grad_weight in the weight's dtype, or fp32 with weight_grad_dtype=torch.float32.
+    out may be grad_y, sum or grad_sum itself."""
     gs = _matrix(grad_y, "grad_y")
     dev = grad_y.device
     dt = _dtype(grad_y, "grad_y")
@@ -347,12 +388,14 @@ def norm_backward(grad_y, sum, weight, rstd, grad_sum=None, out=None, weight_gra
         os_ = width
     else:
         os_ = _matrix(out, "out", grad_y.dtype, dev, rows, width)
+        _apart(out, "out", (grad_y, sum, grad_sum), (weight, rstd))
     if weight_grad_out is None:
         weight_grad_out = torch.empty(width, dtype=weight_grad_dtype or grad_y.dtype, device=dev)
     else:
         _vector(weight_grad_out, "weight_grad_out",
                 (weight_grad_dtype,) if weight_grad_dtype else (grad_y.dtype, torch.float32), dev,
                 width)
+        _apart(weight_grad_out, "weight_grad_out", (), (grad_y, sum, weight, rstd, grad_sum, out))
     if weight_grad_out.dtype not in (grad_y.dtype, torch.float32):
         raise ValueError(f"weight_grad_dtype: {weight_grad_out.dtype}, expected {grad_y.dtype} or "
                          "torch.float32")
@@ -416,6 +459,7 @@ def unpack8(codes, scales, dtype, group=128, out=None):
         stride = width
     else:
         stride = _matrix(out, "out", dtype, dev, rows, width)
+        _apart(out, "out", (), (codes, scales))
     if rows:
         _run(dev, _act8_unpack, codes.data_ptr(), scales.data_ptr(), out.data_ptr(), stride, rows,
              width, dt, cd, group)
@@ -467,6 +511,7 @@ def glu_backward(grad_out, codes, scales, act="silu", group=128, want_out=False,
         os_ = 2 * width
     else:
         os_ = _matrix(out, "out", grad_out.dtype, dev, rows, 2 * width)
+        _apart(out, "out", (), (grad_out, codes, scales))
     again = torch.empty(rows, width, dtype=grad_out.dtype, device=dev) if want_out else None
     if rows:
         _run(dev, _glu_backward, grad_out.data_ptr(), gs, codes.data_ptr(), scales.data_ptr(),
@@ -508,7 +553,7 @@ def linear_xent_backward(hidden, weight, targets, lse, grad_loss, out=None, weig
                          want_hidden=True, want_weight=True, workspace=None):
     """(grad_hidden, grad_weight) of linear_xent for grad_loss [tokens] (fp32; 1/n for
     a mean over n tokens, times the loss scale where gradients are fp16).  What is
-    not wanted is None."""
+    not wanted is None.  out may be hidden itself."""
     hs, wstride, dev, dt, nb = _xent_args(hidden, weight, targets)
     tokens, width = hidden.shape
     vocab = weight.shape[0]
@@ -522,12 +567,14 @@ def linear_xent_backward(hidden, weight, targets, lse, grad_loss, out=None, weig
             gh = torch.empty(tokens, width, dtype=hidden.dtype, device=dev)
         else:
             ghs = _matrix(gh, "out", hidden.dtype, dev, tokens, width)
+            _apart(gh, "out", (hidden,), (weight, targets, lse, grad_loss))
     if want_weight:
         gw = weight_grad_out
         if gw is None:
             gw = torch.empty(vocab, width, dtype=hidden.dtype, device=dev)
         else:
             gws = _matrix(gw, "weight_grad_out", hidden.dtype, dev, vocab, width)
+            _apart(gw, "weight_grad_out", (), (hidden, weight, targets, lse, grad_loss, gh))
     h, w = hidden.data_ptr(), weight.data_ptr()
     ws = _workspace(workspace, _xent_workspace_bytes(h, hs, w, wstride, tokens, vocab, width, 1),
                     dev)
