@@ -305,10 +305,12 @@ Layout layout(int64_t n, int64_t vocab, int64_t width) {
   l.bucket_log2 = 8;
   while (((vocab + (1ll << l.bucket_log2) - 1) >> l.bucket_log2) > kMaxSlots) l.bucket_log2++;
   l.slabs = (width + kCols - 1) / kCols;
-  // short runs where there are few: a wave's rows come one batch after another (3001 tokens of
-  // 1001: 33 us with runs of 32, 14 with 8; 16384 of 4096, with more parts to join: 73 with
-  // 32 and 7 of joining, 73 and 18 with 8)
-  l.run = n * l.slabs <= 8 * 8192 ? 8 : kMaxRun;
+  // short runs where there are few wave-rows (tokens times slabs), since a wave's rows come one
+  // batch after another; long ones where there are more, with fewer parts to join.  Runs of
+  // 8 and of 32, the call's us: 3001 tokens of 1001 23 and 32, 6000 of 1001 28 and 32, 8192 of
+  // 512 26 and 29; about equal at 12000 wave-rows (12000 of 512 30 and 30, 1500 of 4096 60 and
+  // 58); 4096 of 4096 69 and 59, 16384 of 1024 41 and 35, 60000 of 512 96 and 70.
+  l.run = n * l.slabs <= 12288 ? 8 : kMaxRun;
   l.runs = (n + l.run - 1) / l.run;
   l.part_stride = (width + 7) / 8 * 8;
   size_t at = 0;

@@ -38,7 +38,8 @@ def in_order(dout, ids, vocab, run):
 
 @pytest.mark.parametrize("tokens, vocab, kind, run", [
     (5000, 40, "random", 8), (5000, 3000, "skewed", 8), (4000, 5, "same", 8), (3000, 2000, "bucket", 8),
-    (70_000, 300, "skewed", 32), (20_000, 70_000, "skewed", 8)])
+    (70_000, 300, "skewed", 32), (20_000, 70_000, "skewed", 32), (12_288, 900, "random", 8),
+    (12_289, 900, "random", 32)])
 def test_sums_are_added_in_order(tokens, vocab, kind, run):
     ids = make_ids(kind, tokens, vocab, 4)
     dout = rows(tokens, 8, torch.float32, 5)
