@@ -25,11 +25,13 @@ constexpr int64_t kCus = 256;
 inline int64_t tiles(int64_t m, int64_t n, bool small) {
   return small ? up(m, 128) / 128 * (up(n, 64) / 64) : up(m, 256) / 256 * (up(n, 256) / 256);
 }
-// Whether a product takes the small tiles: where few rows of B leave a large one
-// mostly empty, and where large ones leave much of the card idle.  Loss and gradients
-// at 512 tokens x 1024 x 8000 take 77 us so and 138 with large tiles only; where
-// large tiles nearly fill the card they are better (2048 x 2048 x 8000, 250 tiles: 269
-// against 358 us).
+// Whether a product takes the small tiles: where few rows of B leave a large one mostly
+// empty, and where large ones leave much of the card idle.  Loss and gradients, us with small
+// and with large tiles throughout (tokens x width x vocab): 512 x 1024 x 8000 74 and 138, 1024 x
+// 2048 x 4000 111 and 190, 300 x 1536 x 20000 154 and 179, 768 x 512 x 16000 108 and 131; about
+// equal at 1500 x 1024 x 8000, 192 tiles of the logits, 172 and 171 (161 as chosen here); 1500 x
+// 2048 x 8000 275 and 226, 2048 x 2048 x 8000 345 and 259, 1003 x 1000 x 32003 422 and 319.
+// Between 150 and 192 tiles either may win by a tenth.
 inline bool few(int64_t m, int64_t n, int64_t splits) {
   return n <= 128 || tiles(m, n, false) * splits <= 192;
 }
