@@ -55,7 +55,8 @@ extern "C" {
  * out[t] = scale * table[ids[t] - vocab_start], the product rounded once to
  * `dtype` (table and out).  A token whose local id lies outside [0, vocab) -- a
  * padding id, or an id of another part of a divided table -- gives a row of
- * zeros.  id_bytes: 4 or 8.
+ * zeros.  id_bytes: 4 or 8.  1 <= vocab <= 2^24, 1 <= width <= 2^20, n_tokens < 2^23
+ * (more up to 1024 columns: what one launch holds).
  */
 int zs_embed_forward(const void *table, int64_t table_stride, const void *ids, void *out,
                      int64_t out_stride, int64_t n_tokens, int64_t vocab, int64_t width,
@@ -72,7 +73,7 @@ size_t zs_embed_backward_bytes(int64_t n_tokens, int64_t vocab, int64_t width);
  * their rows are not read.  accumulate = 0 writes every row (zeros where no token
  * fell); accumulate = 1 adds to the rows that tokens fell on and leaves the rest
  * as they are (a tied table whose other gradient was written before).
- * n_tokens < 2^31, vocab <= 2^24.
+ * n_tokens < 2^31 and what one launch holds, vocab and width as above.
  */
 int zs_embed_backward(const void *grad_out, int64_t grad_stride, const void *ids,
                       void *grad_table, int64_t table_stride, int64_t n_tokens, int64_t vocab,
@@ -110,7 +111,11 @@ int zs_norm_backward(const void *dy, int64_t dy_stride, const void *sum, int64_t
                      int32_t weight_dtype, void *workspace, size_t workspace_bytes,
                      void *stream);
 
-/* x in the 8-bit form, and back (each value rounded once to `dtype`). */
+/*
+ * x in the 8-bit form, and back (each value rounded once to `dtype`).  Here and in the
+ * gated unit 1 <= width <= 2^20 and rows * ceil(width / 2048) < 2^23 (more rows below
+ * 1024 columns: what one launch holds).
+ */
 int zs_act8_pack(const void *x, int64_t x_stride, void *codes, void *scales, int64_t rows,
                  int64_t width, int32_t dtype, int32_t code, int32_t group, void *stream);
 int zs_act8_unpack(const void *codes, const void *scales, void *x, int64_t x_stride,

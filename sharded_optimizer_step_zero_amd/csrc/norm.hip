@@ -19,7 +19,7 @@
 // element, rounds rstd once, and takes such groups, and elements next to a tie of their
 // code, from products in fp64.  (All products in two parts of fp32 took 172 us for
 // 161.)  The backward sums in fp32.  Measured, bf16: forward at 16384 x 8192 with residual and
-// codes 163 us for 939 MB (5.8 TB/s), backward at 8192 x 4096 46 + 5 us for 268 MB (5.4
+// codes 160 us for 939 MB (5.9 TB/s), backward at 8192 x 4096 46 + 5 us for 268 MB (5.4
 // TB/s; 97 us without the prefetch).
 #include "ops.h"
 
@@ -38,8 +38,10 @@ int64_t backward_groups(int64_t width) {
 
 // How a row is spread: `lanes` threads with nc chunks of 8 each; rows up to 512
 // wide share a workgroup of 256.  Two chunks a thread before more threads: at
-// 16384 rows of 8192, 512 threads with 2 chunks take 165 us, 256 with 4 173 and 1024
-// with 1 200.
+// 16384 rows of 8192, the forward with 512 threads and 2 chunks takes 165 us, with 256 and 4
+// 173 and with 1024 and 1 200.  The backward has the same shape, which serves it up to 8192
+// columns (8192 rows: 96 us, 5.6 TB/s); a workgroup of 1024 leaves it 128 registers a lane
+// where it needs more, and above it spills inside its loop: 8192 x 12288 732 us, 1.1 TB/s.
 struct Shape {
   int lanes, nc, threads;
 };

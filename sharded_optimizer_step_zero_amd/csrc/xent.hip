@@ -38,8 +38,8 @@
 // loops).  Rows past the edge and k past the end read as zeros by the buffer loads'
 // bounds check.
 //
-// Measured, 8192 tokens x 4096 x 32000 bf16: loss 1.65 ms (1300 TFLOP/s), loss and
-// gradients 6.7 ms (1280 TFLOP/s of the 8 tokens vocab width operations done; the
+// Measured, 8192 tokens x 4096 x 32000 bf16: loss 1.68 ms (1280 TFLOP/s), loss and
+// gradients 6.74 ms (1270 TFLOP/s of the 8 tokens vocab width operations done; the
 // library's bare product 1370 to 1430).  The clock gives way under the load: on
 // zeros the same loop runs at 1650.  32x32x16 instructions are faster on zeros (1745) and
 // slower on data (1190).  64 x 2048 x 50304: 46 us of reading W at 4.5 TB/s, and 5 joining.

@@ -31,7 +31,7 @@ inline int64_t tiles(int64_t m, int64_t n, bool small) {
 // 2048 x 4000 111 and 190, 300 x 1536 x 20000 154 and 179, 768 x 512 x 16000 108 and 131; about
 // equal at 1500 x 1024 x 8000, 192 tiles of the logits, 172 and 171 (161 as chosen here); 1500 x
 // 2048 x 8000 275 and 226, 2048 x 2048 x 8000 345 and 259, 1003 x 1000 x 32003 422 and 319.
-// Between 150 and 192 tiles either may win by a tenth.
+// Between 150 and 192 tiles either may win by a tenth or more.
 inline bool few(int64_t m, int64_t n, int64_t splits) {
   return n <= 128 || tiles(m, n, false) * splits <= 192;
 }
