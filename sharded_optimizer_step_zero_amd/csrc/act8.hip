@@ -104,7 +104,8 @@ struct Logistic<ZS_F32> {
   float part;  // s without the power
   int power;
   __device__ __forceinline__ explicit Logistic(float z) {
-    const float a = __builtin_fabsf(z) > 256.0f ? 256.0f : __builtin_fabsf(z);  // NaN stays
+    const bool far = __builtin_fabsf(z) > 256.0f;
+    const float a = far ? 256.0f : __builtin_fabsf(z);  // NaN stays
     const float n = __builtin_rintf(a * 1.44269504f);
     const float d = __builtin_fmaf(a, 1.925963033e-8f, __builtin_fmaf(a, 1.44269502f, -n));
     const float p = __builtin_amdgcn_exp2f(-d), e = __builtin_ldexpf(p, -(int)n);
@@ -112,7 +113,7 @@ struct Logistic<ZS_F32> {
     const bool left = z < 0.0f;
     s = left ? e * r : r;
     q = left ? r : e * r;
-    part = left ? p * r : r;
+    part = left ? far ? 0.0f : p * r : r;  // -infinity times 0 is the formula's NaN
     power = left ? -(int)n : 0;
   }
   __device__ __forceinline__ float times(float x) const { return __builtin_ldexpf(x * part, power); }

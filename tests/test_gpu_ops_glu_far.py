@@ -33,3 +33,14 @@ def test_silu_gradient_keeps_its_digits():
     R.close(dgu[:, :8192], slope, size * 24 * R.E + 4 * R.sub(torch.float32) * (1 + g.abs()), "slope")
     R.close(dgu[:, 8192:], f, f.abs() * 16 * R.E + 2 * R.sub(torch.float32), "act")
     R.close(again, f, f.abs() * 16 * R.E + 2 * R.sub(torch.float32), "out")
+
+
+@pytest.mark.parametrize("act", ["silu", "gelu"])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_infinite_gates(act, dtype):
+    """As the formula has it: infinity at infinity, and no value at -infinity."""
+    x = torch.tensor([[float("inf"), float("-inf"), float("nan"), -3e38, 3e38, -300.0, -256.0, 1, 1, 1, 1, 1, 1, 1]],
+                     dtype=dtype, device=DEV)
+    out = ops.glu(x, act=act, code=None)[0][0].cpu()
+    assert out[0] == float("inf") and torch.isnan(out[1:3]).all()
+    assert out[3] == 0 and out[4] == x[0, 4].cpu() and not out[5:].any()
