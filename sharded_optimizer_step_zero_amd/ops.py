@@ -224,9 +224,9 @@ def _overlap(a, b):
     if na > nb:
         pa, na, sa, wa, pb, nb, sb, wb = pb, nb, sb, wb, pa, na, sa, wa
     if na == 1:
-        at = torch.tensor([pa - pb])
+        at = torch.tensor([pa - pb], device="cpu")
     else:
-        at = torch.arange(na, dtype=torch.int64) * sa + (pa - pb)
+        at = torch.arange(na, dtype=torch.int64, device="cpu") * sa + (pa - pb)
     # of each row of a: the first of b's rows that ends behind its beginning
     row = torch.div(at - wb, sb, rounding_mode="floor").add_(1).clamp_(min=0)
     return bool(((row < nb) & (row * sb < at + wa)).any())

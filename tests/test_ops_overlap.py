@@ -1,6 +1,7 @@
 """Whether two views share memory, against sets of their bytes."""
 import random
 
+import pytest
 import torch
 
 from sharded_optimizer_step_zero_amd import ops
@@ -47,3 +48,14 @@ def test_halves_of_a_row_are_apart():
     assert not ops._overlap(both[:, :32], both[:, 32:])
     assert ops._overlap(both[:, :33], both[:, 32:])
     assert not ops._overlap(both[:2], both[2:]) and ops._overlap(both, both[4])
+
+
+def test_the_default_device_takes_no_part():
+    a = torch.zeros(40, 64)
+    was = torch.get_default_device()
+    try:
+        torch.set_default_device("meta")
+        assert not ops._overlap(a[:, :32], a[:, 32:]) and ops._overlap(a[:, :33], a[:, 32:])
+        assert ops._overlap(a, a[3]) and not ops._overlap(a[:, :8], a[3, 8:])
+    finally:
+        torch.set_default_device(was)
