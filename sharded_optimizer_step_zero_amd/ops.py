@@ -235,7 +235,7 @@ def _overlap(a, b):
 def _apart(out, name, allowed, others):
     """Refuses an output that overlaps an input; it may be one of `allowed` itself."""
     for t in allowed:
-        if t is not None and (t.data_ptr() != out.data_ptr() or t.stride() != out.stride()):
+        if t is not None and _extent(t) != _extent(out):
             others = (*others, t)
     for t in others:
         if t is not None and _overlap(out, t):

@@ -50,6 +50,16 @@ def test_halves_of_a_row_are_apart():
     assert not ops._overlap(both[:2], both[2:]) and ops._overlap(both, both[4])
 
 
+def test_one_row_is_itself_whatever_its_stride():
+    """A row's stride to a next one that is not there does not make it another buffer."""
+    a = torch.zeros(4, 64)
+    ops._apart(a[:1], "out", (a.view(2, 128)[:1, :64],), ())
+    ops._apart(a[:, :32], "out", (a[:, :32],), ())
+    for other in (a[:1, :63], a[:1, 1:], a[:2]):
+        with pytest.raises(ValueError, match="overlaps"):
+            ops._apart(a[:1], "out", (other,), ())
+
+
 def test_the_default_device_takes_no_part():
     a = torch.zeros(40, 64)
     was = torch.get_default_device()
