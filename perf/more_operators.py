@@ -230,6 +230,12 @@ def _e8m0(e):
     return (e + 127).to(torch.uint8).view(torch.float8_e8m0fnu)
 
 
+def _spans(e):
+    """Sixteen neighbours of a row together, the n-th of them at [n % 4, n // 4]; those behind the end are zeros."""
+    p = torch.nn.functional.pad(e, (0, -e.shape[1] % 16)).view(e.shape[0], -1, 4, 4)
+    return p.permute(1, 0, 3, 2).contiguous()
+
+
 def _four(v):
     """Rounded to the 4-bit format's values, ties to the even code."""
     a = v.abs()
@@ -244,7 +250,7 @@ def _packed(w):
     table = torch.tensor([0.0, 0.5, 1.0, 1.5, 2.0, 3.0, 4.0, 6.0], device=DEV)
     nibble = torch.bucketize(v.abs(), table) + torch.where(torch.signbit(v), 8, 0)
     nibble = nibble.to(torch.uint8).view(w.shape[0], -1, 2)
-    return (nibble[..., 0] | nibble[..., 1] << 4).view(torch.float4_e2m1fn_x2), _e8m0(e), w.shape[1]
+    return (nibble[..., 0] | nibble[..., 1] << 4).view(torch.float4_e2m1fn_x2), _e8m0(_spans(e)), w.shape[1]
 
 
 def _values(packed):
@@ -254,14 +260,15 @@ def _values(packed):
     table = torch.tensor([0.0, 0.5, 1.0, 1.5, 2.0, 3.0, 4.0, 6.0], device=DEV)
     table = torch.cat([table, -table])
     v = table[torch.stack([b & 15, b >> 4], -1).int()].view(b.shape[0], -1, 32)
-    return (v * torch.exp2(scales.view(torch.uint8).float() - 127).unsqueeze(-1)).view(b.shape[0], -1)[:, :width]
+    scales = torch.exp2(scales.view(torch.uint8).float() - 127).permute(1, 0, 3, 2).reshape(b.shape[0], -1)[:, :v.shape[1]]
+    return (v * scales.unsqueeze(-1)).view(b.shape[0], -1)[:, :width]
 
 
 def _quantised(x):
     """The fp32 values that a matrix has in the 4-bit form, along its rows, and the scales."""
     v, e = _scaled(x.float(), "e2m1", 32)
     back = (_four(v) * torch.exp2(e.float()).unsqueeze(-1)).view(x.shape[0], -1)[:, :x.shape[1]]
-    return back, _e8m0(e)
+    return back, _e8m0(_spans(e))
 
 
 def _plain(s):
@@ -311,7 +318,7 @@ def _plain(s):
             out.update(y=y.to(dt))
         if s["code"] != "none":
             v, e = _scaled(y, s["code"], s["group"])
-            out.update(scales=_e8m0(e))
+            out.update(scales=_e8m0(_spans(e) if s["code"] == "e2m1" else e))
             if s["code"] == "e2m1":
                 back = _four(v) * torch.exp2(e.double()).unsqueeze(-1)
                 out.update(values=back.view(s["tokens"], -1)[:, :s["width"]].to(torch.bfloat16))
@@ -404,7 +411,16 @@ def _exact_pack(y, code, group):
 
 def _exact_values(x):
     codes, scale = _exact_pack(x.double(), "e2m1", 32)
-    return codes * scale.repeat_interleave(32, 1)[:, :x.shape[1]], scale
+    return codes * scale.repeat_interleave(32, 1)[:, :x.shape[1]], _exact_spans(scale)
+
+
+def _exact_spans(scale):
+    """Scales in the order in which the 4-bit form holds them."""
+    rows, n = scale.shape
+    out = torch.ones(-(-n // 16), rows, 4, 4, dtype=torch.float64, device=DEV)
+    for g in range(n):
+        out[g // 16, :, g % 4, g // 4 % 4] = scale[:, g]
+    return out
 
 
 def _exact_unpacked(packed):
@@ -415,7 +431,10 @@ def _exact_unpacked(packed):
         low, high = nibble % 2, nibble // 2 % 4
         size = torch.where(high == 0, low * 0.5, (1 + 0.5 * low) * torch.exp2(high.double() - 1))
         out[:, at::2] = torch.where(nibble >= 8, -size, size)
-    return (out * torch.exp2(scales.view(torch.uint8).double() - 127).repeat_interleave(32, 1))[:, :width]
+    power = torch.exp2(scales.view(torch.uint8).double() - 127)
+    for g in range(-(-width // 32)):
+        out[:, 32 * g:32 * g + 32] *= power[g // 16, :, g % 4, g // 4 % 4, None]
+    return out[:, :width]
 
 
 def _times(a, b):
@@ -468,7 +487,7 @@ def exact(case, seed):
             out.update(y=y)
         if case["code"] != "none":
             codes, scale = _exact_pack(y, case["code"], case["group"])
-            out.update(scales=scale)
+            out.update(scales=_exact_spans(scale) if case["code"] == "e2m1" else scale)
             if case["code"] == "e2m1":
                 out.update(values=codes * scale.repeat_interleave(32, 1)[:, :d])
             else:
