@@ -10,6 +10,13 @@
  *               that keeps its input so and takes its gradient from it
  *   xent        softmax cross entropy of a linear head, in pieces of the
  *               vocabulary, without keeping the logits; its gradient
+ *   layer norm  with the residual's addition, its output in 16, 8 or 4 bits; its
+ *               gradient with the sums for the weight and the bias
+ *   mx4         matrices in 4 bits, packed along rows, columns or both, and the
+ *               product of two such matrices
+ *   prefer      a preference loss of pairs of packed sequences on the losses of
+ *               xent; its gradient, which is xent's grad_loss
+ *   grads       the gradient norm over many tensors, and clipping by it
  *
  * Conventions are those of zeroshard.h: the caller owns every device buffer and
  * the workspaces, calls enqueue kernels on `stream` and return, a negative return
@@ -29,6 +36,15 @@
  * times 2^-e rounded to nearest even.  The scaling is exact, so a code is off by
  * that one rounding only.  A group with a NaN or an infinity has scale byte 255
  * and codes 0, and reads back as NaN throughout.
+ *
+ * The 4-bit form (e2m1).  Groups have 32 elements, zeros behind a row's end, and 2^e is the
+ * least scale in the same range for which a group's largest magnitude is at most 6 * 2^e;
+ * codes are the elements times 2^-e rounded to 0, 0.5, 1, 1.5, 2, 3, 4 or 6, ties to even.
+ * A row has G = ceil(width / 32) groups: 16 * G bytes of codes (element 2i in the low half of
+ * byte i).  Scale bytes lie as the matrix instructions take them, sixteen groups of a
+ * row together: that of group n of row r at ((n / 16) * rows + r) * 16 + (n % 4) * 4 + n / 4 % 4,
+ * ceil(G / 16) * rows * 16 bytes in all; those of groups that do not exist are 127 (a scale
+ * of 1).  Codes and scales are 16-byte aligned.
  */
 #ifndef ZEROSHARD_OPS_H
 #define ZEROSHARD_OPS_H
@@ -47,6 +63,8 @@ extern "C" {
 /* 8-bit forms */
 #define ZS_E4M3 0
 #define ZS_E5M2 1
+/* the 4-bit form */
+#define ZS_E2M1 2
 /* gated units: act(g) * u */
 #define ZS_SILU 0
 #define ZS_GELU 1 /* the tanh form */
@@ -180,6 +198,134 @@ int zs_xent_backward(const void *hidden, int64_t hidden_stride, const void *weig
                      void *grad_weight, int64_t grad_weight_stride, int64_t tokens,
                      int64_t vocab, int64_t width, int32_t dtype, int32_t target_bytes,
                      void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * s = x + residual (rounded to `dtype`, stored in `sum`; without a residual s is x and `sum`
+ * must be NULL), mean and rstd = 1 / sqrt(mean((s - mean)^2) + eps) of each row in fp32, and
+ * y = (s - mean) * rstd * weight + bias (NULL: none): in `dtype` to y (NULL: not wanted), and in
+ * 8 bits (code ZS_E4M3 or ZS_E5M2, as zs_norm_forward) or in 4 (ZS_E2M1, group 32) to codes and
+ * scales (both NULL: not wanted).  sum may be x or residual itself.  Sizes as zs_norm_forward's.
+ */
+int zs_layer_norm_forward(const void *x, int64_t x_stride, const void *residual,
+                          int64_t residual_stride, const void *weight, const void *bias, void *sum,
+                          int64_t sum_stride, void *y, int64_t y_stride, void *codes, void *scales,
+                          float *mean, float *rstd, int64_t rows, int64_t width, float eps,
+                          int32_t dtype, int32_t code, int32_t group, void *stream);
+
+/* Workspace of zs_layer_norm_backward; 0 when a size is out of range. */
+size_t zs_layer_norm_backward_bytes(int64_t rows, int64_t width);
+
+/*
+ * With h = (s - mean) * rstd and g = weight*dy: grad_x = rstd * (g - mean(g) - h * mean(g*h)) +
+ * grad_sum (NULL: nothing to add), the gradient of x and of the residual alike; grad_weight =
+ * sum over rows of dy * h and grad_bias (NULL: not wanted) = sum of dy, in `weight_dtype`:
+ * `dtype` or ZS_F32.  Sums in fp32.  grad_x may be dy, sum or grad_sum itself.  Above 8192
+ * columns rows < 2^22.
+ */
+int zs_layer_norm_backward(const void *dy, int64_t dy_stride, const void *sum, int64_t sum_stride,
+                           const void *weight, const float *mean, const float *rstd,
+                           const void *grad_sum, int64_t grad_sum_stride, void *grad_x,
+                           int64_t grad_x_stride, void *grad_weight, void *grad_bias, int64_t rows,
+                           int64_t width, int32_t dtype, int32_t weight_dtype, void *workspace,
+                           size_t workspace_bytes, void *stream);
+
+/*
+ * x in the 4-bit form: along its rows to codes and scales, along its columns (the form of the
+ * transposed matrix, which has `width` rows of `rows` elements) to codes_t and scales_t;
+ * either pair may be NULL.  1 <= width <= 2^20, rows <= 2^24 (2^20 along columns), and fewer than
+ * 2^24 pieces of 4 rows x 512 (along columns 128 x 128), counting whole spans of 512.
+ */
+int zs_mx4_pack(const void *x, int64_t x_stride, void *codes, void *scales, void *codes_t,
+                void *scales_t, int64_t rows, int64_t width, int32_t dtype, void *stream);
+
+/* Back: each value rounded once to `dtype` (exact in bf16 and fp32). */
+int zs_mx4_unpack(const void *codes, const void *scales, void *x, int64_t x_stride, int64_t rows,
+                  int64_t width, int32_t dtype, void *stream);
+
+/*
+ * out[t][n] = sum_k x[t][k] * w[n][k] of two matrices in the 4-bit form with rows of `width`
+ * elements, summed in fp32 and rounded once to `dtype`.  (A linear layer's three products are
+ * this one: y from x and w packed along rows, dx from dy along rows and w along columns, dw from
+ * dy and x along columns.)  tokens and features <= 2^24, width <= 2^20, and fewer than 2^24 tiles.
+ */
+int zs_mx4_product(const void *x_codes, const void *x_scales, const void *w_codes,
+                   const void *w_scales, void *out, int64_t out_stride, int64_t tokens,
+                   int64_t features, int64_t width, int32_t dtype, void *stream);
+
+/* kinds of preference loss */
+#define ZS_SIGMOID 0
+#define ZS_HINGE 1
+#define ZS_SQUARED 2
+
+/* Workspace of zs_prefer_forward; 0 when a size is out of range. */
+size_t zs_prefer_workspace_bytes(int64_t tokens, int64_t pairs);
+
+/*
+ * The preference loss of pairs of sequences that lie one behind the other: sequence i is tokens
+ * offsets[i] to offsets[i + 1] - 1 (2 * pairs + 1 offsets that do not fall), pair p has
+ * sequence 2p as the chosen one and 2p + 1 as the rejected.  loss is the policy's -log p of
+ * each token and ref_loss the reference's (NULL: none); a token whose mask byte is 0 (mask NULL:
+ * none) does not count, whatever its losses hold.  With a = -sum(loss - ref_loss) of a sequence,
+ * or the mean over its tokens that count where `average`, rewards[2p], [2p+1] = beta * a,
+ * margins[p] = m = beta * (a_chosen - a_rejected) - margin, and pair_loss[p] =
+ *   ZS_SIGMOID  -(1 - smoothing) * log sigma(m) - smoothing * log sigma(-m)
+ *   ZS_HINGE    max(0, 1 - m)
+ *   ZS_SQUARED  (m - 1/2)^2 / beta^2
+ * lengths: the tokens that count in each sequence (a sequence of none has a = 0).  Sums in fp64.
+ * beta > 0, 0 <= smoothing <= 0.5 (ZS_SIGMOID only); tokens < 2^31, pairs <= 2^22.
+ */
+int zs_prefer_forward(const float *loss, const float *ref_loss, const void *offsets,
+                      const void *mask, float *pair_loss, float *rewards, float *margins,
+                      int32_t *lengths, int64_t tokens, int64_t pairs, float beta, float margin,
+                      float smoothing, int32_t kind, int32_t average, int32_t offset_bytes,
+                      void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * grad[t] = the derivative of sum_p grad_loss[p] * pair_loss[p] by loss[t], for every token: 0
+ * where it does not count or lies in no sequence.  margins and lengths are the forward's.
+ */
+int zs_prefer_backward(const float *margins, const int32_t *lengths, const void *offsets,
+                       const void *mask, const float *grad_loss, float *grad, int64_t tokens,
+                       int64_t pairs, float beta, float smoothing, int32_t kind, int32_t average,
+                       int32_t offset_bytes, void *stream);
+
+/*
+ * A gradient: `rows` rows of `width` adjacent elements of `dtype`, grad_stride elements apart,
+ * and where its clipped values go (NULL: nowhere; the gradient itself, with the same strides
+ * and type, is allowed).
+ */
+typedef struct zs_grad_tensor {
+  const void *grad;
+  void *out;
+  int64_t rows, width, grad_stride, out_stride;
+  int32_t dtype, out_dtype;
+} zs_grad_tensor;
+
+/* How many pieces a list of gradients makes (32 bytes of its table each), or a negative error. */
+int64_t zs_grads_pieces(const zs_grad_tensor *list, int64_t n);
+
+/*
+ * Fills a list's table, in host memory; the calls below read a copy of it in device memory,
+ * 256-byte aligned.  It holds addresses: it is laid out anew when a buffer moves.  An
+ * output must not overlap another buffer of the list (its own gradient excepted).
+ */
+int zs_grads_table(const zs_grad_tensor *list, int64_t n, void *table, size_t table_bytes);
+
+/* Workspace of zs_grads_sumsq; 0 when a size is out of range. */
+size_t zs_grads_workspace_bytes(int64_t pieces);
+
+/* *sumsq (device) = the sum of the squares of all elements of the list, in fp64. */
+int zs_grads_sumsq(const void *table, int64_t pieces, double *sumsq, void *workspace,
+                   size_t workspace_bytes, void *stream);
+
+/*
+ * With the device double *sumsq (of this list, or summed over the ranks): norm = sqrt(*sumsq),
+ * out = c * grad with c = min(1, max_norm / (norm + 1e-6)) in fp32, rounded once to the
+ * output's type; *norm_out (device, may be NULL) = norm.  Every gradient of the list has an
+ * output.  One that is its own output is left alone where c is 1.
+ */
+int zs_grads_clip(const void *table, int64_t pieces, float max_norm, const double *sumsq,
+                  double *norm_out, void *stream);
 
 #ifdef __cplusplus
 }

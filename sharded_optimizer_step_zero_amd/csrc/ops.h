@@ -138,14 +138,15 @@ __device__ __forceinline__ void store8(elem_t<DT>* p, int64_t n, f32x8 x) {
 
 // ---------------------------------------------------------------- 8-bit form
 
-// The scale byte of a group with this largest magnitude.  1.75 * 2^top is the
-// format's largest value: a mantissa above .75 goes to the next power of two.
+// The scale byte of a group with this largest magnitude.  1.75 * 2^top (4 bits: 1.5 * 2^2) is
+// the format's largest value: a mantissa above .75 (.5) goes to the next power of two.
 template <int CODE>
 __device__ __forceinline__ uint32_t scale_byte(float amax) {
-  constexpr int top = CODE == ZS_E4M3 ? 8 : 15;
+  constexpr int top = CODE == ZS_E4M3 ? 8 : CODE == ZS_E5M2 ? 15 : 2;
+  constexpr uint32_t over = CODE == ZS_E2M1 ? 0x3fffffu : 0x1fffffu;
   const uint32_t b = __float_as_uint(amax);
   if (b >= 0x7f800000u) return 255u;
-  const int e = (int)((b + 0x1fffffu) >> 23) - top;  // biased by 127
+  const int e = (int)((b + over) >> 23) - top;  // biased by 127
   return (uint32_t)(e < 0 ? 0 : e);
 }
 // 2^-e of a scale byte that is not 255 (byte 0: 2^127), and 2^e (255: NaN).
@@ -193,6 +194,34 @@ __device__ __forceinline__ f32x8 decode8(u32x2 w) {
     r[4 * h + 3] = b[1];
   }
   return r;
+}
+
+// Eight 4-bit codes (the first in the lowest bits) of x / scale, scale a power of two.
+__device__ __forceinline__ uint32_t encode4(f32x8 x, float scale) {
+  int w = 0;
+  w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, x[0], x[1], scale, 0);
+  w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, x[2], x[3], scale, 1);
+  w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, x[4], x[5], scale, 2);
+  w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, x[6], x[7], scale, 3);
+  return (uint32_t)w;
+}
+// Their values times scale.
+__device__ __forceinline__ f32x8 decode4(uint32_t w, float scale) {
+  f32x8 r;
+  const f32x2 a = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, scale, 0);
+  const f32x2 b = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, scale, 1);
+  const f32x2 c = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, scale, 2);
+  const f32x2 d = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, scale, 3);
+  r[0] = a[0]; r[1] = a[1]; r[2] = b[0]; r[3] = b[1];
+  r[4] = c[0]; r[5] = c[1]; r[6] = d[0]; r[7] = d[1];
+  return r;
+}
+
+// Where the scale byte of a row's group of 32 lies: sixteen groups of a row together, in the
+// order in which the lanes of a matrix instruction take them (a lane has one 32-bit word, whose
+// bytes serve four instructions).
+__host__ __device__ __forceinline__ int64_t scale4_at(int64_t row, int64_t group, int64_t rows) {
+  return ((group >> 4) * rows + row) * 16 + (group & 3) * 4 + ((group >> 2) & 3);
 }
 
 // Eight codes at p, n of them exist.

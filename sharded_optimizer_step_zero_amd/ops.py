@@ -1,9 +1,11 @@
 """Model operators that make the gradient contributions a ZeRO shard step reads.
 
-Four operators on torch tensors, run by the HIP kernels of libzeroshard.so: the
+Operators on torch tensors, run by the HIP kernels of libzeroshard.so: the
 token embedding, the root-mean-square norm with the residual's addition and an
-8-bit output, activations held in 8 bits (alone and under a gated unit), and the
-softmax cross entropy of a linear head.  Every C entry point of
+8-bit output, the layer norm with an output in 16, 8 or 4 bits, activations held
+in 8 bits (alone and under a gated unit), matrices in 4 bits and their product, the
+softmax cross entropy of a linear head, the preference loss on its tokens' losses, and
+the clipping of many tensors by their global norm.  Every C entry point of
 include/zeroshard_ops.h is exposed under the same name; the functions on tensors
 below check what the kernels will stream over, allocate outputs and workspace
 with torch, and enqueue on torch's current stream of the tensors' device.
@@ -19,7 +21,8 @@ could not read or write so are refused with ValueError before anything is enqueu
 
 The 8-bit form: codes as torch.float8_e4m3fn or torch.float8_e5m2, and one
 power-of-two scale (torch.float8_e8m0fnu) for each group of 32, 64 or 128
-neighbouring elements; the value is code * scale.
+neighbouring elements; the value is code * scale.  The 4-bit form (Codes4) has
+groups of 32.
 """
 from __future__ import annotations
 
@@ -31,8 +34,19 @@ import torch
 from . import _check, _f32, _i32, _i64, _sig, _sz, _vp
 
 ZS_F32, ZS_BF16, ZS_F16 = 0, 1, 2
-ZS_E4M3, ZS_E5M2 = 0, 1
+ZS_E4M3, ZS_E5M2, ZS_E2M1 = 0, 1, 2
 ZS_SILU, ZS_GELU = 0, 1
+ZS_SIGMOID, ZS_HINGE, ZS_SQUARED = 0, 1, 2
+
+
+
+class GradTensor(ctypes.Structure):
+    """zs_grad_tensor."""
+    _fields_ = [("grad", ctypes.c_void_p), ("out", ctypes.c_void_p), ("rows", ctypes.c_int64),
+                ("width", ctypes.c_int64), ("grad_stride", ctypes.c_int64),
+                ("out_stride", ctypes.c_int64), ("dtype", ctypes.c_int32),
+                ("out_dtype", ctypes.c_int32)]
+
 
 _INT = ctypes.c_int
 _embed_forward = _sig("zs_embed_forward", _INT, _vp, _i64, _vp, _vp, _i64, _i64, _i64, _i64, _i64,
@@ -58,11 +72,35 @@ _xent_forward = _sig("zs_xent_forward", _INT, _vp, _i64, _vp, _i64, _vp, _vp, _v
                      _i64, _i32, _i32, _vp, _sz, _vp)
 _xent_backward = _sig("zs_xent_backward", _INT, _vp, _i64, _vp, _i64, _vp, _vp, _vp, _vp, _i64,
                       _vp, _i64, _i64, _i64, _i64, _i32, _i32, _vp, _sz, _vp)
+_layer_norm_forward = _sig("zs_layer_norm_forward", _INT, _vp, _i64, _vp, _i64, _vp, _vp, _vp,
+                           _i64, _vp, _i64, _vp, _vp, _vp, _vp, _i64, _i64, _f32, _i32, _i32,
+                           _i32, _vp)
+_layer_norm_backward_bytes = _sig("zs_layer_norm_backward_bytes", _sz, _i64, _i64)
+_layer_norm_backward = _sig("zs_layer_norm_backward", _INT, _vp, _i64, _vp, _i64, _vp, _vp, _vp,
+                            _vp, _i64, _vp, _i64, _vp, _vp, _i64, _i64, _i32, _i32, _vp, _sz, _vp)
+_mx4_pack = _sig("zs_mx4_pack", _INT, _vp, _i64, _vp, _vp, _vp, _vp, _i64, _i64, _i32, _vp)
+_mx4_unpack = _sig("zs_mx4_unpack", _INT, _vp, _vp, _vp, _i64, _i64, _i64, _i32, _vp)
+_mx4_product = _sig("zs_mx4_product", _INT, _vp, _vp, _vp, _vp, _vp, _i64, _i64, _i64, _i64, _i32,
+                    _vp)
+_prefer_workspace_bytes = _sig("zs_prefer_workspace_bytes", _sz, _i64, _i64)
+_prefer_forward = _sig("zs_prefer_forward", _INT, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i64,
+                       _i64, _f32, _f32, _f32, _i32, _i32, _i32, _vp, _sz, _vp)
+_prefer_backward = _sig("zs_prefer_backward", _INT, _vp, _vp, _vp, _vp, _vp, _vp, _i64, _i64,
+                        _f32, _f32, _i32, _i32, _i32, _vp)
+_grads_pieces = _sig("zs_grads_pieces", _i64, _vp, _i64)
+_grads_table = _sig("zs_grads_table", _INT, _vp, _i64, _vp, _sz)
+_grads_workspace_bytes = _sig("zs_grads_workspace_bytes", _sz, _i64)
+_grads_sumsq = _sig("zs_grads_sumsq", _INT, _vp, _i64, _vp, _vp, _sz, _vp)
+_grads_clip = _sig("zs_grads_clip", _INT, _vp, _i64, _f32, _vp, _vp, _vp)
 
 EXPORTED = ["zs_embed_forward", "zs_embed_backward_bytes", "zs_embed_backward", "zs_norm_forward",
             "zs_norm_backward_bytes", "zs_norm_backward", "zs_act8_pack", "zs_act8_unpack",
             "zs_glu_forward", "zs_glu_backward", "zs_xent_workspace_bytes", "zs_xent_forward",
-            "zs_xent_backward"]
+            "zs_xent_backward", "zs_layer_norm_forward", "zs_layer_norm_backward_bytes",
+            "zs_layer_norm_backward", "zs_mx4_pack", "zs_mx4_unpack", "zs_mx4_product",
+            "zs_prefer_workspace_bytes", "zs_prefer_forward", "zs_prefer_backward",
+            "zs_grads_pieces", "zs_grads_table", "zs_grads_workspace_bytes", "zs_grads_sumsq",
+            "zs_grads_clip"]
 
 
 # The C entry points under their names: arguments as in zeroshard_ops.h, device
@@ -121,6 +159,67 @@ def zs_xent_backward(*args) -> None:
     _check(_xent_backward(*args))
 
 
+def zs_layer_norm_forward(*args) -> None:
+    _check(_layer_norm_forward(*args))
+
+
+def zs_layer_norm_backward_bytes(rows: int, width: int) -> int:
+    return int(_layer_norm_backward_bytes(rows, width))
+
+
+def zs_layer_norm_backward(*args) -> None:
+    _check(_layer_norm_backward(*args))
+
+
+def zs_mx4_pack(*args) -> None:
+    _check(_mx4_pack(*args))
+
+
+def zs_mx4_unpack(*args) -> None:
+    _check(_mx4_unpack(*args))
+
+
+def zs_mx4_product(*args) -> None:
+    _check(_mx4_product(*args))
+
+
+def zs_prefer_workspace_bytes(tokens: int, pairs: int) -> int:
+    return int(_prefer_workspace_bytes(tokens, pairs))
+
+
+def zs_prefer_forward(*args) -> None:
+    _check(_prefer_forward(*args))
+
+
+def zs_prefer_backward(*args) -> None:
+    _check(_prefer_backward(*args))
+
+
+def _grad_array(tensors):
+    return (GradTensor * max(1, len(tensors)))(*tensors)
+
+
+def zs_grads_pieces(tensors) -> int:
+    """tensors: GradTensor records."""
+    return int(_check(_grads_pieces(_grad_array(tensors), len(tensors))))
+
+
+def zs_grads_table(tensors, table: int, table_bytes: int) -> None:
+    _check(_grads_table(_grad_array(tensors), len(tensors), table, table_bytes))
+
+
+def zs_grads_workspace_bytes(pieces: int) -> int:
+    return int(_grads_workspace_bytes(pieces))
+
+
+def zs_grads_sumsq(*args) -> None:
+    _check(_grads_sumsq(*args))
+
+
+def zs_grads_clip(*args) -> None:
+    _check(_grads_clip(*args))
+
+
 # ---------------------------------------------------------------- checks
 
 _DTYPES = {torch.float32: ZS_F32, torch.bfloat16: ZS_BF16, torch.float16: ZS_F16}
@@ -128,6 +227,8 @@ _HALVES = {torch.bfloat16: ZS_BF16, torch.float16: ZS_F16}
 _CODES = {"e4m3": (ZS_E4M3, torch.float8_e4m3fn), "e5m2": (ZS_E5M2, torch.float8_e5m2)}
 _CODE_OF = {torch.float8_e4m3fn: ZS_E4M3, torch.float8_e5m2: ZS_E5M2}
 _SCALE = torch.float8_e8m0fnu
+_FOUR = torch.float4_e2m1fn_x2
+_KINDS = {"sigmoid": ZS_SIGMOID, "hinge": ZS_HINGE, "squared": ZS_SQUARED}
 _ACTS = {"silu": ZS_SILU, "gelu": ZS_GELU}
 _ID_BYTES = {torch.int64: 8, torch.int32: 4}
 
@@ -582,3 +683,398 @@ def linear_xent_backward(hidden, weight, targets, lse, grad_loss, out=None, weig
          grad_loss.data_ptr(), gh.data_ptr() if want_hidden else None, ghs, gw.data_ptr() if
          want_weight else None, gws, tokens, vocab, width, dt, nb, ws.data_ptr(), ws.numel())
     return gh, gw
+
+
+# ---------------------------------------------------------------- layer norm
+
+
+class LayerNormOut(NamedTuple):
+    """What layer_norm returns; the fields that were not asked for are None (sum without a
+    residual is x itself)."""
+    y: Optional[torch.Tensor]
+    sum: torch.Tensor
+    mean: torch.Tensor
+    rstd: torch.Tensor
+    codes: Optional[torch.Tensor]
+    scales: Optional[torch.Tensor]
+
+
+def layer_norm(x, weight, bias=None, residual=None, eps=1e-5, code=None, group=None, want_y=True):
+    """y = (s - mean(s)) / sqrt(mean((s - mean(s))^2) + eps) * weight + bias with s = x +
+    residual, row by row.  y in x's dtype where want_y; (codes, scales) in 8 bits where code is
+    "e4m3" or "e5m2" (groups of 128 unless group says 32 or 64), in the 4-bit form where it is
+    "e2m1": Codes4(codes, scales, width) is an operand of linear4.  mean and rstd [rows] and s
+    are what layer_norm_backward reads."""
+    xs = _matrix(x, "x")
+    dev = x.device
+    dt = _dtype(x, "x")
+    rows, width = x.shape
+    _vector(weight, "weight", (x.dtype,), dev, width)
+    if bias is not None:
+        _vector(bias, "bias", (x.dtype,), dev, width)
+    s, rs, ss = x, 0, 0
+    if residual is not None:
+        rs = _matrix(residual, "residual", x.dtype, dev, rows, width)
+        s = torch.empty(rows, width, dtype=x.dtype, device=dev)
+        ss = width
+    y = torch.empty(rows, width, dtype=x.dtype, device=dev) if want_y else None
+    stats = torch.empty(2, rows, dtype=torch.float32, device=dev)
+    mean, rstd = stats.unbind()
+    codes = scales = None
+    cd = 0
+    if code == "e2m1":
+        cd = ZS_E2M1
+        if group not in (None, 32):
+            raise ValueError(f"group: {group!r}, the 4-bit form has groups of 32")
+        group = 32
+        codes, scales = _empty4(rows, width, dev)
+    elif code is not None:
+        cd, ct = _pick(_CODES, code, "code")
+        group = _group(128 if group is None else group)
+        codes = torch.empty(rows, width, dtype=ct, device=dev)
+        scales = torch.empty(rows, -(-width // group), dtype=_SCALE, device=dev)
+    if rows:
+        _run(dev, _layer_norm_forward, x.data_ptr(), xs, residual.data_ptr() if residual is not None
+             else None, rs, weight.data_ptr(), bias.data_ptr() if bias is not None else None,
+             s.data_ptr() if residual is not None else None, ss, y.data_ptr() if want_y else None,
+             width, codes.data_ptr() if code is not None else None, scales.data_ptr() if code is not
+             None else None, mean.data_ptr(), rstd.data_ptr(), rows, width, eps, dt, cd, group or 32)
+    return LayerNormOut(y, s, mean, rstd, codes, scales)
+
+
+def layer_norm_backward(grad_y, sum, weight, mean, rstd, grad_sum=None, out=None,
+                        weight_grad_out=None, bias_grad_out=None, weight_grad_dtype=None,
+                        want_bias=True, workspace=None):
+    """(grad_x, grad_weight, grad_bias) of layer_norm: grad_x is the gradient of x and of the
+    residual alike, with grad_sum (the gradient that reaches s by the residual path) added.
+    grad_weight and grad_bias have one dtype, the weight's, or fp32 with
+    weight_grad_dtype=torch.float32; grad_bias is None without want_bias.  out may be grad_y,
+    sum or grad_sum itself."""
+    gs = _matrix(grad_y, "grad_y")
+    dev = grad_y.device
+    dt = _dtype(grad_y, "grad_y")
+    rows, width = grad_y.shape
+    ss = _matrix(sum, "sum", grad_y.dtype, dev, rows, width)
+    _vector(weight, "weight", (grad_y.dtype,), dev, width)
+    _vector(mean, "mean", (torch.float32,), dev, rows)
+    _vector(rstd, "rstd", (torch.float32,), dev, rows)
+    ds = 0
+    if grad_sum is not None:
+        ds = _matrix(grad_sum, "grad_sum", grad_y.dtype, dev, rows, width)
+    inputs = (weight, mean, rstd)
+    if out is None:
+        out = torch.empty(rows, width, dtype=grad_y.dtype, device=dev)
+        os_ = width
+    else:
+        os_ = _matrix(out, "out", grad_y.dtype, dev, rows, width)
+        _apart(out, "out", (grad_y, sum, grad_sum), inputs)
+    given = weight_grad_out if weight_grad_out is not None else bias_grad_out if want_bias else None
+    wdt = weight_grad_dtype or (given.dtype if given is not None else grad_y.dtype)
+    if wdt not in (grad_y.dtype, torch.float32):
+        raise ValueError(f"weight_grad_dtype: {wdt}, expected {grad_y.dtype} or torch.float32")
+    if weight_grad_out is None:
+        weight_grad_out = torch.empty(width, dtype=wdt, device=dev)
+    else:
+        _vector(weight_grad_out, "weight_grad_out", (wdt,), dev, width)
+        _apart(weight_grad_out, "weight_grad_out", (), (*inputs, grad_y, sum, grad_sum, out))
+    if not want_bias:
+        if bias_grad_out is not None:
+            raise ValueError("bias_grad_out: goes with want_bias")
+    elif bias_grad_out is None:
+        bias_grad_out = torch.empty(width, dtype=wdt, device=dev)
+    else:
+        _vector(bias_grad_out, "bias_grad_out", (wdt,), dev, width)
+        _apart(bias_grad_out, "bias_grad_out", (),
+               (*inputs, grad_y, sum, grad_sum, out, weight_grad_out))
+    ws = _workspace(workspace, _layer_norm_backward_bytes(rows, width), dev)
+    _run(dev, _layer_norm_backward, grad_y.data_ptr(), gs, sum.data_ptr(), ss, weight.data_ptr(),
+         mean.data_ptr(), rstd.data_ptr(), grad_sum.data_ptr() if ds else None, ds, out.data_ptr(),
+         os_, weight_grad_out.data_ptr(), bias_grad_out.data_ptr() if want_bias else None, rows,
+         width, dt, _DTYPES[wdt], ws.data_ptr(), ws.numel())
+    return out, weight_grad_out, bias_grad_out
+
+
+# ---------------------------------------------------------------- 4-bit form
+
+
+class Codes4(NamedTuple):
+    """A matrix [rows, width] in the 4-bit form: codes [rows, 16 * G] (torch.float4_e2m1fn_x2, two
+    elements a byte, the even one low; G = ceil(width / 32) groups, zeros behind the row's end)
+    and scales [ceil(G / 16), rows, 4, 4] (torch.float8_e8m0fnu), that of a row's group n at
+    [n // 16, row, n % 4, n // 4 % 4], as the matrix instructions take them; those of groups
+    that do not exist are 1."""
+    codes: torch.Tensor
+    scales: torch.Tensor
+    width: int
+
+
+def _empty4(rows, width, device):
+    groups = -(-width // 32)
+    return (torch.empty(rows, 16 * groups, dtype=_FOUR, device=device),
+            torch.empty(-(-groups // 16), rows, 4, 4, dtype=_SCALE, device=device))
+
+
+def _codes4(c, name, device=None, width=None):
+    """The rows of a matrix in the 4-bit form, which must lie as pack4 wrote it."""
+    if not isinstance(c, Codes4):
+        raise ValueError(f"{name}: {type(c).__name__}, expected Codes4")
+    codes, scales, w = c
+    if codes.dim() != 2 or not codes.is_cuda or (device is not None and codes.device != device):
+        raise ValueError(f"{name}: codes of {codes.dim()} dimensions on {codes.device}, expected 2 "
+                         f"on {device or 'a GPU'}")
+    if width is not None and w != width:
+        raise ValueError(f"{name}: width {w}, expected {width}")
+    rows, groups = codes.shape[0], -(-w // 32)
+    if codes.dtype != _FOUR or codes.shape[1] != 16 * groups or not codes.is_contiguous():
+        raise ValueError(f"{name}: codes {codes.dtype} {tuple(codes.shape)}, expected {_FOUR} "
+                         f"({rows}, {16 * groups}), contiguous")
+    want = (-(-groups // 16), rows, 4, 4)
+    if (scales.dtype != _SCALE or scales.device != codes.device or tuple(scales.shape) != want
+            or not scales.is_contiguous()):
+        raise ValueError(f"{name}: scales {scales.dtype} {tuple(scales.shape)} on {scales.device}, "
+                         f"expected {_SCALE} {want} on {codes.device}, contiguous")
+    return rows
+
+
+def pack4(x, want="rows"):
+    """A matrix in the 4-bit form: with want="rows" the Codes4 of x, with "columns" that of x.T
+    (groups along x's columns), with "both" the two of them, from one pass over x."""
+    xs = _matrix(x, "x")
+    dev = x.device
+    dt = _dtype(x, "x")
+    if want not in ("rows", "columns", "both"):
+        raise ValueError(f"want: {want!r}, expected one of ('rows', 'columns', 'both')")
+    rows, width = x.shape
+    a = b = None
+    if want != "columns":
+        a = Codes4(*_empty4(rows, width, dev), width)
+    if want != "rows":
+        b = Codes4(*_empty4(width, rows, dev), rows)
+    if rows and width:
+        _run(dev, _mx4_pack, x.data_ptr(), xs, a.codes.data_ptr() if a else None,
+             a.scales.data_ptr() if a else None, b.codes.data_ptr() if b else None,
+             b.scales.data_ptr() if b else None, rows, width, dt)
+    return a if want == "rows" else b if want == "columns" else (a, b)
+
+
+def unpack4(c, dtype, out=None):
+    """The values of a matrix in the 4-bit form, each rounded once to dtype (exact in bf16 and
+    fp32)."""
+    dt = _pick(_DTYPES, dtype, "dtype")
+    rows = _codes4(c, "c")
+    dev = c.codes.device
+    if out is None:
+        out = torch.empty(rows, c.width, dtype=dtype, device=dev)
+        stride = c.width
+    else:
+        stride = _matrix(out, "out", dtype, dev, rows, c.width)
+        _apart(out, "out", (), (c.codes, c.scales))
+    if rows and c.width:
+        _run(dev, _mx4_unpack, c.codes.data_ptr(), c.scales.data_ptr(), out.data_ptr(), stride, rows,
+             c.width, dt)
+    return out
+
+
+def linear4(x, weight, dtype=None, out=None):
+    """x @ weight.T for a weight in the 4-bit form (Codes4), summed in fp32 and rounded once to
+    dtype.  x: a matrix, which is packed along its rows first (dtype: its own unless given), or
+    Codes4 already (dtype: bf16 unless given).  With pack4's other orientations the same product
+    gives the gradients: dx = linear4(dy, pack4(w, "columns")), dw = linear4(pack4(dy,
+    "columns"), pack4(x, "columns"))."""
+    if isinstance(x, torch.Tensor):
+        dtype = dtype or (out.dtype if out is not None else x.dtype)
+        if x.dim() != 2 or x.shape[1] != getattr(weight, "width", None):
+            raise ValueError(f"x: shape {tuple(x.shape)}, expected (any, "
+                             f"{getattr(weight, 'width', 'width')}) and a Codes4 weight")
+        x = pack4(x)
+    tokens = _codes4(x, "x")
+    dev = x.codes.device
+    features = _codes4(weight, "weight", dev, x.width)
+    dtype = dtype or (out.dtype if out is not None else torch.bfloat16)
+    dt = _pick(_DTYPES, dtype, "dtype")
+    if out is None:
+        out = torch.empty(tokens, features, dtype=dtype, device=dev)
+        stride = features
+    else:
+        stride = _matrix(out, "out", dtype, dev, tokens, features)
+        _apart(out, "out", (), (x.codes, x.scales, weight.codes, weight.scales))
+    if x.width == 0:
+        return out.zero_()
+    _run(dev, _mx4_product, x.codes.data_ptr(), x.scales.data_ptr(), weight.codes.data_ptr(),
+         weight.scales.data_ptr(), out.data_ptr(), stride, tokens, features, x.width, dt)
+    return out
+
+
+# ---------------------------------------------------------------- preference loss
+
+
+class PreferenceOut(NamedTuple):
+    """What preference_loss returns, for P pairs: loss [P], rewards [P, 2] (beta times the
+    sequences' log ratios, the chosen one's first), margins [P] and lengths [P, 2] (the tokens
+    that count, int32)."""
+    loss: torch.Tensor
+    rewards: torch.Tensor
+    margins: torch.Tensor
+    lengths: torch.Tensor
+
+
+def _pairs(offsets, mask, device, tokens):
+    if offsets.dim() != 1 or offsets.shape[0] % 2 == 0:
+        raise ValueError(f"offsets: shape {tuple(offsets.shape)}, expected (2 * pairs + 1,)")
+    _vector(offsets, "offsets", _ID_BYTES, device, offsets.shape[0])
+    if mask is not None:
+        _vector(mask, "mask", (torch.bool, torch.uint8), device, tokens)
+    return offsets.shape[0] // 2
+
+
+def preference_loss(loss, ref_loss, offsets, beta=0.1, kind="sigmoid", margin=0.0, smoothing=0.0,
+                    average=False, mask=None, workspace=None):
+    """The preference loss of pairs of packed sequences: loss and ref_loss (None: no reference)
+    are the policy's and the reference's -log p of each token (linear_xent's), fp32 [tokens];
+    sequence i is tokens offsets[i]:offsets[i + 1], pair p has 2p as the chosen and 2p + 1
+    as the rejected one.  With each sequence's log ratio a = -sum(loss - ref_loss), or its
+    mean over the tokens that count with average=True, m = beta * (a_chosen - a_rejected) -
+    margin and the loss is -log sigma(m) ("sigmoid", with smoothing s (1 - s) times that and s
+    times the same of -m), max(0, 1 - m) ("hinge") or (m - 1/2)^2 / beta^2 ("squared").  mask:
+    True where a token counts; what loss and ref_loss hold elsewhere is not used."""
+    tokens = loss.shape[0] if loss.dim() == 1 else -1
+    dev = loss.device
+    if not loss.is_cuda:
+        raise ValueError(f"loss: on {dev}, expected a GPU")
+    _vector(loss, "loss", (torch.float32,), dev, tokens)
+    if ref_loss is not None:
+        _vector(ref_loss, "ref_loss", (torch.float32,), dev, tokens)
+    k = _pick(_KINDS, kind, "kind")
+    pairs = _pairs(offsets, mask, dev, tokens)
+    each = torch.empty(2, pairs, dtype=torch.float32, device=dev)
+    rewards = torch.empty(pairs, 2, dtype=torch.float32, device=dev)
+    lengths = torch.empty(pairs, 2, dtype=torch.int32, device=dev)
+    out, margins = each.unbind()
+    ws = _workspace(workspace, _prefer_workspace_bytes(tokens, pairs), dev)
+    _run(dev, _prefer_forward, loss.data_ptr(), ref_loss.data_ptr() if ref_loss is not None else
+         None, offsets.data_ptr(), mask.data_ptr() if mask is not None else None, out.data_ptr(),
+         rewards.data_ptr(), margins.data_ptr(), lengths.data_ptr(), tokens, pairs, beta, margin,
+         smoothing, k, int(average), _ID_BYTES[offsets.dtype], ws.data_ptr(), ws.numel())
+    return PreferenceOut(out, rewards, margins, lengths)
+
+
+def preference_loss_backward(forward, offsets, grad_loss, tokens, beta=0.1, kind="sigmoid",
+                             smoothing=0.0, average=False, mask=None, out=None):
+    """The gradient of sum(grad_loss * preference_loss(...).loss) by each token's loss, fp32
+    [tokens]: linear_xent_backward's grad_loss.  forward is what preference_loss returned for
+    the same offsets, mask and settings; tokens that do not count or lie in no sequence get 0."""
+    dev = offsets.device
+    if not offsets.is_cuda:
+        raise ValueError(f"offsets: on {dev}, expected a GPU")
+    k = _pick(_KINDS, kind, "kind")
+    pairs = _pairs(offsets, mask, dev, tokens)
+    _vector(forward.margins, "margins", (torch.float32,), dev, pairs)
+    lengths = forward.lengths
+    if (tuple(lengths.shape) != (pairs, 2) or lengths.dtype != torch.int32 or lengths.device != dev
+            or not lengths.is_contiguous()):
+        raise ValueError(f"lengths: {lengths.dtype} {tuple(lengths.shape)} on {lengths.device}, "
+                         f"expected torch.int32 ({pairs}, 2) on {dev}, contiguous")
+    _vector(grad_loss, "grad_loss", (torch.float32,), dev, pairs)
+    if out is None:
+        out = torch.empty(tokens, dtype=torch.float32, device=dev)
+    else:
+        _vector(out, "out", (torch.float32,), dev, tokens)
+        _apart(out, "out", (), (forward.margins, lengths, offsets, mask, grad_loss))
+    _run(dev, _prefer_backward, forward.margins.data_ptr(), lengths.data_ptr(), offsets.data_ptr(),
+         mask.data_ptr() if mask is not None else None, grad_loss.data_ptr(), out.data_ptr(),
+         tokens, pairs, beta, smoothing, k, int(average), _ID_BYTES[offsets.dtype])
+    return out
+
+
+# ---------------------------------------------------------------- many gradients
+
+
+def _grad_rows(g, o, i):
+    """A gradient and its output as rows of adjacent elements: (rows, width, strides)."""
+    if g.is_contiguous() and o.is_contiguous():
+        return 1, g.numel(), g.numel(), o.numel()
+    for t, name in ((g, f"tensors[{i}]"), (o, f"out[{i}]")):
+        if t.dim() != 2 or (t.stride(1) != 1 and t.shape[1] > 1) or (
+                t.stride(0) < t.shape[1] and t.shape[0] > 1):
+            raise ValueError(f"{name}: shape {tuple(t.shape)}, strides {t.stride()}: expected "
+                             "contiguous, or a matrix (or its transpose) with adjacent elements "
+                             "in a row")
+    return (*g.shape, g.stride(0), o.stride(0))
+
+
+class GradList:
+    """Gradients of any types in many tensors, laid out once for grad_sumsq and clip_grads.
+
+    tensors: contiguous ones, and matrices (or their transposes) with any row stride.  out: where
+    their clipped values go, tensors of the same shapes and orientation in any of the types
+    (views of a contribution buffer of ZeroShard); without it they are clipped in place.  The
+    list holds its tensors and their addresses: a tensor must not be resized or given other
+    memory.  Making it copies a table to the device and is not captured in a graph; the calls
+    that use it are."""
+
+    def __init__(self, tensors, out=None):
+        self.tensors = list(tensors)
+        self.out = list(out) if out is not None else None
+        if not self.tensors:
+            raise ValueError("tensors: an empty list")
+        if self.out is not None and len(self.out) != len(self.tensors):
+            raise ValueError(f"out: {len(self.out)} tensors, expected {len(self.tensors)}")
+        self.device = self.tensors[0].device
+        if not self.tensors[0].is_cuda:
+            raise ValueError(f"tensors: on {self.device}, expected a GPU")
+        records = []
+        for i, g in enumerate(self.tensors):
+            o = self.out[i] if self.out is not None else g
+            for t, name in ((g, f"tensors[{i}]"), (o, f"out[{i}]")):
+                if t.device != self.device:
+                    raise ValueError(f"{name}: on {t.device}, expected {self.device}")
+                _dtype(t, name)
+            if o.shape != g.shape:
+                raise ValueError(f"out[{i}]: shape {tuple(o.shape)}, expected {tuple(g.shape)}")
+            dg, do = _DTYPES[g.dtype], _DTYPES[o.dtype]
+            if g.dim() == 2 and not g.is_contiguous() and g.stride(0) == 1 and o.stride(0) == 1:
+                g, o = g.t(), o.t()
+            rows, width, gs, os_ = _grad_rows(g, o, i)
+            records.append(GradTensor(g.data_ptr(), o.data_ptr(), rows, width, gs, os_, dg, do))
+        self.pieces = zs_grads_pieces(records)
+        host = torch.empty(max(1, self.pieces) * 32, dtype=torch.uint8, device="cpu")
+        zs_grads_table(records, host.data_ptr(), host.numel())
+        self.table = host.to(self.device)
+
+
+def _grad_list(grads):
+    return grads if isinstance(grads, GradList) else GradList(grads)
+
+
+def grad_sumsq(grads, out=None, workspace=None):
+    """The sum of the squares of all elements of the tensors, a float64 scalar tensor (out=: one
+    that is given).  grads: a GradList, or tensors.  Over several ranks it is summed by the
+    caller before clip_grads."""
+    grads = _grad_list(grads)
+    dev = grads.device
+    if out is None:
+        out = torch.empty((), dtype=torch.float64, device=dev)
+    elif out.dtype != torch.float64 or out.device != dev or out.numel() != 1:
+        raise ValueError(f"out: {out.dtype} {tuple(out.shape)} on {out.device}, expected one "
+                         f"torch.float64 on {dev}")
+    ws = _workspace(workspace, _grads_workspace_bytes(grads.pieces), dev)
+    _run(dev, _grads_sumsq, grads.table.data_ptr(), grads.pieces, out.data_ptr(), ws.data_ptr(),
+         ws.numel())
+    return out
+
+
+def clip_grads(grads, max_norm, sumsq=None):
+    """Writes min(1, max_norm / (norm + 1e-6)) times the gradients to their outputs (a GradList's
+    out; in place otherwise) and returns their global norm, a float64 scalar tensor.  sumsq:
+    grad_sumsq's result where it is summed over ranks; otherwise it is taken here."""
+    grads = _grad_list(grads)
+    dev = grads.device
+    if sumsq is None:
+        sumsq = grad_sumsq(grads)
+    elif sumsq.dtype != torch.float64 or sumsq.device != dev or sumsq.numel() != 1:
+        raise ValueError(f"sumsq: {sumsq.dtype} {tuple(sumsq.shape)} on {sumsq.device}, expected one "
+                         f"torch.float64 on {dev}")
+    norm = torch.empty((), dtype=torch.float64, device=dev)
+    _run(dev, _grads_clip, grads.table.data_ptr(), grads.pieces, max_norm, sumsq.data_ptr(),
+         norm.data_ptr())
+    return norm

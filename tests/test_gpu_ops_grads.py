@@ -1,0 +1,190 @@
+"""The norm and clipping of many gradients against float64: types, sizes from none to many pieces,
+strided and transposed matrices, views of a contribution buffer, in place, values that are not
+finite, two calls at once, side streams and graphs."""
+import math
+
+import pytest
+import torch
+
+import _more_ref as M
+import _ops_ref as R
+from sharded_optimizer_step_zero_amd import ZeroShardError, ops
+
+pytestmark = pytest.mark.gpu
+E = R.E
+TYPES = [torch.bfloat16, torch.float16, torch.float32]
+
+
+def gen(seed):
+    return torch.Generator(device="cuda").manual_seed(seed)
+
+
+def tensors(shapes, seed, dtypes=TYPES, std=1e-2):
+    g = gen(seed)
+    return [(torch.randn(s, generator=g, device="cuda") * std).to(dtypes[i % len(dtypes)]) for i, s in enumerate(shapes)]
+
+
+SHAPES = [(1,), (7,), (0,), (8, 8), (16384,), (16385,), (3, 5, 11), (2049,), (300, 401), (100000,), ()]
+
+
+def check_out(outs, want, norm, got_norm):
+    assert math.isclose(float(got_norm), norm, rel_tol=1e-13)
+    for o, w in zip(outs, want):
+        # the factor and the product are rounded to fp32, and the result to its type
+        R.close(o, w, R.rounded(w, o.dtype, 2), "clipped")
+
+
+@pytest.mark.parametrize("max_norm", [0.5, 1e-3, 1e6])
+@pytest.mark.parametrize("to", [None, torch.bfloat16, torch.float16, torch.float32])
+def test_clip(max_norm, to):
+    g = tensors(SHAPES, 1)
+    norm, want = M.clip(g, max_norm)
+    keep = [t.clone() for t in g]
+    if to is None:
+        got = ops.clip_grads(g, max_norm)
+        if norm <= max_norm:
+            assert all(torch.equal(a, b) for a, b in zip(g, keep))
+        outs = g
+    else:
+        outs = [torch.full(t.shape, 3.0, dtype=to, device="cuda") for t in g]
+        got = ops.clip_grads(ops.GradList(g, out=outs), max_norm)
+        assert all(torch.equal(a, b) for a, b in zip(g, keep))
+    assert got.dtype == torch.float64 and got.dim() == 0
+    check_out(outs, want, norm, got)
+
+
+@pytest.mark.parametrize("count, longest", [(1, 1), (1, 5_000_000), (3000, 700), (2049, 20000)])
+def test_sumsq_and_many_tensors(count, longest):
+    g = torch.Generator().manual_seed(count)
+    shapes = [(int(torch.randint(1, longest + 1, (1,), generator=g)),) for _ in range(count)]
+    t = tensors(shapes, 2)
+    rows = ops.GradList(t)
+    s = ops.grad_sumsq(rows)
+    want = math.fsum(float((x.double() ** 2).sum()) for x in t)
+    assert math.isclose(float(s), want, rel_tol=1e-13)
+    assert torch.equal(ops.grad_sumsq(rows), s)  # bit for bit
+    # given the sum over the ranks instead
+    total = (s * 4).clone()
+    norm, factor = math.sqrt(4 * want), min(1.0, 0.1 / (math.sqrt(4 * want) + 1e-6))
+    exact = [R.f64(x) * factor for x in t]
+    check_out(t, exact, norm, ops.clip_grads(rows, 0.1, sumsq=total))
+
+
+def test_views_of_a_contribution_with_their_neighbours():
+    shapes = [(31,), (50, 20), (5, 7), (16390,)]
+    g = tensors(shapes, 3, [torch.float32, torch.bfloat16])
+    flat = torch.full((20000,), 4.0, dtype=torch.bfloat16, device="cuda")
+    views, at = [], 5
+    for s in shapes:
+        n = torch.Size(s).numel()
+        views.append(flat[at:at + n].view(s))
+        at += n + 3
+    norm, want = M.clip(g, 0.2)
+    check_out(views, want, norm, ops.clip_grads(ops.GradList(g, out=views), 0.2))
+    for v in views:
+        v.fill_(4.0)
+    assert bool((flat == 4).all())
+
+
+def test_strided_and_transposed_matrices():
+    big = tensors([(200, 300)], 4, [torch.bfloat16])[0]
+    keep = big.clone()
+    g = [big[:50, 3:100], big[60:120, 100:].t(), tensors([(40, 30)], 5)[0].t(), big[150:151, 7:20], big[160:, 5:6]]
+    norm, want = M.clip(g, 0.1)
+    out = [torch.empty(50, 97, dtype=torch.float32, device="cuda"),
+           torch.empty(60, 220, dtype=torch.bfloat16, device="cuda")[:, 10:210].t(),
+           torch.empty(40, 30, dtype=torch.bfloat16, device="cuda").t(),
+           torch.empty(1, 13, device="cuda"), torch.empty(40, 9, device="cuda")[:, 2:3]]
+    check_out(out, want, norm, ops.clip_grads(ops.GradList(g, out=out), 0.1))
+    assert torch.equal(big, keep)
+    check_out(g, want, norm, ops.clip_grads(g, 0.1))  # in place
+    inside = torch.zeros(200, 300, dtype=torch.bool, device="cuda")
+    inside[:50, 3:100], inside[60:120, 100:], inside[150:151, 7:20], inside[160:, 5:6] = True, True, True, True
+    assert torch.equal(big[~inside], keep[~inside])
+
+
+def test_any_magnitude():
+    for v, dt in ((1e38, torch.float32), (1e-40, torch.float32), (3e38, torch.bfloat16), (6e4, torch.float16), (6e-8, torch.float16)):
+        t = torch.full((5000,), v, dtype=dt, device="cuda")
+        norm, want = M.clip([t], 1.0)
+        check_out([t], want, norm, ops.clip_grads([t], 1.0))
+
+
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+def test_values_that_are_not_finite(bad):
+    """As the step's clip: a NaN reaches everything, an infinity makes 0 of the rest and NaN of itself."""
+    t = tensors([(100,), (20000,)], 6, [torch.float32])
+    t[1][777] = bad
+    norm = ops.clip_grads(t, 1.0)
+    if math.isnan(bad):
+        assert math.isnan(float(norm)) and all(bool(torch.isnan(x).all()) for x in t)
+    else:
+        assert math.isinf(float(norm)) and not t[0].any() and bool(torch.isnan(t[1][777]))
+        assert int(torch.isnan(t[1]).sum()) == 1
+
+
+def test_all_zero():
+    t = [torch.zeros(9, device="cuda"), torch.zeros(0, device="cuda")]
+    assert float(ops.clip_grads(t, 1.0)) == 0.0 and not t[0].any()
+    empty = ops.GradList([torch.zeros(0, device="cuda")])
+    assert empty.pieces == 0 and float(ops.clip_grads(empty, 1.0)) == 0.0
+
+
+def test_more_than_four_billion_elements():
+    t = torch.zeros((1 << 32) + 70000, dtype=torch.bfloat16, device="cuda")
+    t[-5:] = 2.0
+    t[(1 << 31) + 1] = 4.0
+    assert float(ops.clip_grads([t], 3.0)) == 6.0
+    assert t[-6:].tolist() == [0.0] + [1.0] * 5 and float(t[(1 << 31) + 1]) == 2.0
+
+
+def test_two_lists_at_once():
+    a, b = tensors([(300000,)], 7, [torch.float32]), tensors([(300000,)], 8, [torch.float32])
+    la, lb = ops.GradList(a), ops.GradList(b)
+    na, wa = M.clip(a, 0.1)
+    nb, wb = M.clip(b, 0.2)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        gb = ops.clip_grads(lb, 0.2)
+    ga = ops.clip_grads(la, 0.1)
+    torch.cuda.synchronize()
+    check_out(a, wa, na, ga)
+    check_out(b, wb, nb, gb)
+
+
+def test_graph():
+    g = tensors([(1000,), (300, 70), (50000,)], 9)
+    out = [torch.empty(t.shape, dtype=torch.bfloat16, device="cuda") for t in g]
+    rows = ops.GradList(g, out=out)
+    want_norm = ops.clip_grads(rows, 0.1)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        norm = ops.clip_grads(rows, 0.1)
+    for seed in range(3):
+        for t, n in zip(g, tensors([(1000,), (300, 70), (50000,)], 30 + seed)):
+            t.copy_(n)
+        want_norm = ops.clip_grads(rows, 0.1)
+        want = [o.clone() for o in out]
+        for o in out:
+            o.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(norm, want_norm) and all(torch.equal(p, q) for p, q in zip(out, want))
+
+
+def test_refusals():
+    t = torch.ones(10, device="cuda")
+    o = torch.ones(10, device="cuda")
+    for call in (lambda: ops.GradList([]), lambda: ops.GradList([t], out=[]), lambda: ops.GradList([t], out=[o[:9]]),
+                 lambda: ops.GradList([t.long()]), lambda: ops.GradList([t, t.cpu()]), lambda: ops.GradList([t[::2]]),
+                 lambda: ops.GradList([t.view(2, 5).t().contiguous()], out=[o.view(2, 5).t()]),
+                 lambda: ops.clip_grads([t], 1.0, sumsq=t[:1]), lambda: ops.grad_sumsq([t], out=t[0])):
+        with pytest.raises(ValueError):
+            call()
+    for call, word in ((lambda: ops.GradList([t, t]), "overlaps"), (lambda: ops.GradList([t, t[5:]]), "overlaps"),
+                       (lambda: ops.GradList([t[:9]], out=[t[1:]]), "overlaps"),
+                       (lambda: ops.clip_grads([t], 0.0), "max_norm"), (lambda: ops.clip_grads([t], float("nan")), "max_norm")):
+        with pytest.raises(ZeroShardError, match=word):
+            call()
+    assert ops.GradList([t, t], out=[o, torch.empty(10, device="cuda")]).pieces == 2
