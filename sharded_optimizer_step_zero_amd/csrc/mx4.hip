@@ -12,15 +12,29 @@
 // byte of a register that holds the scales of four instructions; the scales lie in memory in
 // just that order (scale4_at), so that they go the codes' way with no rearrangement.
 //
-// Tiles of 256 features x 128 tokens, four waves of 128 x 64: a wave's 128 sums a lane leave room
-// for a second workgroup on the compute unit, whose products run while this one waits, reads
-// or writes its tile.  128 k a step, three steps in LDS, which global memory is read straight
-// into.  A row's 64 bytes hold chunk c at c ^ ((row >> 2) & 3), so that the 8 rows that are
-// read at a time lie on different banks.  Rows past the edge and groups past the end read as
-// zeros by the buffer loads' bounds check.
+// All tiles take 256 k a step, two steps in LDS, which global memory is read straight into: a row
+// has 128 bytes there, a cache line of memory (64-byte pieces of lines have twice the requests,
+// which the L2 answers no faster than one a channel and cycle: 8192 x 4096 x 22016 took 430 us for
+// 360).  A row's chunk c of 16 bytes sits at c ^ (row & 7): no bank conflicts.  Rows past the edge
+// and groups past the end read as zeros by the buffer loads' bounds check.
+//
+// Large products: 256 x 256, four waves of 128 x 128 whose sums fill the accumulation registers
+// (eight waves of 128 x 64: 460 us).  A half step's fragments are read while the half before
+// is multiplied; between the halves is the step's one barrier, where the next step's codes,
+// under way for a step and a half, have landed and this one's place is free.  A workgroup goes
+// on from tile to tile: the next one's first loads are under way before the last one's
+// products end, and its rows leave through LDS in pieces of 256 bytes (32-byte pieces straight
+// from the registers: 402 us; 64-byte ones: 368).  Smaller products take 128 x 128 or 128 x 64
+// tiles, two or three workgroups a compute unit.
 //
 // Few tokens: the weight is what is read, each of its rows by one workgroup, whose waves share
 // k out between them and add their sums in LDS.
+//
+// Measured, bf16 out: 8192 x 22016 x 4096 (tokens x width x features) 279 us, 5.3 PFLOP/s; 22016 x
+// 8192 x 4096 311 us; 8192 x 4096 x 22016, sixteen steps a tile and 360 MB to write, 360 us, 4.1
+// PFLOP/s.  The clock gives way under the load: on zeros the first takes 232 us (6.4 PFLOP/s).
+#include <algorithm>
+
 #include "ops.h"
 
 namespace zs {
@@ -150,6 +164,8 @@ __global__ __launch_bounds__(256) void unpack_kernel(const uint8_t* __restrict__
 
 // ---------------------------------------------------------------- product
 
+constexpr int kBig = 256;  // a large tile's side
+
 struct Mx4Args {
   const uint8_t *a, *b;    // codes of w (features) and x (tokens)
   const uint8_t *as, *bs;  // scales
@@ -216,11 +232,12 @@ __device__ __forceinline__ u32x4 descriptor(const uint8_t* p, int64_t bytes) {
                (uint32_t)kRsrcWord3};
 }
 
-// R rows of an operand: their way from memory to LDS, 64 bytes of codes a step and 16 of scales
-// a span of four steps.
-template <int R>
+// R rows of an operand: their way from memory to LDS, 128 bytes of codes a step of 256 k, by
+// `THREADS` threads, and 16 bytes of scales a span of two steps.
+template <int R, int THREADS>
 struct Side {
-  static constexpr int kLoads = R * 64 / 4096;  // of a thread, for a step
+  static constexpr int kLoads = R * 128 / (THREADS * 16);  // of a thread, for a step
+  static_assert(R * 128 % (THREADS * 16) == 0, "whole loads");
   const uint8_t* codes;  // the tile's first row
   const uint8_t* scales;
   int64_t ld, span;      // bytes of a row, and of a span's scales
@@ -236,59 +253,62 @@ struct Side {
     scales = s + row0 * 16;
     rows = (int32_t)(n - row0 < R ? n - row0 : R);
     groups = g;
-    const int row = tid >> 2;
-    chunk = (tid & 3) ^ ((row >> 2) & 3);  // 64 rows on, the same
+    const int row = tid >> 3;
+    chunk = (tid & 7) ^ (row & 7);  // whole eights of rows on, the same
 #pragma unroll
-    for (int i = 0; i < kLoads; i++) off[i] = (uint32_t)((row + i * 64) * ld + chunk * 16);
+    for (int i = 0; i < kLoads; i++) off[i] = (uint32_t)((row + i * (THREADS / 8)) * ld + chunk * 16);
   }
   // The codes of a step, into LDS at `lds` (the wave's part of the first load).  Groups past the
   // end would be the next row's: there a lane reads out of bounds.
   __device__ __forceinline__ void load(int step, uint32_t lds) {
-    const int32_t left = groups - step * 4;
-    if (left < 4) {
+    const int32_t left = groups - step * 8;
+    if (left < 8) {
 #pragma unroll
       for (int i = 0; i < kLoads; i++) off[i] = chunk < left ? off[i] : 0xfffffff0u;
     }
-    const u32x4 d = descriptor(codes + step * 64, left > 0 ? (rows - 1) * ld + left * 16 : 0);
+    const u32x4 d = descriptor(codes + (int64_t)step * 128, left > 0 ? (rows - 1) * ld + left * 16 : 0);
 #pragma unroll
-    for (int i = 0; i < kLoads; i++) load_lds(d, off[i], lds + i * 4096);
+    for (int i = 0; i < kLoads; i++) load_lds(d, off[i], lds + i * (THREADS * 16));
   }
 };
 
-// What lane `lane` has of fragment f of a step's rows.
-__device__ __forceinline__ i32x4 fragment(const uint8_t* tile, int row0, int f, int lane) {
-  const int row = row0 + (lane & 15);
-  return *(const i32x4*)(tile + row * 64 + (((lane >> 4) ^ ((row >> 2) & 3)) * 16) + f * 1024);
+// What lane `lane` has of fragment f of a half step's rows.
+__device__ __forceinline__ i32x4 fragment(const uint8_t* tile, int half, int row0, int f, int lane) {
+  const int row = row0 + (lane & 15), chunk = (half * 4 + (lane >> 4)) ^ (row & 7);
+  return *(const i32x4*)(tile + row * 128 + chunk * 16 + f * 2048);
 }
 
+// Small products: BM x BN tiles, two waves by two, two or three workgroups a compute unit.
 template <int DT, int BM, int BN>
 __global__ __launch_bounds__(256, 2) void product_kernel(Mx4Args g) {
-  constexpr int FM = BM / 32, FN = BN / 32;  // fragments of a wave: two waves by two
-  constexpr int kTile = (BM + BN) * 64, kScales = (BM + BN) * 16;
-  constexpr int kLoads = Side<BM>::kLoads + Side<BN>::kLoads;
-  constexpr int kScaleLoads = (kScales + 4095) / 4096;
-  __shared__ __attribute__((aligned(1024))) uint8_t lds[3 * kTile + kScaleLoads * 4096];
+  constexpr int kThreads = 256;
+  constexpr int FM = BM / 32, FN = BN / 32;  // fragments of a wave
+  using SideA = Side<BM, kThreads>;
+  using SideB = Side<BN, kThreads>;
+  constexpr int kTile = (BM + BN) * 128;
+  constexpr int kScaleLoads = (BM + BN + kThreads - 1) / kThreads;
+  static_assert(BM % 64 == 0, "a wave's scales are of one operand");
+  __shared__ __attribute__((aligned(1024))) uint8_t lds[2 * kTile + kScaleLoads * kThreads * 16];
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   int32_t tm, tn;
   tile_of(g, &tm, &tn);
   const int64_t m0 = (int64_t)tm * BM, n0 = (int64_t)tn * BN;
-  const int steps = (g.groups + 3) / 4;
-  Side<BM> a(g.a, g.as, m0, g.m, g.groups, tid);
-  Side<BN> b(g.b, g.bs, n0, g.n, g.groups, tid);
+  const int steps = (g.groups + 7) / 8;
+  SideA a(g.a, g.as, m0, g.m, g.groups, tid);
+  SideB b(g.b, g.bs, n0, g.n, g.groups, tid);
   const uint32_t lds_at = (uint32_t)(uintptr_t)(ZS_LDS uint8_t*)lds + wave * 1024;
-  uint8_t* const scale_tile = lds + 3 * kTile;
+  const uint8_t* const scale_tile = lds + 2 * kTile;
 
-  // The scales of span p: a load of a thread is 16 bytes, those of one row.
+  // The scales of span p: a load of a thread is 16 bytes, those of one row, A's rows and then B's.
   auto load_scales = [&](int p) {
-    const bool there = p * 4 < steps;
+    const bool there = p * 2 < steps;
     const u32x4 da = descriptor(a.scales + p * a.span, there ? a.rows * 16 : 0);
     const u32x4 db = descriptor(b.scales + p * b.span, there ? b.rows * 16 : 0);
 #pragma unroll
     for (int i = 0; i < kScaleLoads; i++) {
-      // A's rows and then B's; BM is whole waves' rows
-      const int row = i * 256 + wave * 64;
-      const uint32_t to = lds_at + 3 * kTile + i * 4096;
+      const int row = i * kThreads + wave * 64;
+      const uint32_t to = lds_at + 2 * kTile + i * kThreads * 16;
       if (row < BM)
         load_lds(da, (uint32_t)((row + lane) * 16), to);
       else
@@ -297,7 +317,7 @@ __global__ __launch_bounds__(256, 2) void product_kernel(Mx4Args g) {
   };
   auto load = [&](int step, int stage) {
     a.load(step, lds_at + stage * kTile);
-    b.load(step, lds_at + stage * kTile + BM * 64);
+    b.load(step, lds_at + stage * kTile + BM * 128);
   };
 
   f32x4 acc[FM][FN];
@@ -310,16 +330,12 @@ __global__ __launch_bounds__(256, 2) void product_kernel(Mx4Args g) {
 
   load_scales(0);
   load(0, 0);
-  load(1, 1);
   int stage = 0;
-  // Step `step`, the J-th of its span.  Its codes have landed for every wave, and every
-  // wave has read the step before, whose place takes the loads of the step after next.
-  auto one = [&](auto J, int step) {
-    constexpr int j = decltype(J)::value;
-    // what may still be on its way: the next step's codes and, after them, a span's scales
-    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(
-                     j == 2 ? kLoads + kScaleLoads : kLoads)
-                 : "memory");
+  // Step `step`, the first or second of its span.  Its codes have landed for every wave, and
+  // every wave has read the step before, whose place takes the loads of the next one.
+  auto one = [&](auto SECOND, int step) {
+    constexpr int j = decltype(SECOND)::value * 2;
+    asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
     const uint8_t* tile = lds + stage * kTile;
     if (j == 0) {
 #pragma unroll
@@ -329,41 +345,316 @@ __global__ __launch_bounds__(256, 2) void product_kernel(Mx4Args g) {
       for (int i = 0; i < FN; i++)
         sb[i] = *(const uint32_t*)(scale_tile + (BM + rb + i * 16 + (lane & 15)) * 16 + (lane >> 4) * 4);
     }
-    i32x4 fb[FN];
+    // every wave has the span's scales: the next one's come
+    if (j == 2) load_scales((step >> 1) + 1);
+    load(step + 1, stage ^ 1);
+    auto half = [&](auto H) {
+      constexpr int h = decltype(H)::value;
+      i32x4 fb[FN];
 #pragma unroll
-    for (int i = 0; i < FN; i++) fb[i] = fragment(tile + BM * 64, rb, i, lane);
-    const int ahead = stage == 0 ? 2 : stage - 1;
-    if (j == 1) load_scales((step >> 2) + 1);
-    load(step + 2, ahead);
+      for (int k = 0; k < FN; k++) fb[k] = fragment(tile + BM * 128, h, rb, k, lane);
 #pragma unroll
-    for (int i = 0; i < FM; i++) {
-      const i32x4 fa = fragment(tile, ra, i, lane);
+      for (int i = 0; i < FM; i++) {
+        const i32x4 fa = fragment(tile, h, ra, i, lane);
 #pragma unroll
-      for (int k = 0; k < FN; k++) acc[i][k] = mfma4<j>(fa, fb[k], acc[i][k], sa[i], sb[k]);
-    }
-    stage = stage == 2 ? 0 : stage + 1;
+        for (int k = 0; k < FN; k++) acc[i][k] = mfma4<j + h>(fa, fb[k], acc[i][k], sa[i], sb[k]);
+      }
+    };
+    half(std::integral_constant<int, 0>());
+    half(std::integral_constant<int, 1>());
+    stage ^= 1;
   };
-  for (int step = 0; step < steps; step += 4) {
+  for (int step = 0; step < steps; step += 2) {
     one(std::integral_constant<int, 0>(), step);
     if (step + 1 < steps) one(std::integral_constant<int, 1>(), step + 1);
-    if (step + 2 < steps) one(std::integral_constant<int, 2>(), step + 2);
-    if (step + 3 < steps) one(std::integral_constant<int, 3>(), step + 3);
   }
   // no load is on its way into LDS any more
   asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
 
   // acc[i][k][r]: feature m0 + ra + i*16 + (lane>>4)*4 + r, token n0 + rb + k*16 + (lane&15)
+  const int64_t f0 = m0 + ra + (lane >> 4) * 4, t0 = n0 + rb + (lane & 15);
 #pragma unroll
   for (int k = 0; k < FN; k++) {
-    const int64_t t = n0 + rb + k * 16 + (lane & 15);
-    if (t >= g.n) continue;
-    elem_t<DT>* row = (elem_t<DT>*)g.c + t * g.ldc;
+    elem_t<DT>* out = (elem_t<DT>*)g.c + (t0 + k * 16) * g.ldc + f0;
+    const bool there = t0 + k * 16 < g.n;
+    if constexpr (DT != ZS_F32) {
+      if (m0 + BM <= g.m) {
+        // Two fragments' sums change places between the lanes' rows of 16, so that a lane has
+        // eight neighbouring features: rows 0 and 2 the first fragment's, 1 and 3 the second's.
+        typedef elem_t<DT> v4 __attribute__((ext_vector_type(4)));
 #pragma unroll
-    for (int i = 0; i < FM; i++) {
-      const int64_t f = m0 + ra + i * 16 + (lane >> 4) * 4;
-      if (f < g.m) store4<DT>(row + f, g.m - f, acc[i][k]);
+        for (int i = 0; i < FM; i += 2) {
+          const u32x2 x = __builtin_bit_cast(u32x2, __builtin_convertvector(acc[i][k], v4));
+          const u32x2 y = __builtin_bit_cast(u32x2, __builtin_convertvector(acc[i + 1][k], v4));
+          const auto lo = __builtin_amdgcn_permlane16_swap(x[0], y[0], false, false);
+          const auto hi = __builtin_amdgcn_permlane16_swap(x[1], y[1], false, false);
+          if (there)
+            *(u32x4_any*)(out + i * 16 + (lane >> 4 & 1) * 12) = u32x4{lo[0], hi[0], lo[1], hi[1]};
+        }
+        continue;
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < FM; i++)
+      if (there && f0 + i * 16 < g.m) store4<DT>(out + i * 16, g.m - f0 - i * 16, acc[i][k]);
+  }
+}
+
+// c += a b, c in the accumulation registers, where the compiler would not leave all 256 sums of a
+// lane.  It does not know how long the result takes, so settle() has to come before anything
+// else touches the sums.
+template <int J>
+__device__ __forceinline__ void mfma_held(f32x4& c, i32x4 a, i32x4 b, uint32_t sa, uint32_t sb) {
+#define ZS_MFMA(bytes)                                                                       \
+  asm volatile("v_mfma_scale_f32_16x16x128_f8f6f4 %0, %1, %2, %0, %3, %4 " bytes " cbsz:4 blgp:4" \
+               : "+a"(c)                                                                     \
+               : "v"(a), "v"(b), "v"(sa), "v"(sb))
+  if constexpr (J == 0)
+    ZS_MFMA("op_sel:[0,0,0] op_sel_hi:[0,0,0]");
+  else if constexpr (J == 1)
+    ZS_MFMA("op_sel:[1,1,0] op_sel_hi:[0,0,0]");
+  else if constexpr (J == 2)
+    ZS_MFMA("op_sel:[0,0,0] op_sel_hi:[1,1,0]");
+  else
+    ZS_MFMA("op_sel:[1,1,0] op_sel_hi:[1,1,0]");
+#undef ZS_MFMA
+}
+// The last matrix instruction's result is written (19 wait states after its issue at most).
+__device__ __forceinline__ void settle() { asm volatile("s_nop 15\n\ts_nop 3" ::: "memory"); }
+
+// Large products: 256 x 256 tiles, four waves of 128 x 128, one workgroup a compute unit that
+// goes on from tile to tile.
+template <int DT>
+__global__ __launch_bounds__(256, 1) void held_kernel(Mx4Args g) {
+  constexpr int B = kBig, F = 8;
+  using Part = Side<B, 256>;
+  constexpr int kTile = 2 * B * 128, kLoads = 2 * Part::kLoads;
+  constexpr int kStashRow = 256 + 16;  // the rows of a column lie on different banks
+  __shared__ __attribute__((aligned(1024))) uint8_t lds[2 * kTile + 2 * B * 16 + 4 * 16 * kStashRow];
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int spans = (g.groups + 15) / 16;
+  const uint32_t lds_at = (uint32_t)(uintptr_t)(ZS_LDS uint8_t*)lds + wave * 1024;
+  const uint8_t* const scale_tile = lds + 2 * kTile;
+  const int ra = (wave >> 1) * 128, rb = (wave & 1) * 128;
+
+  // the tiles of this workgroup: its die has a contiguous part of them, which go down bands
+  // of 8 tiles of tokens; the die's workgroups take neighbouring ones
+  const uint32_t total = (uint32_t)g.tiles_m * (uint32_t)g.tiles_n;
+  const uint32_t die = blockIdx.x & 7, per = total >> 3, extra = total & 7;
+  const uint32_t end = (die + 1) * per + (die + 1 < extra ? die + 1 : extra);
+  const uint32_t step = (gridDim.x + 7 - die) >> 3;
+  uint32_t id = die * per + (die < extra ? die : extra) + (blockIdx.x >> 3);
+
+  // where the loads are: the tile's rows, and its place in LDS by thread
+  uint32_t off[Part::kLoads];
+  const int row = tid >> 3, chunk = (tid & 7) ^ (row & 7);
+  const int64_t ld = (int64_t)g.groups * 16;
+#pragma unroll
+  for (int i = 0; i < Part::kLoads; i++) off[i] = (uint32_t)((row + i * 32) * ld + chunk * 16);
+  const uint8_t *pa, *pb, *qa, *qb;  // codes and scales of the tile that is loaded
+  int32_t rows_a, rows_b;
+  auto aim = [&](uint32_t id, int64_t* m0, int64_t* n0) {
+    const uint32_t band = id / ((uint32_t)g.tiles_m * 8);
+    const uint32_t in = id - band * (uint32_t)g.tiles_m * 8;
+    const uint32_t wide = (uint32_t)g.tiles_n - band * 8 < 8 ? (uint32_t)g.tiles_n - band * 8 : 8;
+    *m0 = (int64_t)(in / wide) * B;
+    *n0 = (int64_t)(band * 8 + in % wide) * B;
+  };
+  auto aim_loads = [&](uint32_t id) {
+    int64_t m0, n0;
+    aim(id, &m0, &n0);
+    pa = g.a + m0 * ld;
+    pb = g.b + n0 * ld;
+    qa = g.as + m0 * 16;
+    qb = g.bs + n0 * 16;
+    rows_a = (int32_t)(g.m - m0 < B ? g.m - m0 : B);
+    rows_b = (int32_t)(g.n - n0 < B ? g.n - n0 : B);
+  };
+  // a step's descriptors, and whether this thread's chunk of it exists
+  struct Aim {
+    u32x4 a, b;
+    bool there;
+  };
+  auto aim_step = [&](int s, bool any) {
+    const int32_t left = g.groups - s * 8;
+    Aim r;
+    r.a = descriptor(pa + (int64_t)s * 128, any && left > 0 ? (rows_a - 1) * ld + left * 16 : 0);
+    r.b = descriptor(pb + (int64_t)s * 128, any && left > 0 ? (rows_b - 1) * ld + left * 16 : 0);
+    r.there = chunk < left;
+    return r;
+  };
+  auto load = [&](const Aim& r, int buffer, int i) {
+    const int k = i % Part::kLoads;
+    const uint32_t from = r.there ? off[k] : 0xfffffff0u;
+    load_lds(i < Part::kLoads ? r.a : r.b, from, lds_at + buffer * kTile + (i < Part::kLoads ? 0 : B * 128) + k * 4096);
+  };
+  auto load_scales = [&](int p, bool any) {
+    const u32x4 da = descriptor(qa + p * g.m * 16, any ? rows_a * 16 : 0);
+    const u32x4 db = descriptor(qb + p * g.n * 16, any ? rows_b * 16 : 0);
+    load_lds(da, (uint32_t)tid * 16, lds_at + 2 * kTile);
+    load_lds(db, (uint32_t)tid * 16, lds_at + 2 * kTile + B * 16);
+  };
+
+  f32x4 acc[F][F];
+#pragma unroll
+  for (int i = 0; i < F; i++)
+#pragma unroll
+    for (int k = 0; k < F; k++) acc[i][k] = f32x4{};
+  i32x4 fa[F], fb[F], ga[F], gb[F];
+  uint32_t sa[F], sb[F], ta[F], tb[F];
+  auto read_scale = [&](uint32_t* s, int row0, int i) {
+    s[i] = *(const uint32_t*)(scale_tile + (row0 + i * 16 + (lane & 15)) * 16 + (lane >> 4) * 4);
+  };
+  // Multiplies fragments xa, xb (instruction J of the span) while the half `half` of the tile at
+  // `tile` is read into ya, yb, NEXT: and the next span's scales, and LOADS: starts the loads of
+  // a step into `buffer`.  Reads and loads are dealt out between pairs of matrix instructions,
+  // which take longer than issuing them; the last eighth has none, so that the last reads
+  // have arrived.
+  auto multiply = [&](auto JJ, auto NEXT, auto LOADS, i32x4(&xa)[F], i32x4(&xb)[F],
+                      i32x4(&ya)[F], i32x4(&yb)[F], const uint8_t* tile, int half, int buffer,
+                      const Aim& r) {
+    constexpr int J = decltype(JJ)::value;
+    constexpr bool kNext = decltype(NEXT)::value;
+    constexpr int kPairs = F * F / 2, kSpan = kPairs * 7 / 8, kReads = 2 * F + (kNext ? 2 * F : 0);
+    constexpr int n_loads = decltype(LOADS)::value ? kLoads : 0;
+#pragma unroll
+    for (int x = 0; x < kPairs; x++) {
+#pragma unroll
+      for (int e = (x * kReads + kSpan - 1) / kSpan;
+           e < ((x + 1) * kReads + kSpan - 1) / kSpan && e < kReads; e++) {
+        if (e == 0)
+          ya[0] = fragment(tile, half, ra, 0, lane);
+        else if (e <= F)
+          yb[e - 1] = fragment(tile + B * 128, half, rb, e - 1, lane);
+        else if (e < 2 * F)
+          ya[e - F] = fragment(tile, half, ra, e - F, lane);
+        else if (e < 3 * F)
+          read_scale(ta, ra, e - 2 * F);
+        else
+          read_scale(tb, B + rb, e - 3 * F);
+      }
+#pragma unroll
+      for (int e = (x * n_loads + kSpan - 1) / kSpan;
+           e < ((x + 1) * n_loads + kSpan - 1) / kSpan && e < n_loads; e++)
+        load(r, buffer, e);
+#pragma unroll
+      for (int y = 2 * x; y < 2 * x + 2; y++) {
+        // to and fro, so that a turn keeps both a row's and a column's operand
+        const int i = y / F, j = i & 1 ? F - 1 - y % F : y % F;
+        mfma_held<J>(acc[i][j], xa[i], xb[j], sa[i], sb[j]);
+      }
+      __builtin_amdgcn_sched_barrier(0);
+    }
+  };
+  // every load has landed, and every wave has read what it reads
+  auto meet = [] { asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory"); };
+
+  std::integral_constant<int, 0> c0;
+  std::integral_constant<int, 1> c1;
+  std::integral_constant<int, 2> c2;
+  std::integral_constant<int, 3> c3;
+  std::integral_constant<bool, false> no;
+  std::integral_constant<bool, true> yes;
+  if (id >= end) return;
+  aim_loads(id);
+  load_scales(0, true);
+  {
+    const Aim r = aim_step(0, true), q = aim_step(1, true);
+#pragma unroll
+    for (int i = 0; i < kLoads; i++) load(r, 0, i);
+#pragma unroll
+    for (int i = 0; i < kLoads; i++) load(q, 1, i);
+  }
+  asm volatile("s_waitcnt vmcnt(%0)\n\ts_barrier" ::"n"(kLoads) : "memory");
+#pragma unroll
+  for (int i = 0; i < F; i++) {
+    fa[i] = fragment(lds, 0, ra, i, lane);
+    fb[i] = fragment(lds + B * 128, 0, rb, i, lane);
+    read_scale(ta, ra, i);
+    read_scale(tb, B + rb, i);
+  }
+  const Aim none = {};
+  for (; id < end; id += step) {
+    const bool more = id + step < end;
+    int64_t m0, n0;
+    aim(id, &m0, &n0);
+    int p = 0;
+    do {
+      const bool last = p + 1 == spans;
+#pragma unroll
+      for (int i = 0; i < F; i++) {
+        sa[i] = ta[i];
+        sb[i] = tb[i];
+      }
+      multiply(c0, no, no, fa, fb, ga, gb, lds, 1, 0, none);
+      // the span's second step is there; its first one's place and the scales' are free
+      meet();
+      if (last && more) aim_loads(id + step);
+      const bool any = !last || more;
+      load_scales(last ? 0 : p + 1, any);
+      Aim r = aim_step(last ? 0 : 2 * p + 2, any);
+      multiply(c1, no, yes, ga, gb, fa, fb, lds + kTile, 0, 0, r);
+      multiply(c2, no, no, fa, fb, ga, gb, lds + kTile, 1, 0, none);
+      meet();
+      r = aim_step(last ? 1 : 2 * p + 3, any);
+      multiply(c3, yes, yes, ga, gb, fa, fb, lds, 0, 1, r);
+      settle();
+    } while (++p < spans);
+    // acc[i][k][r]: feature m0 + ra + i*16 + (lane>>4)*4 + r, token n0 + rb + k*16 + (lane&15)
+    const int64_t f0 = m0 + ra + (lane >> 4) * 4, t0 = n0 + rb + (lane & 15);
+    elem_t<DT>* out = (elem_t<DT>*)g.c + t0 * g.ldc + f0;
+    auto sums = [&](int i, int k) {
+      f32x4 x;
+#pragma unroll
+      for (int r = 0; r < 4; r++)
+        asm volatile("v_accvgpr_read_b32 %0, %1" : "=v"(x[r]) : "a"(acc[i][k][r]));
+      acc[i][k] = f32x4{};
+      return x;
+    };
+    if (m0 + B > g.m || n0 + B > g.n) {
+#pragma unroll
+      for (int k = 0; k < F; k++) {
+#pragma unroll
+        for (int i = 0; i < F; i++) {
+          const f32x4 x = sums(i, k);
+          if (t0 + k * 16 < g.n && f0 + i * 16 < g.m) store4<DT>(out + i * 16, g.m - f0 - i * 16, x);
+          __builtin_amdgcn_sched_barrier(0);
+        }
+        out += 16 * g.ldc;
+      }
+    } else if constexpr (DT == ZS_F32) {
+#pragma unroll
+      for (int k = 0; k < F; k++) {
+#pragma unroll
+        for (int i = 0; i < F; i++) {
+          store4<DT>(out + i * 16, 4, sums(i, k));
+          __builtin_amdgcn_sched_barrier(0);
+        }
+        out += 16 * g.ldc;
+      }
+    } else {
+      // 16 tokens' rows go through LDS, so that a store has whole lines: four rows of 256 bytes
+      typedef elem_t<DT> v4 __attribute__((ext_vector_type(4)));
+      uint8_t* const stash = lds + 2 * kTile + 2 * B * 16 + wave * 16 * kStashRow;
+      uint8_t* to = stash + (lane & 15) * kStashRow + (lane >> 4) * 8;
+      const uint8_t* from = stash + (lane >> 4) * kStashRow + (lane & 15) * 16;
+      out = (elem_t<DT>*)g.c + (n0 + rb + (lane >> 4)) * g.ldc + m0 + ra + (lane & 15) * 8;
+#pragma unroll
+      for (int k = 0; k < F; k++) {
+#pragma unroll
+        for (int i = 0; i < F; i++)
+          *(u32x2*)(to + i * 32) = __builtin_bit_cast(u32x2, __builtin_convertvector(sums(i, k), v4));
+#pragma unroll
+        for (int i = 0; i < 4; i++)
+          *(u32x4_any*)(out + i * 4 * g.ldc) = *(const u32x4*)(from + i * 4 * kStashRow);
+        __builtin_amdgcn_sched_barrier(0);
+        out += 16 * g.ldc;
+      }
     }
   }
+  // no load is on its way into LDS any more
+  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
 }
 
 // Few tokens: 32 features a workgroup, FN * 16 tokens, spans of k dealt out over eight waves.
@@ -427,6 +718,14 @@ __global__ __launch_bounds__(kFewWaves * 64) void few_kernel(Mx4Args g) {
 
 // Up to so many tokens the weight is streamed.
 constexpr int64_t kFewTokens = 64;
+constexpr int64_t kCus = 256;
+// From so many tiles of 256 x 256 on, the card is filled by them; below, by tiles of 128 x 128
+// while there are as many as compute units; else by 128 x 64.  us with large, middle and small
+// tiles (tokens x width x features): 4096 x 4096 x 4096 34, 42 and 49; 2048 x 2048 x 6144 (192
+// large tiles) 20, 22 and 24; 2048 x 4096 x 4096 (128) 30, 23 and 28; 512 x 4096 x 11008 30, 20
+// and 22; 1024 x 4096 x 4096 (256 middle tiles) 29, 15 and 15; 128 x 4096 x 22016 (172) 30, 18
+// and 16.
+constexpr int64_t kHeldTiles = 192;
 
 }  // namespace
 }  // namespace ops
@@ -546,14 +845,18 @@ extern "C" int zs_mx4_product(const void* x_codes, const void* x_scales, const v
     g.tiles_n = (int32_t)((tokens + bn - 1) / bn);
     return (int64_t)g.tiles_m * g.tiles_n;
   };
-  const bool small = tiles(256, 128) < 512;
-  const int64_t total = small ? tiles(128, 64) : tiles(256, 128);
+  const bool held = tiles(kBig, kBig) >= kHeldTiles;
+  const bool middle = !held && tiles(128, 128) >= kCus;
+  const int64_t total = held ? tiles(kBig, kBig) : middle ? tiles(128, 128) : tiles(128, 64);
   if (total > 0xffffff) return fail(who, "too many tiles for one call");
   with_dtype(dtype, [&](auto DT) {
-    if (small)
-      product_kernel<decltype(DT)::value, 128, 64><<<dim3((uint32_t)total), dim3(256), 0, st>>>(g);
+    constexpr int kDt = decltype(DT)::value;
+    if (held)
+      held_kernel<kDt><<<dim3((uint32_t)std::min(total, kCus)), dim3(256), 0, st>>>(g);
+    else if (middle)
+      product_kernel<kDt, 128, 128><<<dim3((uint32_t)total), dim3(256), 0, st>>>(g);
     else
-      product_kernel<decltype(DT)::value, 256, 128><<<dim3((uint32_t)total), dim3(256), 0, st>>>(g);
+      product_kernel<kDt, 128, 64><<<dim3((uint32_t)total), dim3(256), 0, st>>>(g);
   });
   return launched(who);
 }

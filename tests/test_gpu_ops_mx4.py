@@ -141,18 +141,21 @@ def test_product(dtype, tokens, width, features):
     assert torch.equal(ops.linear4(x, ops.pack4(w)), got)
 
 
-@pytest.mark.parametrize("tokens, width, features", [(4100, 160, 4300), (1000, 544, 17000), (2304, 96, 8200)])
-def test_large_tiles(tokens, width, features):
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("tokens, width, features", [(4100, 160, 4300), (1000, 544, 17000), (2304, 96, 8200),
+                                                     (2100, 700, 2100), (1030, 1100, 4096), (2048, 300, 2304)])
+def test_larger_tiles(tokens, width, features, dtype):
+    """256 x 256, also more than one a workgroup, and 128 x 128, whole and ragged."""
     g = gen(tokens)
     x, w = rand(g, tokens, width, dtype=torch.bfloat16), rand(g, features, width, dtype=torch.bfloat16)
-    check_product(x, w, torch.bfloat16)
+    check_product(x, w, dtype)
 
 
-@pytest.mark.parametrize("tokens", [5, 40, 100, 2500])
+@pytest.mark.parametrize("tokens", [5, 40, 100, 1300, 2500])
 @pytest.mark.parametrize("steps", [1, 2, 3, 4, 5, 7, 8, 9])
 def test_every_length_of_the_loop(tokens, steps):
     """k from one step of 128 to nine, and a group short of each."""
-    features = 13000 if tokens == 2500 else 200  # the first has large tiles
+    features = {2500: 13000, 1300: 4000}.get(tokens, 200)  # large and middle tiles
     for width in (steps * 128, steps * 128 - 40):
         g = gen(width)
         x, w = rand(g, tokens, width, dtype=torch.bfloat16), rand(g, features, width, dtype=torch.bfloat16)
