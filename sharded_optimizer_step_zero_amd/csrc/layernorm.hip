@@ -12,10 +12,10 @@
 // kernel adds the parts in a fixed order.  Wider rows leave no registers for that: there a
 // first kernel takes the rows' two means, and a second goes down strips of 2048 columns.
 //
-// A code or a scale that one bit decides is taken from fp64: the fp32 output is within e =
-// (|(s-m) rstd w| + |b|) 2^-21 of y (eight roundings' worth, six are made), so where y - e and
-// y + e have one code, or one scale for the group, that is y's; elsewhere the products are
-// taken again in fp64 (4e-5 of the chunks).
+// Codes come from an output in fp64 (whose instructions take no longer than fp32's), rounded to
+// fp32 to nearest and, where that may have crossed the border between two codes or two scales, to
+// the odd side, so that each code is one rounding of y.  (The output in fp32 with an error bound,
+// and both of its ends encoded, took 260 us for @@.)
 #include "rows.h"
 
 namespace zs {
@@ -28,132 +28,163 @@ constexpr int64_t kMaxBlocks = 0x7fffff;
 constexpr int64_t kHeldWidth = 8192;
 constexpr int64_t kStrip = 2048;  // columns of a workgroup beyond that
 
-template <int DT, bool NT, int NC, int T, int CODE>
-__global__ __launch_bounds__(T) void layer_norm_kernel(
-    const elem_t<DT>* x, int64_t x_stride, const elem_t<DT>* residual, int64_t residual_stride,
-    const elem_t<DT>* __restrict__ weight, const elem_t<DT>* __restrict__ bias, elem_t<DT>* sum,
-    int64_t sum_stride, elem_t<DT>* __restrict__ y, int64_t y_stride,
-    uint8_t* __restrict__ codes, uint8_t* __restrict__ scales, float* __restrict__ mean,
-    float* __restrict__ rstd, int64_t rows, int64_t width, float eps, double inv_width, int lanes,
-    int rows_per_block, int group_lanes) {
-  __shared__ double slots[2][16];
+template <int DT>
+struct RowArgs {
+  const elem_t<DT>*x, *residual, *weight, *bias;
+  elem_t<DT>*sum, *y;
+  int64_t x_stride, residual_stride, sum_stride, y_stride;
+  uint8_t *codes, *scales;
+  float *mean, *rstd;
+  int64_t rows;
+  int32_t width, lanes, rows_per_block, code, group_lanes;
+  float eps;
+  double inv_width;
+};
+
+// The scale byte of a group, by the format as a value.
+__device__ __forceinline__ uint32_t scale_byte_of(int code, float amax) {
+  return code == ZS_E4M3 ? scale_byte<ZS_E4M3>(amax)
+                         : code == ZS_E5M2 ? scale_byte<ZS_E5M2>(amax) : scale_byte<ZS_E2M1>(amax);
+}
+
+// WHOLE: the threads' chunks cover the row exactly.
+template <int DT, bool NT, int NC, bool CODES, bool WHOLE>
+__device__ __forceinline__ void layer_norm_rows(const RowArgs<DT>& g, double (&slots)[2][16]) {
+  const int lanes = g.lanes, width = g.width;
   const int in_row = threadIdx.x & (lanes - 1);
-  const int64_t row = (int64_t)blockIdx.x * rows_per_block + (rows_per_block > 1 ? threadIdx.x / lanes : 0);
-  const bool live = row < rows;  // no early return: the shuffles and barriers are the workgroup's
-  const int64_t from = live ? row : rows - 1;  // a row that exists
+  const int64_t row = (int64_t)blockIdx.x * g.rows_per_block + (g.rows_per_block > 1 ? threadIdx.x / lanes : 0);
+  const bool live = row < g.rows;  // no early return: the shuffles and barriers are the workgroup's
+  const int64_t from = live ? row : g.rows - 1;  // a row that exists
+  // elements of chunk k that exist
+  auto count = [&](int k) {
+    const int left = width - (k * lanes + in_row) * 8;
+    return WHOLE ? 8 : left;
+  };
   Chunk<DT> in[NC], add[NC];
 #pragma unroll
   for (int k = 0; k < NC; k++) {
-    const int64_t c = (int64_t)(k * lanes + in_row) * 8;
-    in[k] = load_row<DT, NT>(x + from * x_stride, c, width);
-    if (residual) add[k] = load_row<DT, NT>(residual + from * residual_stride, c, width);
+    const int c = (k * lanes + in_row) * 8;
+    if (WHOLE) {
+      in[k] = load_chunk<DT, NT>(g.x + from * g.x_stride + c, 8);
+      if (g.residual) add[k] = load_chunk<DT, NT>(g.residual + from * g.residual_stride + c, 8);
+    } else {
+      in[k] = load_row<DT, NT>(g.x + from * g.x_stride, c, width);
+      if (g.residual) add[k] = load_row<DT, NT>(g.residual + from * g.residual_stride, c, width);
+    }
   }
   f32x8 s[NC];
   double total = 0.0;
 #pragma unroll
   for (int k = 0; k < NC; k++) {
-    const int64_t c = (int64_t)(k * lanes + in_row) * 8, left = live ? width - c : 0;
-    s[k] = take8<DT>(in[k], left, width);
-    if (residual) {
-      s[k] += take8<DT>(add[k], left, width);
+    const int c = (k * lanes + in_row) * 8, left = count(k);
+    s[k] = WHOLE ? widen<DT>(in[k]) : take8<DT>(in[k], left, width);
+    if (g.residual) {
+      s[k] += WHOLE ? widen<DT>(add[k]) : take8<DT>(add[k], left, width);
       // the stored, rounded sum is what is normalised
       s[k] = __builtin_convertvector(__builtin_convertvector(s[k], typename Elem<DT>::vec), f32x8);
-      store8<DT, NT>(sum + row * sum_stride + c, left, s[k]);
+      if (live) store8<DT, NT>(g.sum + row * g.sum_stride + c, left, s[k]);
     }
 #pragma unroll
     for (int i = 0; i < 8; i++) total += (double)s[k][i];
   }
-  const double m = row_sum(total, lanes, slots[0]) * inv_width;
+  const double m = row_sum(total, lanes, slots[0]) * g.inv_width;
+  // differences from the mean: with codes they stay in fp64 for the output
+  constexpr int kHeld = CODES ? NC : 1;
+  double held[kHeld][8];
   double sq = 0.0;
 #pragma unroll
   for (int k = 0; k < NC; k++) {
-    const int64_t left = live ? width - (int64_t)(k * lanes + in_row) * 8 : 0;
 #pragma unroll
     for (int i = 0; i < 8; i++) {
-      const double d = left >= 8 || i < left ? (double)s[k][i] - m : 0.0;
-      sq = __builtin_fma(d, d, sq);
+      const double d = (double)s[k][i] - m;
+      if (WHOLE || i < count(k)) sq = __builtin_fma(d, d, sq);
+      if (CODES) held[CODES ? k : 0][i] = d;
     }
   }
-  const double variance = row_sum(sq, lanes, slots[1]) * inv_width;
-  const double root = inverse_root(variance + (double)eps);
+  const double variance = row_sum(sq, lanes, slots[1]) * g.inv_width;
+  const double root = inverse_root(variance + (double)g.eps);
   const float r = (float)root;
   // the mean in two parts: a difference from it is off by two roundings of itself
   const float m_high = (float)m, m_low = (float)(m - (double)m_high);
   if (live && in_row == 0) {
-    mean[row] = m_high;
-    rstd[row] = r;
+    g.mean[row] = m_high;
+    g.rstd[row] = r;
   }
-  constexpr int kCode = CODE < 0 ? 0 : CODE;
-  const int64_t groups = (width + group_lanes * 8 - 1) / (group_lanes * 8);
-  if (CODE == ZS_E2M1 && live && groups + in_row < (groups + 15) / 16 * 16)  // 15 at most: one a lane
-    scales[scale4_at(row, groups + in_row, rows)] = 127;
+  if constexpr (!CODES) {
 #pragma unroll
-  for (int k = 0; k < NC; k++) {
-    const int64_t chunk = k * lanes + in_row, c = chunk * 8, left = live ? width - c : 0;
-    f32x8 v = {}, e = {};
-    if (left > 0) {
-      const f32x8 w = load8<DT>(weight + c, left);
-      const f32x8 b = bias ? load8<DT>(bias + c, left) : f32x8{};
-#pragma unroll
-      for (int i = 0; i < 8; i++) {
-        const float p = ((s[k][i] - m_high) - m_low) * r * w[i];
-        v[i] = p + b[i];
-        e[i] = (__builtin_fabsf(p) + __builtin_fabsf(b[i])) * 0x1p-21f;
-      }
-      if (y) store8<DT, NT>(y + row * y_stride + c, left, v);
+    for (int k = 0; k < NC; k++) {
+      const int c = (k * lanes + in_row) * 8, left = count(k);
+      if (!live || left <= 0 || !g.y) continue;
+      const f32x8 w = load8<DT>(g.weight + c, left);
+      const f32x8 b = g.bias ? load8<DT>(g.bias + c, left) : f32x8{};
+      store8<DT, NT>(g.y + row * g.y_stride + c, left, ((s[k] - m_high) - m_low) * r * w + b);
     }
-    if (CODE >= 0) {
-      // in fp64, to the odd side where fp32 loses anything
-      auto again = [&](double factor) {
-        f32x8 q = {};
-        if (left > 0) {
-          const f32x8 w = load8<DT>(weight + c, left);
-          const f32x8 b = bias ? load8<DT>(bias + c, left) : f32x8{};
+  } else {
+    const int group_lanes = g.group_lanes, groups = (width + group_lanes * 8 - 1) / (group_lanes * 8);
+    // the scales that fill a span of the 4-bit form up: 15 at most, one a lane
+    if (g.code == ZS_E2M1 && live && groups + in_row < (groups + 15) / 16 * 16)
+      g.scales[scale4_at(row, groups + in_row, g.rows)] = 127;
 #pragma unroll
-          for (int i = 0; i < 8; i++)
-            q[i] = side_of(__builtin_fma((widen_again(s[k][i]) - m) * root, (double)w[i], (double)b[i]) * factor);
+    for (int k = 0; k < NC; k++) {
+      const int chunk = k * lanes + in_row, c = chunk * 8, left = count(k);
+      f32x8 v = {};
+      double q[8] = {};
+      uint32_t nearest = 0xffffffffu;  // the least of the outputs' low halves, moved up
+      if (WHOLE || left > 0) {
+        const f32x8 w = load8<DT>(g.weight + c, left);
+        const f32x8 b = g.bias ? load8<DT>(g.bias + c, left) : f32x8{};
+#pragma unroll
+        for (int i = 0; i < 8; i++) {
+          q[i] = __builtin_fma(held[k][i] * root, (double)w[i], (double)b[i]);
+          v[i] = (float)q[i];
+          const uint32_t low = __float_as_uint(v[i]) << 16;
+          nearest = low < nearest ? low : nearest;
         }
-        return q;
-      };
-      f32x8 least, most;
+        if (live && g.y) store8<DT, NT>(g.y + row * g.y_stride + c, left, v);
+      }
+      // Ties of codes, and borders of scales, have sixteen zeros at least at their end (where
+      // they are normal in fp32).  An output that fp32 rounds to such a value may lie to either
+      // side.
+      float amax = group_amax(v, group_lanes);
+      // the same for all lanes of a group
+      const bool border = (__float_as_uint(amax) & 0xffffu) == 0 || amax < 0x1p-90f;
+      if (border || nearest == 0) {
 #pragma unroll
-      for (int i = 0; i < 8; i++) {
-        const float a = __builtin_fabsf(v[i]);
-        least[i] = a - e[i] > 0.0f ? a - e[i] : 0.0f;
-        most[i] = a + e[i];
+        for (int i = 0; i < 8; i++) v[i] = side_of(q[i]);
       }
-      uint32_t byte = scale_byte<kCode>(group_amax(most, group_lanes));
-      if (byte != scale_byte<kCode>(group_amax(least, group_lanes))) {  // all of the group's lanes
-        const f32x8 q = again(1.0);
-        byte = scale_byte<kCode>(group_amax(q, group_lanes));
-      }
-      const float inv = scale_inverse(byte == 255u ? 127u : byte);
-      f32x8 lo, hi;
-#pragma unroll
-      for (int i = 0; i < 8; i++) {
-        lo[i] = (v[i] - e[i]) * inv;
-        hi[i] = (v[i] + e[i]) * inv;
-      }
-      if constexpr (CODE == ZS_E2M1) {
-        uint32_t q = encode4(lo, 1.0f);
-        if (q != encode4(hi, 1.0f)) q = encode4(again((double)inv), 1.0f);
-        if (byte == 255u) q = 0;
+      if (border) amax = group_amax(v, group_lanes);
+      const uint32_t byte = scale_byte_of(g.code, amax);
+      // the scaling is exact but far below the group's largest, where all that matters is the side
+      v *= scale_inverse(byte == 255u ? 127u : byte);
+      if (g.code == ZS_E2M1) {
+        const uint32_t word = byte == 255u ? 0u : encode4(v, 1.0f);
         if (live && c < groups * 32) {  // zeros behind the row's end
-          *(uint32_t*)(codes + row * groups * 16 + chunk * 4) = q;
-          if (chunk % 4 == 0) scales[scale4_at(row, chunk / 4, rows)] = (uint8_t)byte;
+          *(uint32_t*)(g.codes + row * groups * 16 + chunk * 4) = word;
+          if (chunk % 4 == 0) g.scales[scale4_at(row, chunk / 4, g.rows)] = (uint8_t)byte;
         }
       } else {
-        u32x2 q = encode8<kCode>(lo);
-        const u32x2 other = encode8<kCode>(hi);
-        if (q[0] != other[0] || q[1] != other[1]) q = encode8<kCode>(again((double)inv));
-        if (byte == 255u) q = u32x2{0, 0};
-        if (left > 0) {
-          store_codes<NT>(codes + row * width + c, left, q);
-          if (chunk % group_lanes == 0) scales[row * groups + chunk / group_lanes] = (uint8_t)byte;
+        u32x2 word;
+        if (g.code == ZS_E4M3)
+          word = encode8<ZS_E4M3>(v);
+        else
+          word = encode8<ZS_E5M2>(v);
+        if (byte == 255u) word = u32x2{0, 0};
+        if (live && left > 0) {
+          store_codes<NT>(g.codes + row * width + c, left, word);
+          if ((chunk & (group_lanes - 1)) == 0) g.scales[row * groups + chunk / group_lanes] = (uint8_t)byte;
         }
       }
     }
   }
+}
+
+template <int DT, bool NT, int NC, int T, bool CODES>
+__global__ __launch_bounds__(T) void layer_norm_kernel(RowArgs<DT> g) {
+  __shared__ double slots[2][16];
+  if (g.width == g.lanes * NC * 8)
+    layer_norm_rows<DT, NT, NC, CODES, true>(g, slots);
+  else
+    layer_norm_rows<DT, NT, NC, CODES, false>(g, slots);
 }
 
 // The chunks of a row that the backward pass reads.
@@ -314,6 +345,15 @@ __global__ __launch_bounds__(256) void wide_strip_kernel(
   store8<ZS_F32>(part + part_stride + c, 8, db);
 }
 
+// Calls f with whether a call's data are streamed; fp32's never are.
+template <int DT, typename F>
+void with_streaming(bool nt, F f) {
+  if constexpr (DT == ZS_F32)
+    f(std::integral_constant<bool, false>());
+  else
+    with_bool(nt, f);
+}
+
 // Workgroups of the backward pass, each with a part of dw and db: 1 M floats of parts of each,
 // 512 at least and 2048 at most, so that narrow rows leave enough on their way.
 int64_t grad_blocks(int64_t rows, int64_t width, const Shape& s) {
@@ -369,24 +409,19 @@ extern "C" int zs_layer_norm_forward(const void* x, int64_t x_stride, const void
   const bool nt = dtype != ZS_F32 && streams(rows * width * ((residual ? 3 : 1) * eb + (y ? eb : 0) + (codes ? 1 : 0)));
   const int group_lanes = codes ? group / 8 : 16;
   with_dtype(dtype, [&](auto DT) {
-    with_bool(nt, [&](auto NT) {
-      with_shape(s, [&](auto NC, auto T) {
-        auto go = [&](auto CODE) {
-          using E = elem_t<decltype(DT)::value>;
-          layer_norm_kernel<decltype(DT)::value, decltype(NT)::value, decltype(NC)::value,
-                            decltype(T)::value, decltype(CODE)::value>
-              <<<dim3((uint32_t)blocks), dim3(s.threads), 0, (hipStream_t)stream>>>(
-                  (const E*)x, x_stride, (const E*)residual, residual_stride, (const E*)weight,
-                  (const E*)bias, (E*)sum, sum_stride, (E*)y, y_stride, (uint8_t*)codes,
-                  (uint8_t*)scales, mean, rstd, rows, width, eps, 1.0 / (double)width, s.lanes,
-                  per, group_lanes);
-        };
-        if (!codes)
-          go(std::integral_constant<int, -1>());
-        else if (code == ZS_E2M1)
-          go(std::integral_constant<int, ZS_E2M1>());
-        else
-          with_code(code, go);
+    constexpr int kDt = decltype(DT)::value;
+    using E = elem_t<kDt>;
+    const RowArgs<kDt> g{(const E*)x, (const E*)residual, (const E*)weight, (const E*)bias, (E*)sum, (E*)y,
+                         x_stride, residual_stride, sum_stride, y_stride, (uint8_t*)codes,
+                         (uint8_t*)scales, mean, rstd, rows, (int32_t)width, s.lanes, per, code,
+                         group_lanes, eps, 1.0 / (double)width};
+    with_streaming<kDt>(nt, [&](auto NT) {
+      with_bool(codes != nullptr, [&](auto CODES) {
+        with_shape(s, [&](auto NC, auto T) {
+          layer_norm_kernel<kDt, decltype(NT)::value, decltype(NC)::value, decltype(T)::value,
+                            decltype(CODES)::value>
+              <<<dim3((uint32_t)blocks), dim3(s.threads), 0, (hipStream_t)stream>>>(g);
+        });
       });
     });
   });
@@ -443,7 +478,7 @@ extern "C" int zs_layer_norm_backward(const void* dy, int64_t dy_stride, const v
         wide_means_kernel<kDt><<<dim3((uint32_t)rows), dim3(1024), 0, (hipStream_t)stream>>>(
             (const E*)dy, dy_stride, (const E*)sum, sum_stride, (const E*)weight, mean, rstd, means,
             width);
-      with_bool(nt, [&](auto NT) {
+      with_streaming<kDt>(nt, [&](auto NT) {
         constexpr bool kNt = decltype(NT)::value;
         if (width > kHeldWidth) {
           wide_strip_kernel<kDt, kNt>
