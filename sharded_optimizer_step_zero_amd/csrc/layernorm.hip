@@ -194,22 +194,40 @@ struct GradRow {
   float mean, rstd;
 };
 
-template <int DT, bool NT, int NC, int T>
-__global__ __launch_bounds__(T) void layer_norm_grad_kernel(
+constexpr int kGradThreads = 512;
+
+// Two sums over a row's threads at once, one barrier.  `base` is the row's first wave.
+__device__ __forceinline__ f32x2 row_sums(f32x2 x, int lanes, int base, f32x2* slots) {
+  const int w = lanes < 64 ? lanes : 64;
+  for (int d = 1; d < w; d <<= 1) {
+    x[0] += __shfl_xor(x[0], d, 64);
+    x[1] += __shfl_xor(x[1], d, 64);
+  }
+  if (lanes <= 64) return x;
+  if ((threadIdx.x & 63) == 0) slots[threadIdx.x >> 6] = x;
+  __syncthreads();
+  f32x2 s = {};
+  for (int i = 0; i < lanes / 64; i++) s += slots[base + i];
+  return s;
+}
+
+template <int DT, bool NT, int NC>
+__global__ __launch_bounds__(kGradThreads) void layer_norm_grad_kernel(
     const elem_t<DT>* dy, int64_t dy_stride, const elem_t<DT>* sum, int64_t sum_stride,
     const elem_t<DT>* __restrict__ weight, const float* __restrict__ mean,
     const float* __restrict__ rstd, const elem_t<DT>* ds, int64_t ds_stride, elem_t<DT>* dx,
-    int64_t dx_stride, float* __restrict__ parts, int64_t part_stride, int64_t rows, int64_t width,
+    int64_t dx_stride, float* __restrict__ parts, int64_t part_stride, int64_t rows, int32_t width,
     int lanes, int rows_per_block) {
-  __shared__ float slots[2][2][16];
-  const int in_row = threadIdx.x & (lanes - 1);
-  const int sub = rows_per_block > 1 ? threadIdx.x / lanes : 0;
+  __shared__ f32x2 slots[2][kGradThreads / 64];
+  __shared__ __attribute__((aligned(16))) float all[kGradThreads * 8];
+  const int in_row = threadIdx.x & (lanes - 1), sub = threadIdx.x / lanes;
   const int64_t step = (int64_t)gridDim.x * rows_per_block;
   const float inv_width = 1.0f / (float)width;
+  const bool whole = width == lanes * NC * 8;
   f32x8 w[NC], dw[NC], db[NC];
 #pragma unroll
   for (int k = 0; k < NC; k++) {
-    const int64_t c = (int64_t)(k * lanes + in_row) * 8;
+    const int c = (k * lanes + in_row) * 8;
     w[k] = load8<DT>(weight + c, width - c);
     dw[k] = f32x8{};
     db[k] = f32x8{};
@@ -221,7 +239,7 @@ __global__ __launch_bounds__(T) void layer_norm_grad_kernel(
     r.rstd = rstd[from];
 #pragma unroll
     for (int k = 0; k < NC; k++) {
-      const int64_t c = (int64_t)(k * lanes + in_row) * 8;
+      const int c = (k * lanes + in_row) * 8;
       r.s[k] = load_row<DT, NT>(sum + from * sum_stride, c, width);
       r.dy[k] = load_row<DT, NT>(dy + from * dy_stride, c, width);
       r.ds[k] = Chunk<DT>{};
@@ -239,11 +257,15 @@ __global__ __launch_bounds__(T) void layer_norm_grad_kernel(
     if (row0 + step < rows) next = load(row + step);
     f32x8 h[NC], g[NC];
     f32x2 dot = {};
+    auto take = [&](const Chunk<DT>& x, int k) {  // zeros behind the row's end, and for no row
+      if (whole && row < rows) return widen<DT>(x);
+      const int left = row < rows ? width - (k * lanes + in_row) * 8 : 0;
+      return take8<DT>(x, left, width);
+    };
 #pragma unroll
     for (int k = 0; k < NC; k++) {
-      const int64_t left = row < rows ? width - (int64_t)(k * lanes + in_row) * 8 : 0;
-      h[k] = (take8<DT>(now.s[k], left, width) - now.mean) * now.rstd;
-      g[k] = take8<DT>(now.dy[k], left, width);  // zeros behind the row's end
+      h[k] = (take(now.s[k], k) - now.mean) * now.rstd;
+      g[k] = take(now.dy[k], k);
       dw[k] += g[k] * h[k];
       db[k] += g[k];
       g[k] *= w[k];
@@ -253,35 +275,27 @@ __global__ __launch_bounds__(T) void layer_norm_grad_kernel(
         dot[1] += g[k][i] * h[k][i];
       }
     }
-    const float mean_g = row_sum(dot[0], lanes, slots[turn][0]) * inv_width;
-    const float mean_gh = row_sum(dot[1], lanes, slots[turn][1]) * inv_width;
+    const f32x2 means = row_sums(dot, lanes, sub * lanes / 64, slots[turn]) * inv_width;
 #pragma unroll
     for (int k = 0; k < NC; k++) {
-      const int64_t c = (int64_t)(k * lanes + in_row) * 8, left = row < rows ? width - c : 0;
-      const f32x8 v = (g[k] - mean_g - h[k] * mean_gh) * now.rstd + take8<DT>(now.ds[k], left, width);
+      const int c = (k * lanes + in_row) * 8, left = row < rows ? width - c : 0;
+      const f32x8 v = (g[k] - means[0] - h[k] * means[1]) * now.rstd + take(now.ds[k], k);
       store8<DT, NT>(dx + row * dx_stride + c, left, v);
     }
   }
-  // narrow rows: the workgroup's rows' parts are added here, in order
   float* part = parts + blockIdx.x * 2 * part_stride;
-  if (rows_per_block > 1) {
-    __shared__ float all[2][256 * 8];
-    store8<ZS_F32>(all[0] + threadIdx.x * 8, 8, dw[0]);
-    store8<ZS_F32>(all[1] + threadIdx.x * 8, 8, db[0]);
-    __syncthreads();
-    if (sub != 0) return;
-    for (int i = 1; i < rows_per_block; i++) {
-      dw[0] += load8<ZS_F32>(all[0] + (i * lanes + in_row) * 8, 8);
-      db[0] += load8<ZS_F32>(all[1] + (i * lanes + in_row) * 8, 8);
-    }
-  }
 #pragma unroll
-  for (int k = 0; k < NC; k++) {
-    const int64_t c = (int64_t)(k * lanes + in_row) * 8;
-    if (c < width) {
-      store8<ZS_F32>(part + c, 8, dw[k]);
-      store8<ZS_F32>(part + part_stride + c, 8, db[k]);
+  for (int q = 0; q < 2 * NC; q++) {
+    const int k = q >> 1, c = (k * lanes + in_row) * 8;
+    f32x8 x = q & 1 ? db[k] : dw[k];
+    if (rows_per_block > 1) {  // the workgroup's rows' parts are added here, in order
+      if (q) __syncthreads();
+      store8<ZS_F32>(all + threadIdx.x * 8, 8, x);
+      __syncthreads();
+      if (sub == 0)
+        for (int i = 1; i < rows_per_block; i++) x += load8<ZS_F32>(all + (i * lanes + in_row) * 8, 8);
     }
+    if (sub == 0 && c < width) store8<ZS_F32>(part + (q & 1) * part_stride + c, 8, x);
   }
 }
 
@@ -354,17 +368,25 @@ void with_streaming(bool nt, F f) {
     with_bool(nt, f);
 }
 
-// Workgroups of the backward pass, each with a part of dw and db: 1 M floats of parts of each,
-// 512 at least and 2048 at most, so that narrow rows leave enough on their way.
-int64_t grad_blocks(int64_t rows, int64_t width, const Shape& s) {
-  if (width > kHeldWidth) {  // slices of the rows, for each strip
+// How the backward pass spreads rows of up to 8192 columns: as the forward, but always over
+// workgroups of 512, which add their rows' parts of dw and db, so that there are few parts (3001
+// x 1001: @@).
+Shape grad_shape(int64_t width) {
+  const Shape s = shape(width);
+  return {s.lanes, s.nc, kGradThreads};
+}
+
+// Workgroups of the backward pass, each with a part of dw and db: two on each compute unit.  Of
+// wide rows: slices of them for each strip.
+int64_t grad_blocks(int64_t rows, int64_t width) {
+  if (width > kHeldWidth) {
     const int64_t strips = (width + kStrip - 1) / kStrip, slices = 2048 / strips;
     return rows < slices ? rows : slices;
   }
-  const int64_t g = (2ll << 20) / width, most = g < 512 ? 512 : g > 2048 ? 2048 : g;
+  const Shape s = grad_shape(width);
   const int per = s.threads / s.lanes;
   const int64_t need = (rows + per - 1) / per;
-  return need < most ? need : most;
+  return need < 512 ? need : 512;
 }
 
 }  // namespace
@@ -430,7 +452,7 @@ extern "C" int zs_layer_norm_forward(const void* x, int64_t x_stride, const void
 
 extern "C" size_t zs_layer_norm_backward_bytes(int64_t rows, int64_t width) {
   if (rows < 0 || rows > 0x7fffffff || width < 1 || width > kMaxWidth) return 0;
-  const size_t parts = (size_t)grad_blocks(rows, width, shape(width));
+  const size_t parts = (size_t)grad_blocks(rows, width);
   const size_t means = width > kHeldWidth ? up256((size_t)rows * 8) : 0;
   return up256(parts * 2 * part_stride_of(width) * 4) + means + 256;
 }
@@ -463,9 +485,9 @@ extern "C" int zs_layer_norm_backward(const void* dy, int64_t dy_stride, const v
   if (!workspace || !al(workspace, 256)) return fail(who, "the workspace is NULL or not 256-byte aligned");
   if (workspace_bytes < zs_layer_norm_backward_bytes(rows, width))
     return fail(who, "the workspace is too small");
-  const Shape s = shape(width);
+  const Shape s = grad_shape(width);
   const int per = s.threads / s.lanes;
-  const int64_t blocks = grad_blocks(rows, width, s);
+  const int64_t blocks = grad_blocks(rows, width);
   const int64_t stride = part_stride_of(width);
   const bool nt = dtype != ZS_F32 && streams(rows * width * eb * (grad_sum ? 4 : 3));
   float* parts = (float*)workspace;
@@ -489,19 +511,17 @@ extern "C" int zs_layer_norm_backward(const void* dy, int64_t dy_stride, const v
                                         rows, width);
           return;
         }
-        auto go = [&](auto NC, auto T) {
-          layer_norm_grad_kernel<kDt, kNt, decltype(NC)::value, decltype(T)::value>
-              <<<dim3((uint32_t)blocks), dim3(s.threads), 0, (hipStream_t)stream>>>(
+        auto go = [&](auto NC) {
+          layer_norm_grad_kernel<kDt, kNt, decltype(NC)::value>
+              <<<dim3((uint32_t)blocks), dim3(kGradThreads), 0, (hipStream_t)stream>>>(
                   (const E*)dy, dy_stride, (const E*)sum, sum_stride, (const E*)weight, mean, rstd,
                   (const E*)grad_sum, grad_sum_stride, (E*)grad_x, grad_x_stride, parts, stride,
-                  rows, width, s.lanes, per);
+                  rows, (int32_t)width, s.lanes, per);
         };
-        if (s.threads == 512)
-          go(std::integral_constant<int, 2>(), std::integral_constant<int, 512>());
-        else if (s.nc == 2)
-          go(std::integral_constant<int, 2>(), std::integral_constant<int, 256>());
+        if (s.nc == 1)
+          go(std::integral_constant<int, 1>());
         else
-          go(std::integral_constant<int, 1>(), std::integral_constant<int, 256>());
+          go(std::integral_constant<int, 2>());
       });
     });
   if (int rc = launched(who)) return rc;
