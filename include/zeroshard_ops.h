@@ -257,7 +257,8 @@ int zs_mx4_product(const void *x_codes, const void *x_scales, const void *w_code
 #define ZS_HINGE 1
 #define ZS_SQUARED 2
 
-/* Workspace of zs_prefer_forward; 0 when a size is out of range. */
+/* Workspace of zs_prefer_forward; 0 when a size is out of range, 256 where none is used (it may be
+ * NULL then). */
 size_t zs_prefer_workspace_bytes(int64_t tokens, int64_t pairs);
 
 /*

@@ -1,9 +1,12 @@
 // clip.hip -- the gradient norm over many tensors of any 16- or 32-bit types, and their clipping
 // by it: sumsq = sum of g^2, c = min(1, max / (sqrt(sumsq) + 1e-6)), out = c g.
 //
-// The tensors are laid out once as a table of pieces of up to 16384 elements, each with its
+// The tensors are laid out once as a table of pieces of up to 4096 elements, each with its
 // addresses and types, so that ten thousand small tensors and one large matrix are the same
-// kind of work and a call is two or three launches however many there are.  Squares are exact
+// kind of work and a call is two or three launches however many there are.  A wave takes every
+// n-th piece by itself: what a small tensor takes is the way to its elements, and there are
+// 8192 waves on it at once (pieces of 16384 by workgroups: 118 us
+// for ten thousand tensors of up to 4096 and four of 4096 x 4096, now 115).  Squares are exact
 // in fp64 (24 bits each) and finite whatever the element, and are summed there: a workgroup
 // takes every n-th piece, and a second kernel adds the workgroups' sums in order.
 //
@@ -19,9 +22,9 @@ namespace zs {
 namespace ops {
 namespace {
 
-constexpr int64_t kPiece = 16384;
+constexpr int64_t kPiece = 4096;
 constexpr int64_t kMaxPieces = 1ll << 26;
-constexpr int kGroups = 2048;  // workgroups of a pass over the pieces
+constexpr int kGroups = 2048;  // workgroups of a pass over the pieces, of four waves
 
 struct Piece {
   const void* grad;
@@ -32,16 +35,44 @@ struct Piece {
 };
 static_assert(sizeof(Piece) == 32, "the table's format");
 
+// Calls f(first element, eight elements, how many of them exist) for a lane's chunks of a piece,
+// whose loads come first: all eight of a whole piece, two at a time otherwise.
+template <int DT, typename F>
+__device__ __forceinline__ void each_chunk(const void* grad, int32_t n, F f) {
+  const elem_t<DT>* p = (const elem_t<DT>*)grad;
+  constexpr int kChunks = kPiece / (64 * 8);
+  const int32_t at = (threadIdx.x & 63) * 8;
+  if (n == kPiece) {
+    constexpr int kAtOnce = DT == ZS_F32 ? kChunks / 2 : kChunks;
+#pragma unroll
+    for (int q = 0; q < kChunks; q += kAtOnce) {
+      Chunk<DT> x[kAtOnce];
+#pragma unroll
+      for (int i = 0; i < kAtOnce; i++) x[i] = load_chunk<DT>(p + at + (q + i) * 512, 8);
+#pragma unroll
+      for (int i = 0; i < kAtOnce; i++) f(at + (q + i) * 512, widen<DT>(x[i]), 8);
+    }
+    return;
+  }
+  for (int32_t c0 = 0; c0 < n; c0 += 2 * 512) {
+    Chunk<DT> x[2];
+#pragma unroll
+    for (int i = 0; i < 2; i++) x[i] = load_row<DT>(p, c0 + at + i * 512, n);
+#pragma unroll
+    for (int i = 0; i < 2; i++) {
+      const int32_t c = c0 + at + i * 512;
+      f(c, take8<DT>(x[i], n - c, n), n - c);
+    }
+  }
+}
+
 template <int DT>
 __device__ __forceinline__ double piece_squares(const void* grad, int32_t n) {
-  const elem_t<DT>* p = (const elem_t<DT>*)grad;
   double s = 0.0;
-#pragma unroll 4
-  for (int32_t c = threadIdx.x * 8; c < n; c += 256 * 8) {
-    const f32x8 v = load8<DT>(p + c, n - c);
+  each_chunk<DT>(grad, n, [&](int32_t, f32x8 v, int32_t) {
 #pragma unroll
     for (int i = 0; i < 8; i++) s = __builtin_fma((double)v[i], (double)v[i], s);
-  }
+  });
   return s;
 }
 
@@ -55,13 +86,21 @@ __device__ __forceinline__ double block_sum(double x, double* slots) {
   return s;
 }
 
+// A wave's first piece, the same in all of its lanes.
+__device__ __forceinline__ int64_t first_piece() {
+  return (int64_t)blockIdx.x * 4 + __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
+}
+
 __global__ __launch_bounds__(256) void squares_kernel(const Piece* __restrict__ pieces,
                                                       int64_t n_pieces,
                                                       double* __restrict__ parts) {
   __shared__ double slots[4];
   double s = 0.0;
-  for (int64_t i = blockIdx.x; i < n_pieces; i += gridDim.x) {
-    const Piece p = pieces[i];
+  const int64_t step = gridDim.x * 4, first = first_piece();
+  Piece next = pieces[first < n_pieces ? first : 0];  // one ahead
+  for (int64_t i = first; i < n_pieces; i += step) {
+    const Piece p = next;
+    if (i + step < n_pieces) next = pieces[i + step];
     if (p.dtype == ZS_F32)
       s += piece_squares<ZS_F32>(p.grad, p.n);
     else if (p.dtype == ZS_BF16)
@@ -93,11 +132,10 @@ struct Factor {
 
 template <int DT, int OT>
 __device__ __forceinline__ void scale_piece(const Piece& p, Factor c) {
-  const elem_t<DT>* from = (const elem_t<DT>*)p.grad;
   elem_t<OT>* to = (elem_t<OT>*)p.out;
-#pragma unroll 4
-  for (int32_t k = threadIdx.x * 8; k < p.n; k += 256 * 8)
-    store8<OT>(to + k, p.n - k, load8<DT>(from + k, p.n - k) * c.first * c.second);
+  each_chunk<DT>(p.grad, p.n, [&](int32_t k, f32x8 v, int32_t left) {
+    store8<OT>(to + k, left, v * c.first * c.second);
+  });
 }
 
 __global__ __launch_bounds__(256) void scale_kernel(const Piece* __restrict__ pieces,
@@ -108,8 +146,12 @@ __global__ __launch_bounds__(256) void scale_kernel(const Piece* __restrict__ pi
   if (norm_out && blockIdx.x == 0 && threadIdx.x == 0) *norm_out = norm;
   const double q = (double)max_norm / (norm + 1e-6);
   const Factor c(q > 1.0 ? 1.0 : q);  // NaN goes through
-  for (int64_t i = blockIdx.x; i < n_pieces; i += gridDim.x) {
-    const Piece p = pieces[n_pieces - 1 - i];
+  const int64_t step = gridDim.x * 4, first = first_piece();
+  if (first >= n_pieces) return;
+  Piece next = pieces[n_pieces - 1 - first];
+  for (int64_t i = first; i < n_pieces; i += step) {
+    const Piece p = next;
+    if (i + step < n_pieces) next = pieces[n_pieces - 1 - i - step];
     // nowhere to go, or in place and unclipped: as it is
     if (!p.out || (p.grad == p.out && c.second == 1.0f)) continue;
     auto go = [&](auto DT) {
@@ -218,16 +260,19 @@ extern "C" int zs_grads_table(const zs_grad_tensor* list, int64_t n, void* table
   } catch (const std::bad_alloc&) {
     return fail(who, "no host memory to check the list with");
   }
+  // whole pieces first: the last of a pass, which not every wave has, are short
   Piece* to = (Piece*)table;
-  for (int64_t i = 0; i < n; i++) {
-    const zs_grad_tensor& t = list[i];
-    each_run(t, [&](const void* g, void* o, int64_t m) {
-      for (int64_t at = 0; at < m; at += kPiece, to++)
-        *to = Piece{(const uint8_t*)g + at * elem_bytes(t.dtype),
-                    o ? (uint8_t*)o + at * elem_bytes(t.out_dtype) : nullptr,
-                    (int32_t)std::min(kPiece, m - at), t.dtype, o ? t.out_dtype : t.dtype, 0};
-    });
-  }
+  for (const bool whole : {true, false})
+    for (int64_t i = 0; i < n; i++) {
+      const zs_grad_tensor& t = list[i];
+      each_run(t, [&](const void* g, void* o, int64_t m) {
+        const int64_t rest = m / kPiece * kPiece;
+        for (int64_t at = whole ? 0 : rest; at < (whole ? rest : m); at += kPiece)
+          *to++ = Piece{(const uint8_t*)g + at * elem_bytes(t.dtype),
+                        o ? (uint8_t*)o + at * elem_bytes(t.out_dtype) : nullptr,
+                        (int32_t)std::min(kPiece, m - at), t.dtype, o ? t.out_dtype : t.dtype, 0};
+      });
+    }
   return ZS_OK;
 }
 
@@ -244,7 +289,7 @@ extern "C" int zs_grads_sumsq(const void* table, int64_t pieces, double* sumsq, 
   if (!al(sumsq, 8) || !al(table, 32)) return fail(who, "a buffer is not aligned to its elements");
   if (!workspace || !al(workspace, 256)) return fail(who, "the workspace is NULL or not 256-byte aligned");
   if (workspace_bytes < zs_grads_workspace_bytes(pieces)) return fail(who, "the workspace is too small");
-  const int32_t blocks = (int32_t)std::min<int64_t>(pieces, kGroups);
+  const int32_t blocks = (int32_t)std::min<int64_t>((pieces + 3) / 4, kGroups);
   if (blocks)
     squares_kernel<<<dim3((uint32_t)blocks), dim3(256), 0, (hipStream_t)stream>>>(
         (const Piece*)table, pieces, (double*)workspace);
@@ -262,7 +307,7 @@ extern "C" int zs_grads_clip(const void* table, int64_t pieces, float max_norm,
   if (!sumsq || (pieces && !table)) return fail(who, "NULL buffer");
   if (!al(sumsq, 8) || !al(norm_out, 8) || !al(table, 32))
     return fail(who, "a buffer is not aligned to its elements");
-  const int32_t blocks = (int32_t)std::max<int64_t>(1, std::min<int64_t>(pieces, kGroups));
+  const int32_t blocks = (int32_t)std::max<int64_t>(1, std::min<int64_t>((pieces + 3) / 4, kGroups));
   scale_kernel<<<dim3((uint32_t)blocks), dim3(256), 0, (hipStream_t)stream>>>(
       (const Piece*)table, pieces, max_norm, sumsq, norm_out);
   return launched(who);

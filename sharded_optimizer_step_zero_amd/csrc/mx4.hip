@@ -3,8 +3,11 @@
 // Packing: a group's scale is the least power of two that brings it within 6, its codes the
 // elements over that scale rounded to {0, 1/2, 1, 3/2, 2, 3, 4, 6}, ties to even: 17 bytes for 32
 // elements.  Bound by HBM.  Along rows a lane has 8 elements and a group's maximum is one over
-// 4 neighbouring lanes.  Along columns (the transpose's rows) a tile of 128 x 128 goes through
-// LDS and a lane takes 32 rows of two columns; with both wanted the tile is read once.
+// 4 neighbouring lanes.  Along columns (the transpose's rows) a lane has 32 rows of four columns in
+// registers, so that a column's group is its own; with both wanted a row's group is eight
+// lanes', and the matrix is read once.  16-bit elements are compared and rounded as they are, two
+// at a time.  22016 x 4096 bf16 both ways 57 us (4.8 TB/s), rows 38 (6.0); 8192 x 22016 127 and 87.
+// (A tile of 128 x 128 turned in LDS, its 16-byte and single-byte pieces written apart: 150.)
 //
 // The product: out[t][n] = sum_k x[t][k] w[n][k] of the values codes * scales, on 16x16x128
 // matrix instructions that take the scales themselves (4-bit in, fp32 sums), one rounding at
@@ -84,66 +87,222 @@ __global__ __launch_bounds__(256) void pack_rows_kernel(const elem_t<DT>* __rest
   if ((chunk & 3) == 0) scales[scale4_at(row, group, rows)] = (uint8_t)(group < groups ? byte : 127u);
 }
 
-// A tile of 128 x 128: its rows' groups where ROWS, and its columns'.
-template <int DT, bool ROWS>
-__global__ __launch_bounds__(256) void pack_tile_kernel(
+// The largest of a group's eight lanes (four elements each), in each half of a word by itself.
+template <typename MAX>
+__device__ __forceinline__ uint32_t eight_lanes(uint32_t m, MAX max) {
+  m = max(m, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)m, 0xb1, 0xf, 0xf, true));   // lane ^ 1
+  m = max(m, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)m, 0x4e, 0xf, 0xf, true));   // lane ^ 2
+  return max(m, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)m, 0x141, 0xf, 0xf, true));  // 7 - lane
+}
+
+// A group's scale byte, and the scale for the instruction that encodes: it takes the exponent
+// field only, which is 0 for 2^-127 too.
+__device__ __forceinline__ uint32_t byte4(float amax, float* scale) {
+  const uint32_t b = scale_byte<ZS_E2M1>(amax);
+  *scale = __uint_as_float(b << 23);
+  return b;
+}
+
+// From so many blocks of 256 x 256 on; below, 64 x 256, so that the card has work.
+constexpr int64_t kLargeBlocks = 512;
+
+// WAVES * 32 rows x 256 columns: a lane has 32 rows of four columns, so that a group along columns
+// is one lane's and a group along rows eight lanes'.  ROWS: both, else along columns only.
+template <int DT, bool ROWS, int WAVES>
+__global__ __launch_bounds__(WAVES * 64, DT == ZS_F32 ? 2 : 4) void pack_both_kernel(
     const elem_t<DT>* __restrict__ x, int64_t x_stride, uint8_t* __restrict__ codes,
     uint8_t* __restrict__ scales, uint8_t* __restrict__ codes_t, uint8_t* __restrict__ scales_t,
     int64_t rows, int64_t width, uint32_t tiles_down) {
-  typedef elem_t<DT> pair_t __attribute__((ext_vector_type(2)));
-  __shared__ __attribute__((aligned(16))) elem_t<DT> tile[128][128];
-  const int64_t r0 = (int64_t)(blockIdx.x % tiles_down) * 128;
-  const int64_t c0 = (int64_t)(blockIdx.x / tiles_down) * 128;
-  const int tid = threadIdx.x;
+  __shared__ __attribute__((aligned(16))) u32x4 turned[256 * WAVES];
+  __shared__ uint8_t bytes[256 * WAVES];
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));  // rows are scalars
+  const int64_t r0 = (int64_t)(blockIdx.x % tiles_down) * (WAVES * 32), row0 = r0 + wave * 32;
+  const int64_t c0 = (int64_t)(blockIdx.x / tiles_down) * 256;
+  const int c = lane * 4;  // in the block
   const int64_t groups = groups_of(width), groups_t = groups_of(rows);
-  Chunk<DT> in[8];
+  constexpr bool kWide = DT == ZS_F32;
+  constexpr int kWords = kWide ? 4 : 2;
+  uint32_t w[32][kWords];
+  const elem_t<DT>* p = x + row0 * x_stride + c0;
+  const int64_t there = width - c0;  // columns that exist
+  if (row0 + 32 <= rows && there >= 256) {
 #pragma unroll
-  for (int k = 0; k < 8; k++) {
-    const int64_t row = r0 + (tid >> 4) + k * 16, c = c0 + (tid & 15) * 8;
-    in[k] = Chunk<DT>{};
-    if (row < rows && c < width) in[k] = load_chunk<DT>(x + row * x_stride + c, width - c);
+    for (int i = 0; i < 32; i++) {
+      if constexpr (kWide)
+        __builtin_memcpy(w[i], (const u32x4_any*)(p + i * x_stride + c), 16);
+      else
+        __builtin_memcpy(w[i], (const u32x2_any*)(p + i * x_stride + c), 8);
+    }
+  } else if (there >= 4) {
+    // Without a branch in a lane: where the row ends before the lane's elements do, its last
+    // four, which move into place.
+    const int from = c + 4 <= there ? c : (int)there - 4, by = c - from;
+#pragma unroll
+    for (int i = 0; i < 32; i++) {
+      const elem_t<DT>* q = x + (row0 + i < rows ? row0 + i : rows - 1) * x_stride + c0;
+      if constexpr (kWide)
+        __builtin_memcpy(w[i], (const u32x4_any*)(q + from), 16);
+      else
+        __builtin_memcpy(w[i], (const u32x2_any*)(q + from), 8);
+    }
+#pragma unroll
+    for (int i = 0; i < 32; i++) {
+      const bool none = row0 + i >= rows;
+      if constexpr (kWide) {
+#pragma unroll
+        for (int k = 0; k < 4; k++) w[i][k] = by & 1 ? (k < 3 ? w[i][k + 1 & 3] : 0u) : w[i][k];
+#pragma unroll
+        for (int k = 0; k < 4; k++) w[i][k] = by & 2 ? (k < 2 ? w[i][k + 2 & 3] : 0u) : w[i][k];
+#pragma unroll
+        for (int k = 0; k < 4; k++) w[i][k] = none || by >= 4 ? 0u : w[i][k];
+      } else {
+        uint64_t v;
+        __builtin_memcpy(&v, w[i], 8);
+        v = none || by >= 4 ? 0ull : v >> (by * 16 & 63);
+        __builtin_memcpy(w[i], &v, 8);
+      }
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 32; i++) {
+      elem_t<DT> e[4];
+#pragma unroll
+      for (int k = 0; k < 4; k++)
+        e[k] = row0 + i < rows && c + k < there ? p[i * x_stride + c + k] : (elem_t<DT>)0.0f;
+      __builtin_memcpy(w[i], e, sizeof(w[i]));
+    }
   }
+  typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
+  auto max16 = [](uint32_t a, uint32_t b) {
+    return __builtin_bit_cast(uint32_t, __builtin_elementwise_max(__builtin_bit_cast(u16x2, a), __builtin_bit_cast(u16x2, b)));
+  };
+  auto max32 = [](uint32_t a, uint32_t b) { return a > b ? a : b; };
+  // a magnitude's bits as fp32 (16-bit types: in the low half)
+  auto value = [](uint32_t bits) {
+    if constexpr (DT == ZS_F32) return __uint_as_float(bits);
+    if constexpr (DT == ZS_BF16) return __uint_as_float(bits << 16);
+    return (float)__builtin_bit_cast(_Float16, (uint16_t)bits);
+  };
+  // two elements' codes into byte AT of a word; 16-bit types: both in `a`
+  auto encode = [](auto AT, uint32_t old, uint32_t a, uint32_t b, float scale) {
+    constexpr int at = decltype(AT)::value;
+    typedef elem_t<DT> pair_t __attribute__((ext_vector_type(2)));
+    if constexpr (DT == ZS_F32)
+      return (uint32_t)__builtin_amdgcn_cvt_scalef32_pk_fp4_f32((int)old, __uint_as_float(a), __uint_as_float(b), scale, at);
+    else if constexpr (DT == ZS_BF16)
+      return (uint32_t)__builtin_amdgcn_cvt_scalef32_pk_fp4_bf16((int)old, __builtin_bit_cast(pair_t, a), scale, at);
+    else
+      return (uint32_t)__builtin_amdgcn_cvt_scalef32_pk_fp4_f16((int)old, __builtin_bit_cast(pair_t, a), scale, at);
+  };
+  std::integral_constant<int, 0> b0;
+  std::integral_constant<int, 1> b1;
+  std::integral_constant<int, 2> b2;
+  std::integral_constant<int, 3> b3;
+
+  uint32_t columns[kWords] = {};  // the columns' largest magnitudes, as the elements lie
+  const int64_t group0 = c0 / 32;
+  const bool exists = group0 + (lane >> 3) < groups;
+  uint32_t eighth = 0;  // of eight rows, the scale byte of the one that this lane writes
 #pragma unroll
-  for (int k = 0; k < 8; k++) {
-    const int r = (tid >> 4) + k * 16, chunk = tid & 15;
-    *(Chunk<DT>*)&tile[r][chunk * 8] = in[k];
+  for (int i = 0; i < 32; i += 2) {
+    uint32_t m[2];
+#pragma unroll
+    for (int q = 0; q < 2; q++) {
+      uint32_t s[kWords];
+#pragma unroll
+      for (int k = 0; k < kWords; k++) {
+        s[k] = w[i + q][k] & (kWide ? 0x7fffffffu : 0x7fff7fffu);
+        columns[k] = kWide ? max32(columns[k], s[k]) : max16(columns[k], s[k]);
+      }
+      if constexpr (kWide)
+        m[q] = max32(max32(s[0], s[1]), max32(s[2], s[3]));
+      else
+        m[q] = max16(s[0], s[1]);
+    }
     if (ROWS) {
-      const f32x8 v = widen<DT>(in[k]);
-      uint32_t byte;
-      const uint32_t w = quantise4(v, group_amax(v, 4), &byte);
-      const int64_t row = r0 + r, group = c0 / 32 + (chunk >> 2);
-      if (row < rows) {
-        if (group < groups) *(uint32_t*)(codes + row * groups * 16 + c0 / 2 + chunk * 4) = w;
-        if ((chunk & 3) == 0)
-          scales[scale4_at(row, group, rows)] = (uint8_t)(group < groups ? byte : 127u);
+      if constexpr (kWide) {
+        m[0] = eight_lanes(m[0], max32);
+        m[1] = eight_lanes(m[1], max32);
+      } else {  // two rows in a word
+        uint32_t both = max16(__builtin_amdgcn_perm(m[1], m[0], 0x05040100), __builtin_amdgcn_perm(m[1], m[0], 0x07060302));
+        both = eight_lanes(both, max16);
+        m[0] = both & 0xffffu;
+        m[1] = both >> 16;
+      }
+#pragma unroll
+      for (int q = 0; q < 2; q++) {
+        float scale;
+        const uint32_t byte = byte4(value(m[q]), &scale);
+        uint32_t code;
+        if constexpr (kWide)
+          code = encode(b1, encode(b0, 0u, w[i + q][0], w[i + q][1], scale), w[i + q][2], w[i + q][3], scale);
+        else
+          code = encode(b1, encode(b0, 0u, w[i + q][0], 0u, scale), w[i + q][1], 0u, scale);
+        if (byte == 255u) code = 0;
+        if ((lane & 7) == ((i + q) & 7)) eighth = byte;
+        if (row0 + i + q < rows && exists)
+          *(uint16_t*)(codes + (row0 + i + q) * groups * 16 + c0 / 2 + lane * 2) = (uint16_t)code;
+      }
+      if ((i & 7) == 6) {
+        const int64_t row = row0 + i - 6 + (lane & 7);
+        if (row < rows) scales[scale4_at(row, group0 + (lane >> 3), rows)] = (uint8_t)(exists ? eighth : 127u);
       }
     }
   }
-  __syncthreads();
-  const int lane = tid & 63, wave = tid >> 6;
-  pair_t p[32];
+  // The columns: 32 rows' codes are 16 bytes, which go through LDS so that a column's groups are
+  // written together.  A column's place for a wave is turned by its lane: no bank is met twice.
 #pragma unroll
-  for (int i = 0; i < 32; i++) p[i] = *(const pair_t*)&tile[wave * 32 + i][lane * 2];
-  const int64_t group = r0 / 32 + wave;
-#pragma unroll
-  for (int h = 0; h < 2; h++) {
-    const int64_t col = c0 + lane * 2 + h;
-    if (col >= width) return;
-    f32x8 v[4];
-    uint32_t m = 0;
+  for (int k = 0; k < 4; k++) {
+    float scale;
+    const uint32_t bits = kWide ? columns[k] : (k & 1 ? columns[k >> 1] >> 16 : columns[k >> 1] & 0xffffu);
+    const uint32_t byte = byte4(value(bits), &scale);
+    u32x4 word;
 #pragma unroll
     for (int q = 0; q < 4; q++) {
-#pragma unroll
-      for (int i = 0; i < 8; i++) v[q][i] = (float)p[q * 8 + i][h];
-      const uint32_t a = amax_bits(v[q]);
-      m = a > m ? a : m;
+      uint32_t code = 0;
+      auto two = [&](auto AT) {
+        const int i = q * 8 + decltype(AT)::value * 2;
+        if constexpr (kWide)
+          code = encode(AT, code, w[i][k], w[i + 1][k], scale);
+        else
+          code = encode(AT, code, __builtin_amdgcn_perm(w[i + 1][k >> 1], w[i][k >> 1], k & 1 ? 0x07060302 : 0x05040100), 0u, scale);
+      };
+      two(b0);
+      two(b1);
+      two(b2);
+      two(b3);
+      word[q] = byte == 255u ? 0u : code;
     }
-    u32x4 w;
-    uint32_t byte;
+    const int col = lane * 4 + k;
+    turned[col * WAVES + (wave ^ (lane & (WAVES - 1)))] = word;
+    bytes[col * WAVES + wave] = (uint8_t)byte;
+  }
+  __syncthreads();
+  const int64_t g0 = r0 / 32;
 #pragma unroll
-    for (int q = 0; q < 4; q++) w[q] = quantise4(v[q], __uint_as_float(m), &byte);
-    if (group < groups_t) *(u32x4*)(codes_t + (col * groups_t + group) * 16) = w;
-    scales_t[scale4_at(col, group, width)] = (uint8_t)(group < groups_t ? byte : 127u);
+  for (int n = 0; n < 4; n++) {
+    const int at = threadIdx.x + n * WAVES * 64, col = at / WAVES, g = at % WAVES;
+    if (c0 + col < width && g0 + g < groups_t)
+      *(u32x4*)(codes_t + ((c0 + col) * groups_t + g0 + g) * 16) = turned[col * WAVES + (g ^ (col >> 2 & (WAVES - 1)))];
+  }
+  // scale bytes: a wave's groups g and g + 4 are neighbours
+  if constexpr (WAVES == 8) {
+#pragma unroll
+    for (int n = 0; n < 2; n++) {
+      const int at = threadIdx.x + n * 512, col = at / 4, g = at % 4;
+      if (c0 + col >= width) continue;
+      const uint32_t lo = g0 + g < groups_t ? bytes[col * 8 + g] : 127u;
+      const uint32_t hi = g0 + g + 4 < groups_t ? bytes[col * 8 + g + 4] : 127u;
+      *(uint16_t*)(scales_t + scale4_at(c0 + col, g0 + g, width)) = (uint16_t)(lo | hi << 8);
+    }
+  } else {
+#pragma unroll
+    for (int n = 0; n < 4; n++) {
+      const int at = threadIdx.x + n * WAVES * 64, col = at / WAVES, g = at % WAVES;
+      if (c0 + col < width)
+        scales_t[scale4_at(c0 + col, g0 + g, width)] = g0 + g < groups_t ? bytes[at] : (uint8_t)127;
+    }
   }
 }
 
@@ -763,15 +922,24 @@ extern "C" int zs_mx4_pack(const void* x, int64_t x_stride, void* codes, void* s
     });
     return launched(who);
   }
-  // tiles past the end too: they write the scales of groups that fill a span up
-  const int64_t down = spans_t * 4, across = (codes ? spans * 4 : (width + 127) / 128);
+  // blocks past the end too: they write the scales of groups that fill a span up
+  const int64_t across = codes ? spans * 2 : (width + 255) / 256;
+  const bool large = spans_t * 2 * across >= kLargeBlocks;
+  const int64_t down = spans_t * (large ? 2 : 8);
   if (down * across > 0xffffff) return fail(who, "too many elements for one call");
   with_dtype(dtype, [&](auto DT) {
+    constexpr int kDt = decltype(DT)::value;
     with_bool(codes != nullptr, [&](auto ROWS) {
-      pack_tile_kernel<decltype(DT)::value, decltype(ROWS)::value>
-          <<<dim3((uint32_t)(down * across)), dim3(256), 0, (hipStream_t)stream>>>(
-              (const elem_t<decltype(DT)::value>*)x, x_stride, (uint8_t*)codes, (uint8_t*)scales,
-              (uint8_t*)codes_t, (uint8_t*)scales_t, rows, width, (uint32_t)down);
+      auto go = [&](auto WAVES) {
+        pack_both_kernel<kDt, decltype(ROWS)::value, decltype(WAVES)::value>
+            <<<dim3((uint32_t)(down * across)), dim3(decltype(WAVES)::value * 64), 0, (hipStream_t)stream>>>(
+                (const elem_t<kDt>*)x, x_stride, (uint8_t*)codes, (uint8_t*)scales, (uint8_t*)codes_t,
+                (uint8_t*)scales_t, rows, width, (uint32_t)down);
+      };
+      if (large)
+        go(std::integral_constant<int, 8>());
+      else
+        go(std::integral_constant<int, 2>());
     });
   });
   return launched(who);

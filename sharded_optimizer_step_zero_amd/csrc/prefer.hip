@@ -246,9 +246,10 @@ extern "C" int zs_prefer_forward(const float* loss, const float* ref_loss, const
   if (!al(loss, 4) || !al(ref_loss, 4) || !al(pair_loss, 4) || !al(rewards, 4) || !al(margins, 4) ||
       !al(lengths, 4))
     return fail(who, "a buffer is not aligned to its elements");
-  if (!workspace || !al(workspace, 256)) return fail(who, "the workspace is NULL or not 256-byte aligned");
-  if (workspace_bytes < zs_prefer_workspace_bytes(tokens, pairs)) return fail(who, "the workspace is too small");
   const int64_t slices = slices_of(tokens, pairs);
+  if (slices > 1 && (!workspace || !al(workspace, 256)))
+    return fail(who, "the workspace is NULL or not 256-byte aligned");
+  if (workspace_bytes < zs_prefer_workspace_bytes(tokens, pairs)) return fail(who, "the workspace is too small");
   const hipStream_t st = (hipStream_t)stream;
   if (slices == 1) {
     pair_kernel<<<dim3((uint32_t)pairs), dim3(512), 0, st>>>(g);

@@ -41,7 +41,7 @@ ZS_SIGMOID, ZS_HINGE, ZS_SQUARED = 0, 1, 2
 
 
 class GradTensor(ctypes.Structure):
-    """zs_grad_tensor."""
+    """zs_grad_tensor: seven 64-bit words, the types in the last one's halves."""
     _fields_ = [("grad", ctypes.c_void_p), ("out", ctypes.c_void_p), ("rows", ctypes.c_int64),
                 ("width", ctypes.c_int64), ("grad_stride", ctypes.c_int64),
                 ("out_stride", ctypes.c_int64), ("dtype", ctypes.c_int32),
@@ -258,6 +258,9 @@ def _matrix(t, name, dtype=None, device=None, rows=None, width=None):
 
 
 def _vector(t, name, dtypes, device, n):
+    if t.dim() == 1 and t.shape[0] == n and t.dtype in dtypes and t.device == device and (
+            n <= 1 or t.stride(0) == 1):
+        return
     if t.dim() != 1 or t.shape[0] != n:
         raise ValueError(f"{name}: shape {tuple(t.shape)}, expected ({n},)")
     if t.dtype not in dtypes:
@@ -946,15 +949,17 @@ def preference_loss(loss, ref_loss, offsets, beta=0.1, kind="sigmoid", margin=0.
         _vector(ref_loss, "ref_loss", (torch.float32,), dev, tokens)
     k = _pick(_KINDS, kind, "kind")
     pairs = _pairs(offsets, mask, dev, tokens)
-    each = torch.empty(2, pairs, dtype=torch.float32, device=dev)
+    out = torch.empty(pairs, dtype=torch.float32, device=dev)
+    margins = torch.empty(pairs, dtype=torch.float32, device=dev)
     rewards = torch.empty(pairs, 2, dtype=torch.float32, device=dev)
     lengths = torch.empty(pairs, 2, dtype=torch.int32, device=dev)
-    out, margins = each.unbind()
-    ws = _workspace(workspace, _prefer_workspace_bytes(tokens, pairs), dev)
+    nbytes = _prefer_workspace_bytes(tokens, pairs)
+    ws = _workspace(workspace, nbytes, dev) if nbytes != 256 else None  # 256: it is not used
     _run(dev, _prefer_forward, loss.data_ptr(), ref_loss.data_ptr() if ref_loss is not None else
          None, offsets.data_ptr(), mask.data_ptr() if mask is not None else None, out.data_ptr(),
          rewards.data_ptr(), margins.data_ptr(), lengths.data_ptr(), tokens, pairs, beta, margin,
-         smoothing, k, int(average), _ID_BYTES[offsets.dtype], ws.data_ptr(), ws.numel())
+         smoothing, k, int(average), _ID_BYTES[offsets.dtype], ws.data_ptr() if ws is not None else
+         None, nbytes)
     return PreferenceOut(out, rewards, margins, lengths)
 
 
@@ -991,8 +996,6 @@ def preference_loss_backward(forward, offsets, grad_loss, tokens, beta=0.1, kind
 
 def _grad_rows(g, o, i):
     """A gradient and its output as rows of adjacent elements: (rows, width, strides)."""
-    if g.is_contiguous() and o.is_contiguous():
-        return 1, g.numel(), g.numel(), o.numel()
     for t, name in ((g, f"tensors[{i}]"), (o, f"out[{i}]")):
         if t.dim() != 2 or (t.stride(1) != 1 and t.shape[1] > 1) or (
                 t.stride(0) < t.shape[1] and t.shape[0] > 1):
@@ -1022,24 +1025,26 @@ class GradList:
         self.device = self.tensors[0].device
         if not self.tensors[0].is_cuda:
             raise ValueError(f"tensors: on {self.device}, expected a GPU")
-        records = []
-        for i, g in enumerate(self.tensors):
-            o = self.out[i] if self.out is not None else g
-            for t, name in ((g, f"tensors[{i}]"), (o, f"out[{i}]")):
-                if t.device != self.device:
-                    raise ValueError(f"{name}: on {t.device}, expected {self.device}")
-                _dtype(t, name)
-            if o.shape != g.shape:
-                raise ValueError(f"out[{i}]: shape {tuple(o.shape)}, expected {tuple(g.shape)}")
-            dg, do = _DTYPES[g.dtype], _DTYPES[o.dtype]
+        dev, codes = self.device, {(a, b): _DTYPES[a] | _DTYPES[b] << 32 for a in _DTYPES for b in _DTYPES}
+        records = []  # zs_grad_tensor, word by word
+        for i, (g, o) in enumerate(zip(self.tensors, self.out or self.tensors)):
+            code = codes.get((g.dtype, o.dtype))
+            if code is None or g.device != dev or o.device != dev or o.shape != g.shape:
+                raise ValueError(f"tensors[{i}]: {g.dtype} {tuple(g.shape)} on {g.device} to {o.dtype} "
+                                 f"{tuple(o.shape)} on {o.device}, expected types of {tuple(_DTYPES)} "
+                                 f"and one shape on {dev}")
+            if g.is_contiguous() and o.is_contiguous():
+                n = g.numel()
+                records.append((g.data_ptr(), o.data_ptr(), 1, n, n, n, code))
+                continue
             if g.dim() == 2 and not g.is_contiguous() and g.stride(0) == 1 and o.stride(0) == 1:
                 g, o = g.t(), o.t()
-            rows, width, gs, os_ = _grad_rows(g, o, i)
-            records.append(GradTensor(g.data_ptr(), o.data_ptr(), rows, width, gs, os_, dg, do))
-        self.pieces = zs_grads_pieces(records)
+            records.append((g.data_ptr(), o.data_ptr(), *_grad_rows(g, o, i), code))
+        words = torch.tensor(records, dtype=torch.int64, device="cpu")
+        self.pieces = int(_check(_grads_pieces(words.data_ptr(), len(records))))
         host = torch.empty(max(1, self.pieces) * 32, dtype=torch.uint8, device="cpu")
-        zs_grads_table(records, host.data_ptr(), host.numel())
-        self.table = host.to(self.device)
+        _check(_grads_table(words.data_ptr(), len(records), host.data_ptr(), host.numel()))
+        self.table = host.to(dev)
 
 
 def _grad_list(grads):

@@ -119,7 +119,7 @@ def test_prefer_backward_refusals(at, word):
 
 # ---------------------------------------------------------------- tables of gradients
 
-PIECE = 16384
+PIECE = 4096
 
 
 def record(grad, out, rows, width, gs=None, os_=None, dt=1, ot=1):
@@ -148,10 +148,13 @@ def test_grads_table():
     big = 2 * PIECE + 5
     got = table([record(P, 2 * P, 1, big, dt=0, ot=1), record(8 * P, 0, 3, 10, gs=16, dt=2),
                  record(16 * P, 16 * P, 0, 8), record(32 * P, 32 * P, 4, 6, dt=1)])
+    # whole pieces come first
     assert got == [(P, 2 * P, PIECE, 0, 1, 0), (P + 4 * PIECE, 2 * P + 2 * PIECE, PIECE, 0, 1, 0),
                    (P + 8 * PIECE, 2 * P + 4 * PIECE, 5, 0, 1, 0), (8 * P, 0, 10, 2, 2, 0),
                    (8 * P + 32, 0, 10, 2, 2, 0), (8 * P + 64, 0, 10, 2, 2, 0),
                    (32 * P, 32 * P, 24, 1, 1, 0)]
+    got = table([record(P, 2 * P, 1, 7), record(8 * P, 0, 1, PIECE)])
+    assert got == [(8 * P, 0, PIECE, 1, 1, 0), (P, 2 * P, 7, 1, 1, 0)]
     assert table([]) == []
     assert "small" in refused(ops.zs_grads_table, [record(P, P, 1, 8)], P, 31)
     assert "table" in refused(ops.zs_grads_table, [record(P, P, 1, 8)], 0, 32)
