@@ -706,8 +706,15 @@ __global__ __launch_bounds__(256, 1) void held_kernel(Mx4Args g) {
       __builtin_amdgcn_sched_barrier(0);
     }
   };
-  // every load has landed, and every wave has read what it reads
+  // Every load has landed, and every wave has read what it reads.  Loads and stores complete in
+  // the order in which they were issued: a whole tile's stores, which come after the loads
+  // waited for, may go on.
   auto meet = [] { asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory"); };
+  constexpr int kStores = DT == ZS_F32 ? 63 : F * 4;  // 64 in fp32, one more than can be asked for
+  auto meet_storing = [] {
+    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(kStores) : "memory");
+  };
+  bool storing = false;
 
   std::integral_constant<int, 0> c0;
   std::integral_constant<int, 1> c1;
@@ -748,7 +755,11 @@ __global__ __launch_bounds__(256, 1) void held_kernel(Mx4Args g) {
       }
       multiply(c0, no, no, fa, fb, ga, gb, lds, 1, 0, none);
       // the span's second step is there; its first one's place and the scales' are free
-      meet();
+      if (storing)
+        meet_storing();
+      else
+        meet();
+      storing = false;
       if (last && more) aim_loads(id + step);
       const bool any = !last || more;
       load_scales(last ? 0 : p + 1, any);
@@ -771,7 +782,8 @@ __global__ __launch_bounds__(256, 1) void held_kernel(Mx4Args g) {
       acc[i][k] = f32x4{};
       return x;
     };
-    if (m0 + B > g.m || n0 + B > g.n) {
+    storing = m0 + B <= g.m && n0 + B <= g.n;
+    if (!storing) {
 #pragma unroll
       for (int k = 0; k < F; k++) {
 #pragma unroll
