@@ -17,8 +17,7 @@
 //
 // All tiles take 256 k a step, two steps in LDS, which global memory is read straight into: a row
 // has 128 bytes there, a cache line of memory (64-byte pieces of lines have twice the requests,
-// which the L2 answers no faster than one a channel and cycle: 8192 x 4096 x 22016 took 430 us for
-// 360).  A row's chunk c of 16 bytes sits at c ^ (row & 7): no bank conflicts.  Rows past the edge
+// which the L2 answers no faster than one a channel and cycle: 8192 x 4096 x 22016 took 430 us).  A row's chunk c of 16 bytes sits at c ^ (row & 7): no bank conflicts.  Rows past the edge
 // and groups past the end read as zeros by the buffer loads' bounds check.
 //
 // Large products: 256 x 256, four waves of 128 x 128 whose sums fill the accumulation registers
@@ -27,14 +26,14 @@
 // under way for a step and a half, have landed and this one's place is free.  A workgroup goes
 // on from tile to tile: the next one's first loads are under way before the last one's
 // products end, and its rows leave through LDS in pieces of 256 bytes (32-byte pieces straight
-// from the registers: 402 us; 64-byte ones: 368).  Smaller products take 128 x 128 or 128 x 64
+// from the registers: 402 us; 64-byte ones: 368; these 360, and 338 streamed).  Smaller products take 128 x 128 or 128 x 64
 // tiles, two or three workgroups a compute unit.
 //
 // Few tokens: the weight is what is read, each of its rows by one workgroup, whose waves share
 // k out between them and add their sums in LDS.
 //
 // Measured, bf16 out: 8192 x 22016 x 4096 (tokens x width x features) 279 us, 5.3 PFLOP/s; 22016 x
-// 8192 x 4096 311 us; 8192 x 4096 x 22016, sixteen steps a tile and 360 MB to write, 360 us, 4.1
+// 8192 x 4096 311 us; 8192 x 4096 x 22016, sixteen steps a tile and 360 MB to write, 338 us, 4.4
 // PFLOP/s.  The clock gives way under the load: on zeros the first takes 232 us (6.4 PFLOP/s).
 #include <algorithm>
 
@@ -333,6 +332,7 @@ struct Mx4Args {
   int32_t tiles_m, tiles_n;
   void* c;
   int64_t ldc;
+  int32_t streaming;       // the output passes the last-level cache
 };
 
 template <int J>
@@ -811,17 +811,23 @@ __global__ __launch_bounds__(256, 1) void held_kernel(Mx4Args g) {
       uint8_t* to = stash + (lane & 15) * kStashRow + (lane >> 4) * 8;
       const uint8_t* from = stash + (lane >> 4) * kStashRow + (lane & 15) * 16;
       out = (elem_t<DT>*)g.c + (n0 + rb + (lane >> 4)) * g.ldc + m0 + ra + (lane & 15) * 8;
+      auto write = [&](auto NT) {
 #pragma unroll
-      for (int k = 0; k < F; k++) {
+        for (int k = 0; k < F; k++) {
 #pragma unroll
-        for (int i = 0; i < F; i++)
-          *(u32x2*)(to + i * 32) = __builtin_bit_cast(u32x2, __builtin_convertvector(sums(i, k), v4));
+          for (int i = 0; i < F; i++)
+            *(u32x2*)(to + i * 32) = __builtin_bit_cast(u32x2, __builtin_convertvector(sums(i, k), v4));
 #pragma unroll
-        for (int i = 0; i < 4; i++)
-          *(u32x4_any*)(out + i * 4 * g.ldc) = *(const u32x4*)(from + i * 4 * kStashRow);
-        __builtin_amdgcn_sched_barrier(0);
-        out += 16 * g.ldc;
-      }
+          for (int i = 0; i < 4; i++)
+            st16<decltype(NT)::value>(out + i * 4 * g.ldc, *(const u32x4*)(from + i * 4 * kStashRow));
+          __builtin_amdgcn_sched_barrier(0);
+          out += 16 * g.ldc;
+        }
+      };
+      if (g.streaming)
+        write(yes);
+      else
+        write(no);
     }
   }
   // no load is on its way into LDS any more
@@ -1006,6 +1012,9 @@ extern "C" int zs_mx4_product(const void* x_codes, const void* x_scales, const v
   g.groups = (int32_t)groups_of(width);
   g.c = out;
   g.ldc = out_stride;
+  // 8192 x 4096 x 22016 (360 MB) 338 us streamed and 369 not, 16384 x 8192 x 8192 (268 MB) 453 and
+  // 472, 16384 x 2048 x 8192 141 and 137; smaller outputs are read again from the cache
+  g.streaming = streams(tokens * features * elem_bytes(dtype));
   const hipStream_t st = (hipStream_t)stream;
   if (tokens <= kFewTokens) {
     const uint32_t blocks = (uint32_t)((features + 31) / 32);
