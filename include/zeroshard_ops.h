@@ -246,11 +246,21 @@ int zs_mx4_unpack(const void *codes, const void *scales, void *x, int64_t x_stri
  * out[t][n] = sum_k x[t][k] * w[n][k] of two matrices in the 4-bit form with rows of `width`
  * elements, summed in fp32 and rounded once to `dtype`.  (A linear layer's three products are
  * this one: y from x and w packed along rows, dx from dy along rows and w along columns, dw from
- * dy and x along columns.)  tokens and features <= 2^24, width <= 2^20, and fewer than 2^24 tiles.
+ * dy and x along columns.)  tokens and features <= 2^24, width <= 2^20, and fewer than 2^24
+ * tiles of 256 x 256.
  */
 int zs_mx4_product(const void *x_codes, const void *x_scales, const void *w_codes,
                    const void *w_scales, void *out, int64_t out_stride, int64_t tokens,
                    int64_t features, int64_t width, int32_t dtype, void *stream);
+
+/* Workspace of zs_mx4_linear; 0 when a size is out of range. */
+size_t zs_mx4_linear_bytes(int64_t tokens, int64_t width);
+
+/* The same for an x of `x_dtype`, which is packed along its rows into the workspace first. */
+int zs_mx4_linear(const void *x, int64_t x_stride, const void *w_codes, const void *w_scales,
+                  void *out, int64_t out_stride, int64_t tokens, int64_t features, int64_t width,
+                  int32_t x_dtype, int32_t dtype, void *workspace, size_t workspace_bytes,
+                  void *stream);
 
 /* kinds of preference loss */
 #define ZS_SIGMOID 0

@@ -15,7 +15,11 @@
 // Codes come from an output in fp64 (whose instructions take no longer than fp32's), rounded to
 // fp32 to nearest and, where that may have crossed the border between two codes or two scales, to
 // the odd side, so that each code is one rounding of y.  (The output in fp32 with an error bound,
-// and both of its ends encoded, took 260 us for @@.)
+// and both of its ends encoded, took 260 us for 193.)
+//
+// Bound by HBM.  Measured, bf16: forward at 16384 x 8192 with residual and 8-bit codes 193 us for
+// 943 MB (4.9 TB/s; the instructions for the codes are what keeps it from 5.9), backward at 32768 x 2048 101 us for 537 MB (5.3 TB/s), 16384 x 8192
+// 186 us (5.8), 8192 x 12288 in two passes 217 us.
 #include "rows.h"
 
 namespace zs {
@@ -370,7 +374,7 @@ void with_streaming(bool nt, F f) {
 
 // How the backward pass spreads rows of up to 8192 columns: as the forward, but always over
 // workgroups of 512, which add their rows' parts of dw and db, so that there are few parts (3001
-// x 1001: @@).
+// x 1001: 17.7 us for 19.9 with two thousand, a call's launches and Python included).
 Shape grad_shape(int64_t width) {
   const Shape s = shape(width);
   return {s.lanes, s.nc, kGradThreads};

@@ -30,7 +30,9 @@
 // tiles, two or three workgroups a compute unit.
 //
 // Few tokens: the weight is what is read, each of its rows by one workgroup, whose waves share
-// k out between them and add their sums in LDS.
+// k out between them and add their sums in LDS: 16 x 4096 x 22016 14 us (3.5 TB/s, weights from
+// HBM; a pass of 48 MB has about 3 us of start and end, and the tokens' codes come again for
+// every 32 features: one token 12 us).
 //
 // Measured, bf16 out: 8192 x 22016 x 4096 (tokens x width x features) 279 us, 5.3 PFLOP/s; 22016 x
 // 8192 x 4096 311 us; 8192 x 4096 x 22016, sixteen steps a tile and 360 MB to write, 338 us, 4.4
@@ -404,14 +406,15 @@ struct Side {
   uint32_t off[kLoads];
   int32_t chunk;
 
+  // `count` groups from span `first` on, of rows of `g`.
   __device__ __forceinline__ Side(const uint8_t* c, const uint8_t* s, int64_t row0, int64_t n,
-                                  int32_t g, int tid) {
+                                  int32_t g, int32_t first, int32_t count, int tid) {
     ld = (int64_t)g * 16;
     span = n * 16;
-    codes = c + row0 * ld;
-    scales = s + row0 * 16;
+    codes = c + row0 * ld + (int64_t)first * 256;
+    scales = s + row0 * 16 + first * span;
     rows = (int32_t)(n - row0 < R ? n - row0 : R);
-    groups = g;
+    groups = count;
     const int row = tid >> 3;
     chunk = (tid & 7) ^ (row & 7);  // whole eights of rows on, the same
 #pragma unroll
@@ -437,31 +440,40 @@ __device__ __forceinline__ i32x4 fragment(const uint8_t* tile, int half, int row
   return *(const i32x4*)(tile + row * 128 + chunk * 16 + f * 2048);
 }
 
-// Small products: BM x BN tiles, two waves by two, two or three workgroups a compute unit.
-template <int DT, int BM, int BN>
-__global__ __launch_bounds__(256, 2) void product_kernel(Mx4Args g) {
+// Small products: BM x BN tiles, two waves by two, two or three workgroups a compute unit; PARTS > 1:
+// k is divided among so many fours of waves, whose sums are added at the end.
+template <int DT, int BM, int BN, int PARTS>
+__global__ __launch_bounds__(256 * PARTS, 2) void product_kernel(Mx4Args g) {
   constexpr int kThreads = 256;
   constexpr int FM = BM / 32, FN = BN / 32;  // fragments of a wave
   using SideA = Side<BM, kThreads>;
   using SideB = Side<BN, kThreads>;
   constexpr int kTile = (BM + BN) * 128;
   constexpr int kScaleLoads = (BM + BN + kThreads - 1) / kThreads;
+  constexpr int kPart = 2 * kTile + kScaleLoads * kThreads * 16;  // bytes of LDS
   static_assert(BM % 64 == 0, "a wave's scales are of one operand");
-  __shared__ __attribute__((aligned(1024))) uint8_t lds[2 * kTile + kScaleLoads * kThreads * 16];
-  const int tid = threadIdx.x, lane = tid & 63;
+  static_assert(PARTS == 1 || kPart >= FM * FN * 256 * 16, "a part's sums fit its LDS");
+  __shared__ __attribute__((aligned(1024))) uint8_t all_lds[PARTS * kPart];
+  const int tid = threadIdx.x & 255, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int part = PARTS > 1 ? __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 8)) : 0;
+  uint8_t* const lds = all_lds + part * kPart;
   int32_t tm, tn;
   tile_of(g, &tm, &tn);
   const int64_t m0 = (int64_t)tm * BM, n0 = (int64_t)tn * BN;
-  const int steps = (g.groups + 7) / 8;
-  SideA a(g.a, g.as, m0, g.m, g.groups, tid);
-  SideB b(g.b, g.bs, n0, g.n, g.groups, tid);
+  // every part has as many steps, whose groups need not exist
+  const int each = ((g.groups + 15) / 16 + PARTS - 1) / PARTS;
+  const int before = part * each * 16 < g.groups ? part * each * 16 : g.groups;
+  const int mine = g.groups - before < each * 16 ? g.groups - before : each * 16;
+  const int steps = PARTS > 1 ? each * 2 : (g.groups + 7) / 8;
+  SideA a(g.a, g.as, m0, g.m, g.groups, before / 16, mine, tid);
+  SideB b(g.b, g.bs, n0, g.n, g.groups, before / 16, mine, tid);
   const uint32_t lds_at = (uint32_t)(uintptr_t)(ZS_LDS uint8_t*)lds + wave * 1024;
   const uint8_t* const scale_tile = lds + 2 * kTile;
 
   // The scales of span p: a load of a thread is 16 bytes, those of one row, A's rows and then B's.
   auto load_scales = [&](int p) {
-    const bool there = p * 2 < steps;
+    const bool there = p * 16 < mine;
     const u32x4 da = descriptor(a.scales + p * a.span, there ? a.rows * 16 : 0);
     const u32x4 db = descriptor(b.scales + p * b.span, there ? b.rows * 16 : 0);
 #pragma unroll
@@ -529,6 +541,25 @@ __global__ __launch_bounds__(256, 2) void product_kernel(Mx4Args g) {
   }
   // no load is on its way into LDS any more
   asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+
+  if constexpr (PARTS > 1) {  // the first part adds the others' sums, in order
+    __syncthreads();
+    if (part) {
+#pragma unroll
+      for (int i = 0; i < FM; i++)
+#pragma unroll
+        for (int k = 0; k < FN; k++) ((f32x4*)lds)[(i * FN + k) * 256 + tid] = acc[i][k];
+    }
+    __syncthreads();
+    if (part) return;
+#pragma unroll
+    for (int q = 1; q < PARTS; q++)
+#pragma unroll
+      for (int i = 0; i < FM; i++)
+#pragma unroll
+        for (int k = 0; k < FN; k++)
+          acc[i][k] += ((const f32x4*)(all_lds + q * kPart))[(i * FN + k) * 256 + tid];
+  }
 
   // acc[i][k][r]: feature m0 + ra + i*16 + (lane>>4)*4 + r, token n0 + rb + k*16 + (lane&15)
   const int64_t f0 = m0 + ra + (lane >> 4) * 4, t0 = n0 + rb + (lane & 15);
@@ -834,11 +865,10 @@ __global__ __launch_bounds__(256, 1) void held_kernel(Mx4Args g) {
   asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
 }
 
-// Few tokens: 32 features a workgroup, FN * 16 tokens, spans of k dealt out over eight waves.
+// Few tokens: FM * 16 features a workgroup, FN * 16 tokens, spans of k dealt out over eight waves.
 constexpr int kFewWaves = 8;
-template <int DT, int FN>
+template <int DT, int FM, int FN>
 __global__ __launch_bounds__(kFewWaves * 64) void few_kernel(Mx4Args g) {
-  constexpr int FM = 2;
   __shared__ f32x4 parts[kFewWaves][FM][FN][64];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int64_t m0 = (int64_t)blockIdx.x * FM * 16, n0 = (int64_t)blockIdx.y * FN * 16;
@@ -849,25 +879,47 @@ __global__ __launch_bounds__(kFewWaves * 64) void few_kernel(Mx4Args g) {
   for (int i = 0; i < FM; i++)
 #pragma unroll
     for (int k = 0; k < FN; k++) acc[i][k] = f32x4{};
+  // rows that do not exist are the last one's, and go nowhere
+  const uint8_t *pa[FM], *pb[FN], *qa[FM], *qb[FN];
+#pragma unroll
+  for (int i = 0; i < FM; i++) {
+    const int64_t row = m0 + i * 16 + (lane & 15) < g.m ? m0 + i * 16 + (lane & 15) : g.m - 1;
+    pa[i] = g.a + row * ld + (lane >> 4) * 16;
+    qa[i] = g.as + row * 16 + (lane >> 4) * 4;
+  }
+#pragma unroll
+  for (int k = 0; k < FN; k++) {
+    const int64_t row = n0 + k * 16 + (lane & 15) < g.n ? n0 + k * 16 + (lane & 15) : g.n - 1;
+    pb[k] = g.b + row * ld + (lane >> 4) * 16;
+    qb[k] = g.bs + row * 16 + (lane >> 4) * 4;
+  }
   for (int p = wave; p < spans; p += kFewWaves) {
     i32x4 fa[FM][4], fb[FN][4];
     uint32_t sa[FM], sb[FN];
-    // rows that do not exist are the last one's, and go nowhere; groups past the end are zeros
-    auto read = [&](const uint8_t* codes, const uint8_t* scales, int64_t row, int64_t rows,
-                    i32x4(&f)[4], uint32_t& s) {
-      row = row < rows ? row : rows - 1;
-      s = *(const uint32_t*)(scales + ((int64_t)p * rows + row) * 16 + (lane >> 4) * 4);
+    const int left = g.groups - p * 16;
+    // a lane's groups past the end are zeros: what is read there is its last one
+    auto read = [&](const uint8_t* codes, i32x4(&f)[4]) {
 #pragma unroll
       for (int j = 0; j < 4; j++) {
-        const int group = p * 16 + j * 4 + (lane >> 4);
-        f[j] = i32x4{};
-        if (group < g.groups) f[j] = *(const i32x4*)(codes + row * ld + group * 16);
+        if (left >= 16) {
+          f[j] = *(const i32x4*)(codes + p * 256 + j * 64);
+        } else {
+          const int group = j * 4 + (lane >> 4), at = group < left ? j * 64 : -(lane >> 4) * 16;
+          f[j] = *(const i32x4*)(codes + p * 256 + at);
+          if (group >= left) f[j] = i32x4{};
+        }
       }
     };
 #pragma unroll
-    for (int i = 0; i < FM; i++) read(g.a, g.as, m0 + i * 16 + (lane & 15), g.m, fa[i], sa[i]);
+    for (int i = 0; i < FM; i++) {
+      sa[i] = *(const uint32_t*)(qa[i] + (int64_t)p * g.m * 16);
+      read(pa[i], fa[i]);
+    }
 #pragma unroll
-    for (int k = 0; k < FN; k++) read(g.b, g.bs, n0 + k * 16 + (lane & 15), g.n, fb[k], sb[k]);
+    for (int k = 0; k < FN; k++) {
+      sb[k] = *(const uint32_t*)(qb[k] + (int64_t)p * g.n * 16);
+      read(pb[k], fb[k]);
+    }
 #pragma unroll
     for (int i = 0; i < FM; i++)
 #pragma unroll
@@ -893,8 +945,13 @@ __global__ __launch_bounds__(kFewWaves * 64) void few_kernel(Mx4Args g) {
   }
 }
 
-// Up to so many tokens the weight is streamed.
-constexpr int64_t kFewTokens = 64;
+// Up to so many tokens the weight is streamed, and up to 64 where tiles would leave most of the card
+// idle.  us streamed and in tiles, on weights that are not in the caches (tokens x width x
+// features): 32 x 4096 x 22016 17 and 18, 48 x 4096 x 22016 (172 tiles) 26 and 18, 64 x 22016 x
+// 4096 (32) 26 and 71.  32 features a workgroup where there are workgroups enough, else 16: 16 x
+// 4096 x 22016 14 and 16, 16 x 22016 x 4096 21 and 17.
+constexpr int64_t kFewTokens = 32;
+constexpr int64_t kFewTiles = 96;
 constexpr int64_t kCus = 256;
 // From so many tiles of 256 x 256 on, the card is filled by them; below, by tiles of 128 x 128
 // while there are as many as compute units; else by 128 x 64.  us with large, middle and small
@@ -903,6 +960,30 @@ constexpr int64_t kCus = 256;
 // and 22; 1024 x 4096 x 4096 (256 middle tiles) 29, 15 and 15; 128 x 4096 x 22016 (172) 30, 18
 // and 16.
 constexpr int64_t kHeldTiles = 192;
+// Fewer tiles than this leave half of the card idle; with a long k, from so many groups on, tiles of
+// 64 x 64 whose k is divided among the workgroup's waves are faster: 128 x 22016 x 4096 39 us for 72,
+// 100 x 28672 x 500 29 for 64, 128 x 2048 x 2048 6.2 for 7.4.
+constexpr int64_t kSplitTiles = 128;
+constexpr int64_t kSplitGroups = 64;
+
+int check_product(const char* who, const void* x_codes, const void* x_scales, const void* w_codes,
+                  const void* w_scales, const void* out, int64_t out_stride, int64_t tokens,
+                  int64_t features, int64_t width, int32_t dtype) {
+  if (!good_dtype(dtype)) return fail(who, "unknown element type");
+  if (tokens < 0 || tokens > kMaxSide || features < 0 || features > kMaxSide || width < 1 ||
+      width > kMaxWidth)
+    return fail(who, "a size is out of range");
+  if (out_stride < features) return fail(who, "a row stride is below the features");
+  if (tokens == 0 || features == 0) return ZS_OK;
+  if (!x_codes || !x_scales || !w_codes || !w_scales || !out) return fail(who, "NULL buffer");
+  if (!al(out, elem_bytes(dtype)) || !al(x_codes, 16) || !al(x_scales, 16) || !al(w_codes, 16) ||
+      !al(w_scales, 16))
+    return fail(who, "a buffer is not aligned to its elements, or codes or scales not to 16 bytes");
+  // large tiles, the only ones that so many can be of
+  if (((features + kBig - 1) / kBig) * ((tokens + kBig - 1) / kBig) > 0xffffff)
+    return fail(who, "too many tiles for one call");
+  return ZS_OK;
+}
 
 }  // namespace
 }  // namespace ops
@@ -988,20 +1069,39 @@ extern "C" int zs_mx4_unpack(const void* codes, const void* scales, void* x, int
   return launched(who);
 }
 
+extern "C" size_t zs_mx4_linear_bytes(int64_t tokens, int64_t width) {
+  if (tokens < 0 || tokens > kMaxSide || width < 1 || width > kMaxWidth) return 0;
+  return up256((size_t)(tokens * groups_of(width)) * 16) + up256((size_t)(spans_of(width) * tokens) * 16) + 256;
+}
+
+extern "C" int zs_mx4_linear(const void* x, int64_t x_stride, const void* w_codes,
+                             const void* w_scales, void* out, int64_t out_stride, int64_t tokens,
+                             int64_t features, int64_t width, int32_t x_dtype, int32_t dtype,
+                             void* workspace, size_t workspace_bytes, void* stream) {
+  const char* who = "zs_mx4_linear";
+  const size_t need = zs_mx4_linear_bytes(tokens, width);
+  if (need == 0) return fail(who, "a size is out of range");
+  if (!workspace || !al(workspace, 256)) return fail(who, "the workspace is NULL or not 256-byte aligned");
+  if (workspace_bytes < need) return fail(who, "the workspace is too small");
+  if (features == 0) return ZS_OK;
+  uint8_t* codes = (uint8_t*)workspace;
+  uint8_t* scales = codes + up256((size_t)(tokens * groups_of(width)) * 16);
+  // the product's arguments are looked at before anything is enqueued
+  if (int rc = check_product(who, codes, scales, w_codes, w_scales, out, out_stride, tokens, features, width, dtype))
+    return rc;
+  if (int rc = zs_mx4_pack(x, x_stride, codes, scales, nullptr, nullptr, tokens, width, x_dtype, stream))
+    return rc;
+  return zs_mx4_product(codes, scales, w_codes, w_scales, out, out_stride, tokens, features, width,
+                        dtype, stream);
+}
+
 extern "C" int zs_mx4_product(const void* x_codes, const void* x_scales, const void* w_codes,
                               const void* w_scales, void* out, int64_t out_stride, int64_t tokens,
                               int64_t features, int64_t width, int32_t dtype, void* stream) {
   const char* who = "zs_mx4_product";
-  if (!good_dtype(dtype)) return fail(who, "unknown element type");
-  if (tokens < 0 || tokens > kMaxSide || features < 0 || features > kMaxSide || width < 1 ||
-      width > kMaxWidth)
-    return fail(who, "a size is out of range");
-  if (out_stride < features) return fail(who, "a row stride is below the features");
+  if (int rc = check_product(who, x_codes, x_scales, w_codes, w_scales, out, out_stride, tokens, features, width, dtype))
+    return rc;
   if (tokens == 0 || features == 0) return ZS_OK;
-  if (!x_codes || !x_scales || !w_codes || !w_scales || !out) return fail(who, "NULL buffer");
-  if (!al(out, elem_bytes(dtype)) || !al(x_codes, 16) || !al(x_scales, 16) || !al(w_codes, 16) ||
-      !al(w_scales, 16))
-    return fail(who, "a buffer is not aligned to its elements, or codes or scales not to 16 bytes");
   Mx4Args g{};
   g.a = (const uint8_t*)w_codes;
   g.b = (const uint8_t*)x_codes;
@@ -1016,36 +1116,51 @@ extern "C" int zs_mx4_product(const void* x_codes, const void* x_scales, const v
   // 472, 16384 x 2048 x 8192 141 and 137; smaller outputs are read again from the cache
   g.streaming = streams(tokens * features * elem_bytes(dtype));
   const hipStream_t st = (hipStream_t)stream;
-  if (tokens <= kFewTokens) {
-    const uint32_t blocks = (uint32_t)((features + 31) / 32);
+  auto tiles = [&](int64_t bm, int64_t bn) {
+    return (features + bm - 1) / bm * ((tokens + bn - 1) / bn);
+  };
+  if (tokens <= kFewTokens || (tokens <= 64 && tiles(128, 64) < kFewTiles)) {
     with_dtype(dtype, [&](auto DT) {
       constexpr int kDt = decltype(DT)::value;
-      if (tokens <= 16)
-        few_kernel<kDt, 1><<<dim3(blocks, 1), dim3(kFewWaves * 64), 0, st>>>(g);
-      else if (tokens <= 32)
-        few_kernel<kDt, 2><<<dim3(blocks, 1), dim3(kFewWaves * 64), 0, st>>>(g);
-      else
-        few_kernel<kDt, 2><<<dim3(blocks, 2), dim3(kFewWaves * 64), 0, st>>>(g);
+      auto go = [&](auto FM, auto FN) {
+        constexpr int kM = decltype(FM)::value * 16, kN = decltype(FN)::value * 16;
+        few_kernel<kDt, kM / 16, kN / 16>
+            <<<dim3((uint32_t)((features + kM - 1) / kM), (uint32_t)((tokens + kN - 1) / kN)),
+               dim3(kFewWaves * 64), 0, st>>>(g);
+      };
+      using std::integral_constant;
+      if (tiles(32, kFewTokens) >= kCus) {
+        if (tokens <= 16)
+          go(integral_constant<int, 2>(), integral_constant<int, 1>());
+        else
+          go(integral_constant<int, 2>(), integral_constant<int, 2>());
+      } else if (tokens <= 16) {
+        go(integral_constant<int, 1>(), integral_constant<int, 1>());
+      } else {
+        go(integral_constant<int, 1>(), integral_constant<int, 2>());
+      }
     });
     return launched(who);
   }
-  auto tiles = [&](int64_t bm, int64_t bn) {
-    g.tiles_m = (int32_t)((features + bm - 1) / bm);
-    g.tiles_n = (int32_t)((tokens + bn - 1) / bn);
-    return (int64_t)g.tiles_m * g.tiles_n;
-  };
   const bool held = tiles(kBig, kBig) >= kHeldTiles;
   const bool middle = !held && tiles(128, 128) >= kCus;
-  const int64_t total = held ? tiles(kBig, kBig) : middle ? tiles(128, 128) : tiles(128, 64);
-  if (total > 0xffffff) return fail(who, "too many tiles for one call");
+  const bool split = !middle && tiles(128, 64) < kSplitTiles && g.groups >= kSplitGroups;
+  auto go = [&](auto kernel, int64_t bm, int64_t bn, int threads, int64_t most) {
+    g.tiles_m = (int32_t)((features + bm - 1) / bm);
+    g.tiles_n = (int32_t)((tokens + bn - 1) / bn);
+    kernel<<<dim3((uint32_t)std::min(tiles(bm, bn), most)), dim3(threads), 0, st>>>(g);
+  };
+  constexpr int64_t kAll = 1ll << 31;
   with_dtype(dtype, [&](auto DT) {
     constexpr int kDt = decltype(DT)::value;
     if (held)
-      held_kernel<kDt><<<dim3((uint32_t)std::min(total, kCus)), dim3(256), 0, st>>>(g);
+      go(held_kernel<kDt>, kBig, kBig, 256, kCus);
     else if (middle)
-      product_kernel<kDt, 128, 128><<<dim3((uint32_t)total), dim3(256), 0, st>>>(g);
+      go(product_kernel<kDt, 128, 128, 1>, 128, 128, 256, kAll);
+    else if (split)
+      go(product_kernel<kDt, 64, 64, 4>, 64, 64, 1024, kAll);
     else
-      product_kernel<kDt, 128, 64><<<dim3((uint32_t)total), dim3(256), 0, st>>>(g);
+      go(product_kernel<kDt, 128, 64, 1>, 128, 64, 256, kAll);
   });
   return launched(who);
 }

@@ -82,6 +82,9 @@ _mx4_pack = _sig("zs_mx4_pack", _INT, _vp, _i64, _vp, _vp, _vp, _vp, _i64, _i64,
 _mx4_unpack = _sig("zs_mx4_unpack", _INT, _vp, _vp, _vp, _i64, _i64, _i64, _i32, _vp)
 _mx4_product = _sig("zs_mx4_product", _INT, _vp, _vp, _vp, _vp, _vp, _i64, _i64, _i64, _i64, _i32,
                     _vp)
+_mx4_linear_bytes = _sig("zs_mx4_linear_bytes", _sz, _i64, _i64)
+_mx4_linear = _sig("zs_mx4_linear", _INT, _vp, _i64, _vp, _vp, _vp, _i64, _i64, _i64, _i64, _i32,
+                   _i32, _vp, _sz, _vp)
 _prefer_workspace_bytes = _sig("zs_prefer_workspace_bytes", _sz, _i64, _i64)
 _prefer_forward = _sig("zs_prefer_forward", _INT, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i64,
                        _i64, _f32, _f32, _f32, _i32, _i32, _i32, _vp, _sz, _vp)
@@ -98,6 +101,7 @@ EXPORTED = ["zs_embed_forward", "zs_embed_backward_bytes", "zs_embed_backward", 
             "zs_glu_forward", "zs_glu_backward", "zs_xent_workspace_bytes", "zs_xent_forward",
             "zs_xent_backward", "zs_layer_norm_forward", "zs_layer_norm_backward_bytes",
             "zs_layer_norm_backward", "zs_mx4_pack", "zs_mx4_unpack", "zs_mx4_product",
+            "zs_mx4_linear_bytes", "zs_mx4_linear",
             "zs_prefer_workspace_bytes", "zs_prefer_forward", "zs_prefer_backward",
             "zs_grads_pieces", "zs_grads_table", "zs_grads_workspace_bytes", "zs_grads_sumsq",
             "zs_grads_clip"]
@@ -181,6 +185,14 @@ def zs_mx4_unpack(*args) -> None:
 
 def zs_mx4_product(*args) -> None:
     _check(_mx4_product(*args))
+
+
+def zs_mx4_linear_bytes(tokens: int, width: int) -> int:
+    return int(_mx4_linear_bytes(tokens, width))
+
+
+def zs_mx4_linear(*args) -> None:
+    _check(_mx4_linear(*args))
 
 
 def zs_prefer_workspace_bytes(tokens: int, pairs: int) -> int:
@@ -878,33 +890,42 @@ def unpack4(c, dtype, out=None):
     return out
 
 
-def linear4(x, weight, dtype=None, out=None):
+def linear4(x, weight, dtype=None, out=None, workspace=None):
     """x @ weight.T for a weight in the 4-bit form (Codes4), summed in fp32 and rounded once to
-    dtype.  x: a matrix, which is packed along its rows first (dtype: its own unless given), or
-    Codes4 already (dtype: bf16 unless given).  With pack4's other orientations the same product
-    gives the gradients: dx = linear4(dy, pack4(w, "columns")), dw = linear4(pack4(dy,
-    "columns"), pack4(x, "columns"))."""
-    if isinstance(x, torch.Tensor):
-        dtype = dtype or (out.dtype if out is not None else x.dtype)
-        if x.dim() != 2 or x.shape[1] != getattr(weight, "width", None):
-            raise ValueError(f"x: shape {tuple(x.shape)}, expected (any, "
-                             f"{getattr(weight, 'width', 'width')}) and a Codes4 weight")
-        x = pack4(x)
-    tokens = _codes4(x, "x")
-    dev = x.codes.device
-    features = _codes4(weight, "weight", dev, x.width)
-    dtype = dtype or (out.dtype if out is not None else torch.bfloat16)
+    dtype.  x: a matrix, which is packed along its rows on the way (dtype: its own unless given;
+    workspace= takes zs_mx4_linear_bytes), or Codes4 already (dtype: bf16 unless given).  With
+    pack4's other orientations the same product gives the gradients: dx = linear4(dy, pack4(w,
+    "columns")), dw = linear4(pack4(dy, "columns"), pack4(x, "columns"))."""
+    packed = isinstance(x, Codes4)
+    if packed:
+        tokens, width = _codes4(x, "x"), x.width
+        dev = x.codes.device
+        inputs = (x.codes, x.scales)
+    else:
+        xs = _matrix(x, "x")
+        tokens, width = x.shape
+        dev = x.device
+        xt = _dtype(x, "x")
+        inputs = (x,)
+    features = _codes4(weight, "weight", dev, width)
+    if dtype is None:
+        dtype = out.dtype if out is not None else torch.bfloat16 if packed else x.dtype
     dt = _pick(_DTYPES, dtype, "dtype")
     if out is None:
         out = torch.empty(tokens, features, dtype=dtype, device=dev)
         stride = features
     else:
         stride = _matrix(out, "out", dtype, dev, tokens, features)
-        _apart(out, "out", (), (x.codes, x.scales, weight.codes, weight.scales))
-    if x.width == 0:
+        _apart(out, "out", (), (*inputs, weight.codes, weight.scales))
+    if width == 0:
         return out.zero_()
-    _run(dev, _mx4_product, x.codes.data_ptr(), x.scales.data_ptr(), weight.codes.data_ptr(),
-         weight.scales.data_ptr(), out.data_ptr(), stride, tokens, features, x.width, dt)
+    if packed:
+        _run(dev, _mx4_product, x.codes.data_ptr(), x.scales.data_ptr(), weight.codes.data_ptr(),
+             weight.scales.data_ptr(), out.data_ptr(), stride, tokens, features, width, dt)
+    else:
+        ws = _workspace(workspace, _mx4_linear_bytes(tokens, width), dev)
+        _run(dev, _mx4_linear, x.data_ptr(), xs, weight.codes.data_ptr(), weight.scales.data_ptr(),
+             out.data_ptr(), stride, tokens, features, width, xt, dt, ws.data_ptr(), ws.numel())
     return out
 
 

@@ -128,7 +128,9 @@ def check_product(x, w, dtype, **more):
 
 
 SIZES = [(1, 1, 1), (1, 32, 16), (3, 33, 5), (16, 100, 40), (17, 512, 33), (32, 1000, 100), (33, 513, 65), (64, 4096, 96),
-         (65, 128, 64), (66, 129, 130), (100, 700, 300), (200, 2048, 257), (300, 1025, 129), (513, 31, 1000)]
+         (65, 128, 64), (66, 129, 130), (100, 700, 300), (200, 2048, 257), (300, 1025, 129), (513, 31, 1000),
+         (40, 2048, 70), (64, 2300, 200), (65, 2048, 64), (100, 4100, 300), (70, 2561, 65), (200, 22016, 130),
+         (33, 1100, 13000)]
 
 
 @pytest.mark.parametrize("dtype", list(DT))
@@ -149,6 +151,17 @@ def test_larger_tiles(tokens, width, features, dtype):
     g = gen(tokens)
     x, w = rand(g, tokens, width, dtype=torch.bfloat16), rand(g, features, width, dtype=torch.bfloat16)
     check_product(x, w, dtype)
+
+
+def test_outputs_that_pass_the_cache():
+    """Streamed stores: bit for bit what smaller calls give."""
+    g = gen(17)
+    x, w = ops.pack4(rand(g, 16400, 96, dtype=torch.bfloat16)), ops.pack4(rand(g, 8300, 96, dtype=torch.bfloat16))
+    y = ops.linear4(x, w)
+    assert y.numel() * 2 > 256 << 20
+    for at in (0, 8192, 16200):
+        part = ops.Codes4(x.codes[at:at + 200].contiguous(), x.scales[:, at:at + 200].contiguous(), 96)
+        assert torch.equal(y[at:at + 200], ops.linear4(part, w))
 
 
 @pytest.mark.parametrize("tokens", [5, 40, 100, 1300, 2500])

@@ -61,6 +61,7 @@ def test_layer_norm_backward_of_too_many_wide_rows():
 PACK4 = [P, 64, P, P, P, P, 10, 64, 1, 0]
 UNPACK4 = [P, P, P, 64, 10, 64, 1, 0]
 PRODUCT = [P, P, P, P, P, 70, 10, 70, 64, 1, 0]
+LINEAR = [P, 64, P, P, P, 70, 10, 70, 64, 1, 1, P, 1 << 20, 0]
 
 
 @pytest.mark.parametrize("call, args, at, word", [
@@ -83,7 +84,14 @@ PRODUCT = [P, P, P, P, P, 70, 10, 70, 64, 1, 0]
     (ops.zs_mx4_product, PRODUCT, dict(_5=69), "stride"), (ops.zs_mx4_product, PRODUCT, dict(_4=0), "NULL"),
     (ops.zs_mx4_product, PRODUCT, dict(_1=0), "NULL"), (ops.zs_mx4_product, PRODUCT, dict(_3=P + 8), "aligned"),
     (ops.zs_mx4_product, PRODUCT, dict(_4=P + 1), "aligned"),
-    (ops.zs_mx4_product, PRODUCT, dict(_5=1 << 24, _6=1 << 24, _7=1 << 24), "too many")])
+    (ops.zs_mx4_product, PRODUCT, dict(_5=1 << 24, _6=1 << 24, _7=1 << 24), "too many"),
+    (ops.zs_mx4_linear, LINEAR, dict(_6=-1), "range"), (ops.zs_mx4_linear, LINEAR, dict(_8=0), "range"),
+    (ops.zs_mx4_linear, LINEAR, dict(_1=63), "stride"), (ops.zs_mx4_linear, LINEAR, dict(_5=69), "stride"),
+    (ops.zs_mx4_linear, LINEAR, dict(_0=0), "NULL"), (ops.zs_mx4_linear, LINEAR, dict(_2=0), "NULL"),
+    (ops.zs_mx4_linear, LINEAR, dict(_4=0), "NULL"), (ops.zs_mx4_linear, LINEAR, dict(_9=5), "type"),
+    (ops.zs_mx4_linear, LINEAR, dict(_10=5), "type"), (ops.zs_mx4_linear, LINEAR, dict(_11=0), "workspace"),
+    (ops.zs_mx4_linear, LINEAR, dict(_11=P + 16), "workspace"), (ops.zs_mx4_linear, LINEAR, dict(_12=500), "workspace"),
+    (ops.zs_mx4_linear, LINEAR, dict(_3=P + 8), "aligned"), (ops.zs_mx4_linear, LINEAR, dict(_0=P + 1), "aligned")])
 def test_mx4_refusals(call, args, at, word):
     assert word in refused(call, *change(args, **at))
 
