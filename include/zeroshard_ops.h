@@ -233,7 +233,7 @@ int zs_layer_norm_backward(const void *dy, int64_t dy_stride, const void *sum, i
  * x in the 4-bit form: along its rows to codes and scales, along its columns (the form of the
  * transposed matrix, which has `width` rows of `rows` elements) to codes_t and scales_t;
  * either pair may be NULL.  1 <= width <= 2^20, rows <= 2^24 (2^20 along columns), and fewer than
- * 2^24 pieces of 4 rows x 512 (along columns 128 x 128), counting whole spans of 512.
+ * 2^24 pieces of 4 rows x 512 (along columns 2^23 of 256 x 256), counting whole spans of 512.
  */
 int zs_mx4_pack(const void *x, int64_t x_stride, void *codes, void *scales, void *codes_t,
                 void *scales_t, int64_t rows, int64_t width, int32_t dtype, void *stream);

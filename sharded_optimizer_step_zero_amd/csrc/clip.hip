@@ -257,7 +257,7 @@ extern "C" int zs_grads_table(const zs_grad_tensor* list, int64_t n, void* table
   if (!table || !al(table, 8)) return fail(who, "the table is NULL or not 8-byte aligned");
   try {
     if (outputs_overlap(list, n)) return fail(who, "an output overlaps another buffer of the list");
-  } catch (const std::bad_alloc&) {
+  } catch (...) {  // nothing leaves a C entry
     return fail(who, "no host memory to check the list with");
   }
   // whole pieces first: the last of a pass, which not every wave has, are short

@@ -18,8 +18,8 @@
 // and both of its ends encoded, took 260 us for 193.)
 //
 // Bound by HBM.  Measured, bf16: forward at 16384 x 8192 with residual and 8-bit codes 193 us for
-// 943 MB (4.9 TB/s; the instructions for the codes are what keeps it from 5.9), backward at 32768 x 2048 101 us for 537 MB (5.3 TB/s), 16384 x 8192
-// 186 us (5.8), 8192 x 12288 in two passes 217 us.
+// 943 MB (4.9 TB/s; the instructions for the codes keep it from 5.9), backward at 32768 x 2048
+// 101 us for 537 MB (5.3 TB/s), 16384 x 8192 186 us (5.8), 8192 x 12288 in two passes 217 us.
 #include "rows.h"
 
 namespace zs {

@@ -1025,7 +1025,8 @@ extern "C" int zs_mx4_pack(const void* x, int64_t x_stride, void* codes, void* s
   const int64_t across = codes ? spans * 2 : (width + 255) / 256;
   const bool large = spans_t * 2 * across >= kLargeBlocks;
   const int64_t down = spans_t * (large ? 2 : 8);
-  if (down * across > 0xffffff) return fail(who, "too many elements for one call");
+  // a launch has fewer than 2^32 threads
+  if (down * across > 0x7fffff) return fail(who, "too many elements for one call");
   with_dtype(dtype, [&](auto DT) {
     constexpr int kDt = decltype(DT)::value;
     with_bool(codes != nullptr, [&](auto ROWS) {

@@ -992,6 +992,8 @@ def preference_loss_backward(forward, offsets, grad_loss, tokens, beta=0.1, kind
     dev = offsets.device
     if not offsets.is_cuda:
         raise ValueError(f"offsets: on {dev}, expected a GPU")
+    if tokens < 0:
+        raise ValueError(f"tokens: {tokens}, expected 0 or more")
     k = _pick(_KINDS, kind, "kind")
     pairs = _pairs(offsets, mask, dev, tokens)
     _vector(forward.margins, "margins", (torch.float32,), dev, pairs)
