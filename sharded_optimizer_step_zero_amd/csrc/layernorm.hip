@@ -15,11 +15,12 @@
 // Codes come from an output in fp64 (whose instructions take no longer than fp32's), rounded to
 // fp32 to nearest and, where that may have crossed the border between two codes or two scales, to
 // the odd side, so that each code is one rounding of y.  (The output in fp32 with an error bound,
-// and both of its ends encoded, took 260 us for 193.)
+// and both of its ends encoded, took 260 us for 203.)
 //
-// Bound by HBM.  Measured, bf16: forward at 16384 x 8192 with residual and 8-bit codes 193 us for
-// 943 MB (4.9 TB/s; the instructions for the codes keep it from 5.9), backward at 32768 x 2048
-// 101 us for 537 MB (5.3 TB/s), 16384 x 8192 186 us (5.8), 8192 x 12288 in two passes 217 us.
+// Bound by HBM.  Measured, bf16: forward at 16384 x 8192 with residual and 8-bit codes 183 us for
+// 943 MB (5.2 TB/s; the vector unit is busy for three quarters of it), in 4 bits 175; backward at
+// 32768 x 2048 96 us for 537 MB (5.6 TB/s), 16384 x 8192 186 us (5.8), 8192 x 12288 in two passes
+// 212 us.  Outputs with codes above 32768 columns spill registers.
 #include "rows.h"
 
 namespace zs {
@@ -44,6 +45,80 @@ struct RowArgs {
   float eps;
   double inv_width;
 };
+
+// Sums and maxima over lanes by moves inside the vector unit (the LDS ways of a shuffle wait some
+// hundred cycles each, of which a row has fourteen in a chain: forward at 16384 x 8192 195 us for
+// 183, at 32768 x 2048 115 for 98, backward there 101 for 96).
+
+// x of another lane of the row of 16: CTRL 0xb1 lane ^ 1, 0x4e lane ^ 2, 0x141 the other end of the
+// eight, 0x140 of the sixteen.
+template <int CTRL, typename F>
+__device__ __forceinline__ F other_lane(F x) {
+  uint32_t w[sizeof(F) / 4];
+  __builtin_memcpy(w, &x, sizeof(F));
+#pragma unroll
+  for (size_t i = 0; i < sizeof(F) / 4; i++)
+    w[i] = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)w[i], CTRL, 0xf, 0xf, true);
+  __builtin_memcpy(&x, w, sizeof(F));
+  return x;
+}
+// Joins x over n neighbouring lanes, n = 1, 2, 4, 8 or 16.
+template <typename F, typename JOIN>
+__device__ __forceinline__ F join_lanes(F x, int n, JOIN join) {
+  if (n >= 2) x = join(x, other_lane<0xb1>(x));
+  if (n >= 4) x = join(x, other_lane<0x4e>(x));
+  if (n >= 8) x = join(x, other_lane<0x141>(x));
+  if (n >= 16) x = join(x, other_lane<0x140>(x));
+  return x;
+}
+// The sum over 16, 32 or 64 lanes, in all of them.
+template <typename F>
+__device__ __forceinline__ F wave_sum(F x, int lanes) {
+  x = join_lanes(x, 16, [](F a, F b) { return a + b; });
+  constexpr int kWords = sizeof(F) / 4;
+  uint32_t a[kWords], b[kWords];
+  F p, q;
+  if (lanes >= 32) {  // rows of 16 change places: 0 and 1, 2 and 3
+    __builtin_memcpy(a, &x, sizeof(F));
+#pragma unroll
+    for (int i = 0; i < kWords; i++) {
+      const auto s = __builtin_amdgcn_permlane16_swap(a[i], a[i], false, false);
+      a[i] = s[0];
+      b[i] = s[1];
+    }
+    __builtin_memcpy(&p, a, sizeof(F));
+    __builtin_memcpy(&q, b, sizeof(F));
+    x = p + q;
+  }
+  if (lanes >= 64) {  // halves of the wave
+    __builtin_memcpy(a, &x, sizeof(F));
+#pragma unroll
+    for (int i = 0; i < kWords; i++) {
+      const auto s = __builtin_amdgcn_permlane32_swap(a[i], a[i], false, false);
+      a[i] = s[0];
+      b[i] = s[1];
+    }
+    __builtin_memcpy(&p, a, sizeof(F));
+    __builtin_memcpy(&q, b, sizeof(F));
+    x = p + q;
+  }
+  return x;
+}
+// The sum over a row's threads, of which `base` is the first wave: through LDS where they are more
+// than a wave (each call its own slots, written before and read after one barrier).
+template <typename F>
+__device__ __forceinline__ F sum_row(F x, int lanes, int base, F* slots) {
+  x = wave_sum(x, lanes);
+  if (lanes <= 64) return x;
+  if ((threadIdx.x & 63) == 0) slots[threadIdx.x >> 6] = x;
+  __syncthreads();
+  const int n = lanes / 64;
+  return join_lanes(slots[base + (threadIdx.x & (n - 1))], n, [](F a, F b) { return a + b; });
+}
+// The largest magnitude of a group of 4, 8 or 16 lanes' elements.
+__device__ __forceinline__ float amax_lanes(f32x8 x, int lanes) {
+  return __uint_as_float(join_lanes(amax_bits(x), lanes, [](uint32_t a, uint32_t b) { return a > b ? a : b; }));
+}
 
 // The scale byte of a group, by the format as a value.
 __device__ __forceinline__ uint32_t scale_byte_of(int code, float amax) {
@@ -91,7 +166,7 @@ __device__ __forceinline__ void layer_norm_rows(const RowArgs<DT>& g, double (&s
 #pragma unroll
     for (int i = 0; i < 8; i++) total += (double)s[k][i];
   }
-  const double m = row_sum(total, lanes, slots[0]) * g.inv_width;
+  const double m = sum_row(total, lanes, 0, slots[0]) * g.inv_width;
   // differences from the mean: with codes they stay in fp64 for the output
   constexpr int kHeld = CODES ? NC : 1;
   double held[kHeld][8];
@@ -105,7 +180,7 @@ __device__ __forceinline__ void layer_norm_rows(const RowArgs<DT>& g, double (&s
       if (CODES) held[CODES ? k : 0][i] = d;
     }
   }
-  const double variance = row_sum(sq, lanes, slots[1]) * g.inv_width;
+  const double variance = sum_row(sq, lanes, 0, slots[1]) * g.inv_width;
   const double root = inverse_root(variance + (double)g.eps);
   const float r = (float)root;
   // the mean in two parts: a difference from it is off by two roundings of itself
@@ -133,7 +208,8 @@ __device__ __forceinline__ void layer_norm_rows(const RowArgs<DT>& g, double (&s
       const int chunk = k * lanes + in_row, c = chunk * 8, left = count(k);
       f32x8 v = {};
       double q[8] = {};
-      uint32_t nearest = 0xffffffffu;  // the least of the outputs' low halves, moved up
+      typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
+      u16x2 nearest = {0xffff, 0xffff};  // the least of the outputs' low halves
       if (WHOLE || left > 0) {
         const f32x8 w = load8<DT>(g.weight + c, left);
         const f32x8 b = g.bias ? load8<DT>(g.bias + c, left) : f32x8{};
@@ -141,22 +217,24 @@ __device__ __forceinline__ void layer_norm_rows(const RowArgs<DT>& g, double (&s
         for (int i = 0; i < 8; i++) {
           q[i] = __builtin_fma(held[k][i] * root, (double)w[i], (double)b[i]);
           v[i] = (float)q[i];
-          const uint32_t low = __float_as_uint(v[i]) << 16;
-          nearest = low < nearest ? low : nearest;
         }
+#pragma unroll
+        for (int i = 0; i < 8; i += 2)
+          nearest = __builtin_elementwise_min(nearest, __builtin_bit_cast(u16x2, __builtin_amdgcn_perm(
+              __float_as_uint(v[i + 1]), __float_as_uint(v[i]), 0x05040100)));
         if (live && g.y) store8<DT, NT>(g.y + row * g.y_stride + c, left, v);
       }
       // Ties of codes, and borders of scales, have sixteen zeros at least at their end (where
       // they are normal in fp32).  An output that fp32 rounds to such a value may lie to either
       // side.
-      float amax = group_amax(v, group_lanes);
+      float amax = amax_lanes(v, group_lanes);
       // the same for all lanes of a group
       const bool border = (__float_as_uint(amax) & 0xffffu) == 0 || amax < 0x1p-90f;
-      if (border || nearest == 0) {
+      if (border || nearest[0] == 0 || nearest[1] == 0) {
 #pragma unroll
         for (int i = 0; i < 8; i++) v[i] = side_of(q[i]);
       }
-      if (border) amax = group_amax(v, group_lanes);
+      if (border) amax = amax_lanes(v, group_lanes);
       const uint32_t byte = scale_byte_of(g.code, amax);
       // the scaling is exact but far below the group's largest, where all that matters is the side
       v *= scale_inverse(byte == 255u ? 127u : byte);
@@ -199,21 +277,6 @@ struct GradRow {
 };
 
 constexpr int kGradThreads = 512;
-
-// Two sums over a row's threads at once, one barrier.  `base` is the row's first wave.
-__device__ __forceinline__ f32x2 row_sums(f32x2 x, int lanes, int base, f32x2* slots) {
-  const int w = lanes < 64 ? lanes : 64;
-  for (int d = 1; d < w; d <<= 1) {
-    x[0] += __shfl_xor(x[0], d, 64);
-    x[1] += __shfl_xor(x[1], d, 64);
-  }
-  if (lanes <= 64) return x;
-  if ((threadIdx.x & 63) == 0) slots[threadIdx.x >> 6] = x;
-  __syncthreads();
-  f32x2 s = {};
-  for (int i = 0; i < lanes / 64; i++) s += slots[base + i];
-  return s;
-}
 
 template <int DT, bool NT, int NC>
 __global__ __launch_bounds__(kGradThreads) void layer_norm_grad_kernel(
@@ -279,7 +342,7 @@ __global__ __launch_bounds__(kGradThreads) void layer_norm_grad_kernel(
         dot[1] += g[k][i] * h[k][i];
       }
     }
-    const f32x2 means = row_sums(dot, lanes, sub * lanes / 64, slots[turn]) * inv_width;
+    const f32x2 means = sum_row(dot, lanes, sub * lanes / 64, slots[turn]) * inv_width;
 #pragma unroll
     for (int k = 0; k < NC; k++) {
       const int c = (k * lanes + in_row) * 8, left = row < rows ? width - c : 0;
@@ -309,7 +372,7 @@ __global__ __launch_bounds__(1024) void wide_means_kernel(
     const elem_t<DT>* __restrict__ dy, int64_t dy_stride, const elem_t<DT>* __restrict__ sum,
     int64_t sum_stride, const elem_t<DT>* __restrict__ weight, const float* __restrict__ mean,
     const float* __restrict__ rstd, f32x2* __restrict__ means, int64_t width) {
-  __shared__ float slots[2][16];
+  __shared__ f32x2 slots[16];
   const int64_t row = blockIdx.x;
   const float m = mean[row], r = rstd[row];
   f32x2 dot = {};
@@ -326,9 +389,8 @@ __global__ __launch_bounds__(1024) void wide_means_kernel(
     }
   }
   const float inv_width = 1.0f / (float)width;
-  const float mean_g = row_sum(dot[0], 1024, slots[0]) * inv_width;
-  const float mean_gh = row_sum(dot[1], 1024, slots[1]) * inv_width;
-  if (threadIdx.x == 0) means[row] = f32x2{mean_g, mean_gh};
+  const f32x2 both = sum_row(dot, 1024, 0, slots) * inv_width;
+  if (threadIdx.x == 0) means[row] = both;
 }
 
 // Wide rows, then: a strip of columns down every gridDim.y-th row.
