@@ -104,8 +104,10 @@ __device__ __forceinline__ uint32_t byte4(float amax, float* scale) {
   return b;
 }
 
-// From so many blocks of 256 x 256 on; below, 64 x 256, so that the card has work.
-constexpr int64_t kLargeBlocks = 512;
+// From so many blocks of 256 x 256 on; below, 64 x 256, so that the card has work.  us with large and
+// with small blocks, bf16 from HBM: 8192 x 4096 (512) 33 and 26, 22016 x 4096 (1376) 70 and 74, 8192
+// x 22016 (2752) 130 and 182.
+constexpr int64_t kLargeBlocks = 1024;
 
 // WAVES * 32 rows x 256 columns: a lane has 32 rows of four columns, so that a group along columns
 // is one lane's and a group along rows eight lanes'.  ROWS: both, else along columns only.
