@@ -4,15 +4,15 @@
 // The tensors are laid out once as a table of pieces of up to 4096 elements, each with its
 // addresses and types, so that ten thousand small tensors and one large matrix are the same
 // kind of work and a call is two or three launches however many there are.  A wave takes every
-// n-th piece by itself: what a small tensor takes is the way to its elements, and there are
-// 8192 waves on it at once (pieces of 16384 by workgroups: 118 us
-// for ten thousand tensors of up to 4096 and four of 4096 x 4096, now 115).  Squares are exact
-// in fp64 (24 bits each) and finite whatever the element, and are summed there: a workgroup
-// takes every n-th piece, and a second kernel adds the workgroups' sums in order.
+// n-th piece by itself: what a small tensor takes is the way to its elements, and there are 8192
+// waves on it at once.  Squares are exact in fp64 (24 bits each) and finite whatever the
+// element, and are summed there; a second kernel adds the workgroups' sums in order.
 //
 // Bound by HBM: every gradient is read, and read again and written.  The second pass goes
 // through the pieces from the last to the first, so that what the first read last is still in
-// the caches.
+// the caches.  Measured: 195 tensors of 1.3 G elements, bf16 and fp32 into bf16, 459 us (5.7 TB/s) and
+// 1005; ten thousand tensors of up to 4096 and four of 4096 x 4096, bf16, 47 and 62 us, and 5 for the
+// sums (by workgroups in pieces of 16384: 53 and 73).
 #include <algorithm>
 #include <vector>
 

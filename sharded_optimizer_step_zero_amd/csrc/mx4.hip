@@ -254,7 +254,8 @@ __global__ __launch_bounds__(WAVES * 64, DT == ZS_F32 ? 2 : 4) void pack_both_ke
     }
   }
   // The columns: 32 rows' codes are 16 bytes, which go through LDS so that a column's groups are
-  // written together.  A column's place for a wave is turned by its lane: no bank is met twice.
+  // written together.  A column's place for a wave is turned by its lane, so that eight
+  // neighbouring lanes meet different banks.
 #pragma unroll
   for (int k = 0; k < 4; k++) {
     float scale;

@@ -1,7 +1,8 @@
 """What the compiler cannot guard around the inline assembly of the 4-bit products: descriptors and
 m0 are old enough when a load into LDS reads them, a matrix instruction's operands when
-it reads those, and the sums in the accumulation registers are left alone until they are
-ready.  This compiles the kernels and looks."""
+it reads those, the sums in the accumulation registers are left alone until they are
+ready, and the stores that a wait lets go on are as many as it counts.  This compiles the
+kernels and looks."""
 import os
 import re
 import subprocess
@@ -87,3 +88,17 @@ def test_sums_are_left_alone_until_they_are_ready(kernels):
                 todo.append(labels[to.group(1)])
             if not c.startswith("s_branch"):
                 todo.append(i + 1)
+
+
+def test_a_whole_tiles_stores_are_as_many_as_are_left_under_way(kernels):
+    """The first wait after a whole tile lets its stores go on by their number: 32 of 16 bytes in
+    16-bit types, streamed or not; in fp32 63 of its 64 (there the ragged tile has as many)."""
+    for name, code, _ in [k for k in kernels if "held_kernel" in k[0]]:
+        wide = [c for c in code if c.startswith("global_store_dwordx4")]
+        waits = [c for c in code if re.match(r"s_waitcnt vmcnt\((32|63)\)", c)]
+        if "held_kernelILi0E" in name:
+            assert len(wide) == 128 and any("63" in c for c in waits), name
+        else:
+            streamed = [c for c in wide if re.search(r"\bnt\b", c)]
+            assert len(streamed) == 32 and len(wide) == 64 and any("32" in c for c in waits), name
+        assert not any(c.startswith("scratch_") for c in code), name
