@@ -322,7 +322,7 @@ int64_t zs_grads_pieces(const zs_grad_tensor *list, int64_t n);
  */
 int zs_grads_table(const zs_grad_tensor *list, int64_t n, void *table, size_t table_bytes);
 
-/* Workspace of zs_grads_sumsq; 0 when a size is out of range. */
+/* Workspace of zs_grads_sumsq and zs_grads_clip; 0 when a size is out of range. */
 size_t zs_grads_workspace_bytes(int64_t pieces);
 
 /* *sumsq (device) = the sum of the squares of all elements of the list, in fp64. */
@@ -330,13 +330,14 @@ int zs_grads_sumsq(const void *table, int64_t pieces, double *sumsq, void *works
                    size_t workspace_bytes, void *stream);
 
 /*
- * With the device double *sumsq (of this list, or summed over the ranks): norm = sqrt(*sumsq),
+ * With the device double *sumsq (of this list, or summed over the ranks; NULL: this list's is taken
+ * here, for which alone the workspace is used): norm = sqrt(*sumsq),
  * out = c * grad with c = min(1, max_norm / (norm + 1e-6)) in fp32, rounded once to the
  * output's type; *norm_out (device, may be NULL) = norm.  Every gradient of the list has an
  * output.  One that is its own output is left alone where c is 1.
  */
 int zs_grads_clip(const void *table, int64_t pieces, float max_norm, const double *sumsq,
-                  double *norm_out, void *stream);
+                  double *norm_out, void *workspace, size_t workspace_bytes, void *stream);
 
 #ifdef __cplusplus
 }

@@ -6,13 +6,13 @@
 // kind of work and a call is two or three launches however many there are.  A wave takes every
 // n-th piece by itself: what a small tensor takes is the way to its elements, and there are 8192
 // waves on it at once.  Squares are exact in fp64 (24 bits each) and finite whatever the
-// element, and are summed there; a second kernel adds the workgroups' sums in order.
+// element, and are summed there in a fixed order.
 //
 // Bound by HBM: every gradient is read, and read again and written.  The second pass goes
 // through the pieces from the last to the first, so that what the first read last is still in
 // the caches.  Measured: 195 tensors of 1.3 G elements, bf16 and fp32 into bf16, 459 us (5.7 TB/s) and
-// 1005; ten thousand tensors of up to 4096 and four of 4096 x 4096, bf16, 47 and 62 us, and 5 for the
-// sums (by workgroups in pieces of 16384: 53 and 73).
+// 1005; ten thousand tensors of up to 4096 and four of 4096 x 4096, bf16, 47 and 65 us (by workgroups
+// in pieces of 16384: 53 and 73).
 #include <algorithm>
 #include <vector>
 
@@ -112,12 +112,17 @@ __global__ __launch_bounds__(256) void squares_kernel(const Piece* __restrict__ 
   if (threadIdx.x == 0) parts[blockIdx.x] = s;
 }
 
-__global__ __launch_bounds__(1024) void total_kernel(const double* __restrict__ parts, int32_t n,
-                                                     double* __restrict__ sumsq) {
-  __shared__ double slots[16];
+// The workgroups' sums, added in one order by every workgroup that needs them.
+__device__ __forceinline__ double total_of(const double* parts, int32_t n, double* slots) {
   double s = 0.0;
-  for (int32_t i = threadIdx.x; i < n; i += 1024) s += parts[i];
-  s = block_sum(s, slots);
+  for (int32_t i = threadIdx.x; i < n; i += 256) s += parts[i];
+  return block_sum(s, slots);
+}
+
+__global__ __launch_bounds__(256) void total_kernel(const double* __restrict__ parts, int32_t n,
+                                                    double* __restrict__ sumsq) {
+  __shared__ double slots[4];
+  const double s = total_of(parts, n, slots);
   if (threadIdx.x == 0) *sumsq = s;
 }
 
@@ -138,11 +143,15 @@ __device__ __forceinline__ void scale_piece(const Piece& p, Factor c) {
   });
 }
 
+// The sum of squares is *sumsq, or, where that is NULL, of the `n_parts` workgroups' sums: their
+// 16 KB from the L2 cost a workgroup less than a launch between the two passes.
 __global__ __launch_bounds__(256) void scale_kernel(const Piece* __restrict__ pieces,
                                                     int64_t n_pieces, float max_norm,
                                                     const double* __restrict__ sumsq,
+                                                    const double* __restrict__ parts, int32_t n_parts,
                                                     double* __restrict__ norm_out) {
-  const double norm = sqrt(*sumsq);
+  __shared__ double slots[4];
+  const double norm = sqrt(sumsq ? *sumsq : total_of(parts, n_parts, slots));
   if (norm_out && blockIdx.x == 0 && threadIdx.x == 0) *norm_out = norm;
   const double q = (double)max_norm / (norm + 1e-6);
   const Factor c(q > 1.0 ? 1.0 : q);  // NaN goes through
@@ -281,34 +290,46 @@ extern "C" size_t zs_grads_workspace_bytes(int64_t pieces) {
   return up256(kGroups * 8) + 256;
 }
 
+// Enqueues the sums of squares of the workgroups, `*blocks` of them, into the workspace.
+static int enqueue_squares(const char* who, const void* table, int64_t pieces, void* workspace,
+                           size_t workspace_bytes, int32_t* blocks, hipStream_t stream) {
+  if (!workspace || !al(workspace, 256)) return fail(who, "the workspace is NULL or not 256-byte aligned");
+  if (workspace_bytes < zs_grads_workspace_bytes(pieces)) return fail(who, "the workspace is too small");
+  *blocks = (int32_t)std::min<int64_t>((pieces + 3) / 4, kGroups);
+  if (*blocks)
+    squares_kernel<<<dim3((uint32_t)*blocks), dim3(256), 0, stream>>>((const Piece*)table, pieces,
+                                                                      (double*)workspace);
+  return launched(who);
+}
+
 extern "C" int zs_grads_sumsq(const void* table, int64_t pieces, double* sumsq, void* workspace,
                               size_t workspace_bytes, void* stream) {
   const char* who = "zs_grads_sumsq";
   if (pieces < 0 || pieces > kMaxPieces) return fail(who, "a size is out of range");
   if (!sumsq || (pieces && !table)) return fail(who, "NULL buffer");
   if (!al(sumsq, 8) || !al(table, 32)) return fail(who, "a buffer is not aligned to its elements");
-  if (!workspace || !al(workspace, 256)) return fail(who, "the workspace is NULL or not 256-byte aligned");
-  if (workspace_bytes < zs_grads_workspace_bytes(pieces)) return fail(who, "the workspace is too small");
-  const int32_t blocks = (int32_t)std::min<int64_t>((pieces + 3) / 4, kGroups);
-  if (blocks)
-    squares_kernel<<<dim3((uint32_t)blocks), dim3(256), 0, (hipStream_t)stream>>>(
-        (const Piece*)table, pieces, (double*)workspace);
-  if (int rc = launched(who)) return rc;
-  total_kernel<<<dim3(1), dim3(1024), 0, (hipStream_t)stream>>>((const double*)workspace, blocks,
-                                                                sumsq);
+  int32_t blocks;
+  if (int rc = enqueue_squares(who, table, pieces, workspace, workspace_bytes, &blocks, (hipStream_t)stream))
+    return rc;
+  total_kernel<<<dim3(1), dim3(256), 0, (hipStream_t)stream>>>((const double*)workspace, blocks, sumsq);
   return launched(who);
 }
 
 extern "C" int zs_grads_clip(const void* table, int64_t pieces, float max_norm,
-                             const double* sumsq, double* norm_out, void* stream) {
+                             const double* sumsq, double* norm_out, void* workspace,
+                             size_t workspace_bytes, void* stream) {
   const char* who = "zs_grads_clip";
   if (pieces < 0 || pieces > kMaxPieces) return fail(who, "a size is out of range");
   if (!(max_norm > 0.0f) || !__builtin_isfinite(max_norm)) return fail(who, "max_norm must be finite and above 0");
-  if (!sumsq || (pieces && !table)) return fail(who, "NULL buffer");
+  if (pieces && !table) return fail(who, "NULL buffer");
   if (!al(sumsq, 8) || !al(norm_out, 8) || !al(table, 32))
     return fail(who, "a buffer is not aligned to its elements");
+  int32_t parts = 0;
+  if (!sumsq)
+    if (int rc = enqueue_squares(who, table, pieces, workspace, workspace_bytes, &parts, (hipStream_t)stream))
+      return rc;
   const int32_t blocks = (int32_t)std::max<int64_t>(1, std::min<int64_t>((pieces + 3) / 4, kGroups));
   scale_kernel<<<dim3((uint32_t)blocks), dim3(256), 0, (hipStream_t)stream>>>(
-      (const Piece*)table, pieces, max_norm, sumsq, norm_out);
+      (const Piece*)table, pieces, max_norm, sumsq, (const double*)workspace, parts, norm_out);
   return launched(who);
 }

@@ -94,7 +94,7 @@ _grads_pieces = _sig("zs_grads_pieces", _i64, _vp, _i64)
 _grads_table = _sig("zs_grads_table", _INT, _vp, _i64, _vp, _sz)
 _grads_workspace_bytes = _sig("zs_grads_workspace_bytes", _sz, _i64)
 _grads_sumsq = _sig("zs_grads_sumsq", _INT, _vp, _i64, _vp, _vp, _sz, _vp)
-_grads_clip = _sig("zs_grads_clip", _INT, _vp, _i64, _f32, _vp, _vp, _vp)
+_grads_clip = _sig("zs_grads_clip", _INT, _vp, _i64, _f32, _vp, _vp, _vp, _sz, _vp)
 
 EXPORTED = ["zs_embed_forward", "zs_embed_backward_bytes", "zs_embed_backward", "zs_norm_forward",
             "zs_norm_backward_bytes", "zs_norm_backward", "zs_act8_pack", "zs_act8_unpack",
@@ -1091,18 +1091,20 @@ def grad_sumsq(grads, out=None, workspace=None):
     return out
 
 
-def clip_grads(grads, max_norm, sumsq=None):
+def clip_grads(grads, max_norm, sumsq=None, workspace=None):
     """Writes min(1, max_norm / (norm + 1e-6)) times the gradients to their outputs (a GradList's
     out; in place otherwise) and returns their global norm, a float64 scalar tensor.  sumsq:
     grad_sumsq's result where it is summed over ranks; otherwise it is taken here."""
     grads = _grad_list(grads)
     dev = grads.device
+    ws = None
     if sumsq is None:
-        sumsq = grad_sumsq(grads)
+        ws = _workspace(workspace, _grads_workspace_bytes(grads.pieces), dev)
     elif sumsq.dtype != torch.float64 or sumsq.device != dev or sumsq.numel() != 1:
         raise ValueError(f"sumsq: {sumsq.dtype} {tuple(sumsq.shape)} on {sumsq.device}, expected one "
                          f"torch.float64 on {dev}")
     norm = torch.empty((), dtype=torch.float64, device=dev)
-    _run(dev, _grads_clip, grads.table.data_ptr(), grads.pieces, max_norm, sumsq.data_ptr(),
-         norm.data_ptr())
+    _run(dev, _grads_clip, grads.table.data_ptr(), grads.pieces, max_norm, sumsq.data_ptr() if sumsq
+         is not None else None, norm.data_ptr(), ws.data_ptr() if ws is not None else None,
+         ws.numel() if ws is not None else 0)
     return norm

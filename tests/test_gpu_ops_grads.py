@@ -63,6 +63,9 @@ def test_sumsq_and_many_tensors(count, longest):
     want = math.fsum(float((x.double() ** 2).sum()) for x in t)
     assert math.isclose(float(s), want, rel_tol=1e-13)
     assert torch.equal(ops.grad_sumsq(rows), s)  # bit for bit
+    # the norm that the clip takes itself is that sum's root, bit for bit
+    copies = [x.clone() for x in t]
+    assert torch.equal(ops.clip_grads(copies, 0.1), ops.clip_grads(rows, 1e30, sumsq=s))
     # given the sum over the ranks instead
     total = (s * 4).clone()
     norm, factor = math.sqrt(4 * want), min(1.0, 0.1 / (math.sqrt(4 * want) + 1e-6))

@@ -143,7 +143,7 @@ def test_product(dtype, tokens, width, features):
     assert torch.equal(ops.linear4(x, ops.pack4(w)), got)
 
 
-@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16, torch.float32])
 @pytest.mark.parametrize("tokens, width, features", [(4100, 160, 4300), (1000, 544, 17000), (2304, 96, 8200),
                                                      (2100, 700, 2100), (1030, 1100, 4096), (2048, 300, 2304)])
 def test_larger_tiles(tokens, width, features, dtype):

@@ -192,10 +192,11 @@ def test_grads_outputs_that_overlap(records, bad):
     (ops.zs_grads_sumsq, [P, -1, P, P, 1 << 20, 0], "range"), (ops.zs_grads_sumsq, [0, 1, P, P, 1 << 20, 0], "NULL"),
     (ops.zs_grads_sumsq, [P, 1, 0, P, 1 << 20, 0], "NULL"), (ops.zs_grads_sumsq, [P, 1, P + 4, P, 1 << 20, 0], "aligned"),
     (ops.zs_grads_sumsq, [P + 8, 1, P, P, 1 << 20, 0], "aligned"), (ops.zs_grads_sumsq, [P, 1, P, 0, 1 << 20, 0], "workspace"),
-    (ops.zs_grads_sumsq, [P, 1, P, P, 255, 0], "workspace"), (ops.zs_grads_clip, [P, 1, 0.0, P, P, 0], "max_norm"),
-    (ops.zs_grads_clip, [P, 1, NAN, P, P, 0], "max_norm"), (ops.zs_grads_clip, [P, 1, INF, P, P, 0], "max_norm"),
-    (ops.zs_grads_clip, [P, 1, 1.0, 0, P, 0], "NULL"), (ops.zs_grads_clip, [0, 1, 1.0, P, P, 0], "NULL"),
-    (ops.zs_grads_clip, [P, 1, 1.0, P, P + 4, 0], "aligned"), (ops.zs_grads_clip, [P, -1, 1.0, P, P, 0], "range")])
+    (ops.zs_grads_sumsq, [P, 1, P, P, 255, 0], "workspace"),(ops.zs_grads_clip, [P, 1, 0.0, P, P, 0, 0, 0], "max_norm"), (ops.zs_grads_clip, [P, 1, NAN, P, P, 0, 0, 0], "max_norm"),
+    (ops.zs_grads_clip, [P, 1, INF, P, P, 0, 0, 0], "max_norm"), (ops.zs_grads_clip, [0, 1, 1.0, P, P, 0, 0, 0], "NULL"),
+    (ops.zs_grads_clip, [P, 1, 1.0, 0, P, 0, 0, 0], "workspace"), (ops.zs_grads_clip, [P, 1, 1.0, 0, P, P, 255, 0], "workspace"),
+    (ops.zs_grads_clip, [P, 1, 1.0, 0, P, P + 8, 1 << 20, 0], "workspace"), (ops.zs_grads_clip, [P, 1, 1.0, P, P + 4, 0, 0, 0], "aligned"),
+    (ops.zs_grads_clip, [P, 1, 1.0, P + 4, P, 0, 0, 0], "aligned"), (ops.zs_grads_clip, [P, -1, 1.0, P, P, 0, 0, 0], "range")])
 def test_grads_refusals(call, args, word):
     assert word in refused(call, *args)
 
