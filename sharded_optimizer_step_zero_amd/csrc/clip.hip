@@ -3,7 +3,7 @@
 //
 // The tensors are laid out once as a table of pieces of up to 4096 elements, each with its
 // addresses and types, so that ten thousand small tensors and one large matrix are the same
-// kind of work and a call is two or three launches however many there are.  A wave takes every
+// kind of work and a call is two launches however many there are.  A wave takes every
 // n-th piece by itself: what a small tensor takes is the way to its elements, and there are 8192
 // waves on it at once.  Squares are exact in fp64 (24 bits each) and finite whatever the
 // element, and are summed there in a fixed order.

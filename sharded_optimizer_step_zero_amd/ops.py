@@ -307,13 +307,14 @@ def _group(group):
 # twentieth of making a Stream object, which a call on a few rows would notice.
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
     lambda index: torch.cuda.current_stream(index).cuda_stream)
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 
 
 def _run(device, entry, *args):
     """Calls a C entry point on torch's current stream of the device, with that
     device current."""
     index = device.index
-    if torch.cuda.current_device() == index:
+    if _current_device() == index:
         rc = entry(*args, _raw_stream(index))
     else:
         with torch.cuda.device(index):
@@ -970,9 +971,7 @@ def preference_loss(loss, ref_loss, offsets, beta=0.1, kind="sigmoid", margin=0.
         _vector(ref_loss, "ref_loss", (torch.float32,), dev, tokens)
     k = _pick(_KINDS, kind, "kind")
     pairs = _pairs(offsets, mask, dev, tokens)
-    out = torch.empty(pairs, dtype=torch.float32, device=dev)
-    margins = torch.empty(pairs, dtype=torch.float32, device=dev)
-    rewards = torch.empty(pairs, 2, dtype=torch.float32, device=dev)
+    out, margins, rewards = loss.new_empty(pairs), loss.new_empty(pairs), loss.new_empty(pairs, 2)
     lengths = torch.empty(pairs, 2, dtype=torch.int32, device=dev)
     nbytes = _prefer_workspace_bytes(tokens, pairs)
     ws = _workspace(workspace, nbytes, dev) if nbytes != 256 else None  # 256: it is not used
