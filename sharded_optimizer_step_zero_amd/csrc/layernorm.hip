@@ -269,6 +269,13 @@ __global__ __launch_bounds__(T) void layer_norm_kernel(RowArgs<DT> g) {
     layer_norm_rows<DT, NT, NC, CODES, false>(g, slots);
 }
 
+// The first n of eight values, zeros for the others.
+__device__ __forceinline__ f32x8 first_of(f32x8 x, int n) {
+#pragma unroll
+  for (int i = 0; i < 8; i++) x[i] = i < n ? x[i] : 0.0f;
+  return x;
+}
+
 // The chunks of a row that the backward pass reads.
 template <int DT, int NC>
 struct GradRow {
@@ -332,6 +339,8 @@ __global__ __launch_bounds__(kGradThreads) void layer_norm_grad_kernel(
 #pragma unroll
     for (int k = 0; k < NC; k++) {
       h[k] = (take(now.s[k], k) - now.mean) * now.rstd;
+      // zeros behind the row's end and for no row: -mean rstd, which may be infinite, is not one
+      if (!whole || row >= rows) h[k] = first_of(h[k], row < rows ? width - (k * lanes + in_row) * 8 : 0);
       g[k] = take(now.dy[k], k);
       dw[k] += g[k] * h[k];
       db[k] += g[k];
@@ -380,7 +389,7 @@ __global__ __launch_bounds__(1024) void wide_means_kernel(
     const int64_t left = width - c;
     const Chunk<DT> a = load_row<DT>(sum + row * sum_stride, c, width);
     const Chunk<DT> b = load_row<DT>(dy + row * dy_stride, c, width);
-    const f32x8 h = (take8<DT>(a, left, width) - m) * r;
+    const f32x8 h = first_of((take8<DT>(a, left, width) - m) * r, (int)(left < 8 ? left : 8));
     const f32x8 g = take8<DT>(b, left, width) * load8<DT>(weight + c, left);
 #pragma unroll
     for (int i = 0; i < 8; i++) {

@@ -178,6 +178,25 @@ def test_backward(dtype, rows, width):
     check_backward(dy, s, w, ds, torch.float32 if rows % 2 else None)
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("width", [1, 64, 512, 1001, 8191, 8200])
+def test_backward_of_equal_large_elements(dtype, width):
+    """mean * rstd passes fp32's range, which nothing of the row itself does."""
+    g = gen(width)
+    dt = DT[dtype]
+    rows = 71
+    dy, w = rand(g, rows, width, dtype=dt), rand(g, width, dtype=dt, std=0.2, shift=1.0)
+    s = torch.full((rows, width), 2.0 ** 125, dtype=dt, device="cuda")
+    s[::2] *= -1
+    mean, rstd = s[:, 0].float().contiguous(), torch.full((rows,), 316.0, device="cuda")
+    want = M.layer_norm_grad(R.f64(dy), R.f64(s), R.f64(w), R.f64(mean), R.f64(rstd), None)
+    dx, dw, db = ops.layer_norm_backward(dy, s, w, mean, rstd)
+    # as in check_backward
+    R.close(dx, want[0], want[0].abs() * R.u(dt) * 1.01 + want[3] * 96 * E + R.sub(dt), "dx")
+    assert not dw.any()
+    R.close(db, want[2], want[2].abs() * R.u(dt) * 1.01 + want[5] * 260 * E + R.sub(dt), "db")
+
+
 def test_backward_without_a_bias_and_into_given_views():
     g = gen(21)
     dt = torch.bfloat16
