@@ -158,22 +158,25 @@ __global__ __launch_bounds__(256) void prefer_grad_kernel(PreferArgs g,
                                                           float* __restrict__ grad) {
   const int64_t t0 = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4;
   if (t0 >= g.tokens) return;
-  // the last sequence that begins at or before t0 (offsets do not fall)
-  int64_t low = -1, high = g.pairs * 2;  // offset[low] <= t0 < offset[high], as far as they exist
-  if (offset_of(g, high) <= t0) {
-    low = high;
-  } else {
+  const int64_t last = g.pairs * 2;
+  // the last sequence that begins at or before t (offsets do not fall), of those from `low` on:
+  // -1 before the first, `last` behind all of them
+  auto find = [&](int64_t t, int64_t low) {
+    int64_t high = last;
+    if (offset_of(g, high) <= t) return high;
     while (high - low > 1) {
       const int64_t mid = (low + high) >> 1;
-      if (offset_of(g, mid) <= t0)
+      if (offset_of(g, mid) <= t)
         low = mid;
       else
         high = mid;
     }
-  }
-  int64_t seq = low, end = seq < g.pairs * 2 ? offset_of(g, seq + 1) : g.tokens;
+    return low;
+  };
+  auto end_of = [&](int64_t s) { return s < last ? offset_of(g, s + 1) : g.tokens; };
+  int64_t seq = find(t0, -1), end = end_of(seq);
   auto factor = [&](int64_t s) {
-    if (s < 0 || s >= g.pairs * 2) return 0.0f;
+    if (s < 0 || s >= last) return 0.0f;
     const int64_t pair = s >> 1;
     const double m = g.margins[pair], smooth = g.smoothing;
     double slope;
@@ -195,13 +198,11 @@ __global__ __launch_bounds__(256) void prefer_grad_kernel(PreferArgs g,
   for (int i = 0; i < 4; i++) {
     const int64_t t = t0 + i;
     if (t >= g.tokens) return;
-    bool moved = false;
-    while (t >= end && seq < g.pairs * 2) {
-      seq++;
-      end = seq < g.pairs * 2 ? offset_of(g, seq + 1) : g.tokens;
-      moved = true;
+    if (t >= end && seq < last) {  // the next one, or the one behind any number of empty ones
+      end = end_of(++seq);
+      if (t >= end && seq < last) end = end_of(seq = find(t, seq));
+      f = factor(seq);
     }
-    if (moved) f = factor(seq);
     grad[t] = g.mask && !g.mask[t] ? 0.0f : f;
   }
 }

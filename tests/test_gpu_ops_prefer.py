@@ -106,6 +106,18 @@ def test_empty_sequences_and_masks_that_leave_nothing(kind, smoothing):
                                                average=average, mask=mask8).loss, r.loss)
 
 
+@pytest.mark.parametrize("empty", [1, 2, 3, 3001])
+def test_many_empty_sequences_between_two_tokens(empty):
+    """A thread's four tokens on either side of them, at each place among the four."""
+    for at in (4, 5, 6, 7):
+        o = torch.tensor([0, 3] + [at] * (empty + 1) + [9, 17][:2 - empty % 2], device="cuda")
+        pairs = (len(o) - 1) // 2
+        g = gen(at)
+        loss = torch.rand(20, generator=g, device="cuda")
+        grad = torch.rand(pairs, generator=g, device="cuda") + 0.1
+        check(loss, None, o, None, grad, 0.5, "sigmoid")
+
+
 def test_no_tokens_and_no_pairs():
     none = torch.empty(0, device="cuda")
     o = torch.zeros(5, dtype=torch.int64, device="cuda")
