@@ -133,6 +133,7 @@ struct Factor {
     first = c < 0x1p-120 ? 0x1p-120f : 1.0f;
     second = (float)(c < 0x1p-120 ? c * 0x1p120 : c);
   }
+  __device__ __forceinline__ bool one() const { return first == 1.0f && second == 1.0f; }
 };
 
 template <int DT, int OT>
@@ -162,7 +163,7 @@ __global__ __launch_bounds__(256) void scale_kernel(const Piece* __restrict__ pi
     const Piece p = next;
     if (i + step < n_pieces) next = pieces[n_pieces - 1 - i - step];
     // nowhere to go, or in place and unclipped: as it is
-    if (!p.out || (p.grad == p.out && c.second == 1.0f)) continue;
+    if (!p.out || (p.grad == p.out && c.one())) continue;
     auto go = [&](auto DT) {
       constexpr int kDt = decltype(DT)::value;
       if (p.out_dtype == ZS_F32)
@@ -181,11 +182,16 @@ __global__ __launch_bounds__(256) void scale_kernel(const Piece* __restrict__ pi
   }
 }
 
+// Whether all elements of a tensor are one run; otherwise each row is.
+bool one_run(const zs_grad_tensor& t) {
+  return t.rows <= 1 || (t.grad_stride == t.width && (!t.out || t.out_stride == t.width));
+}
+
 // Calls f(grad, out, elements) for each run of adjacent elements of a tensor.
 template <typename F>
 void each_run(const zs_grad_tensor& t, F f) {
   const int64_t eb = elem_bytes(t.dtype), ob = elem_bytes(t.out_dtype);
-  const bool whole = t.rows <= 1 || (t.grad_stride == t.width && (!t.out || t.out_stride == t.width));
+  const bool whole = one_run(t);
   const int64_t runs = whole ? 1 : t.rows, n = whole ? t.rows * t.width : t.width;
   if (n == 0) return;
   for (int64_t r = 0; r < runs; r++)
@@ -208,7 +214,10 @@ int check_list(const char* who, const zs_grad_tensor* list, int64_t n, int64_t* 
     if (t.rows && t.width && !t.grad) return fail(who, "NULL buffer");
     if (!al(t.grad, elem_bytes(t.dtype)) || (t.out && !al(t.out, elem_bytes(t.out_dtype))))
       return fail(who, "a buffer is not aligned to its elements");
-    each_run(t, [&](const void*, void*, int64_t m) { *pieces += (m + kPiece - 1) / kPiece; });
+    const int64_t runs = one_run(t) ? 1 : t.rows, n = one_run(t) ? t.rows * t.width : t.width;
+    const int64_t each = (n + kPiece - 1) / kPiece;
+    if (each && runs > kMaxPieces / each) return fail(who, "too many elements or rows");
+    *pieces += runs * each;
     if (*pieces > kMaxPieces) return fail(who, "too many elements or rows");
   }
   return ZS_OK;

@@ -113,6 +113,16 @@ def test_any_magnitude():
         check_out([t], want, norm, ops.clip_grads([t], 1.0))
 
 
+def test_a_factor_next_to_where_it_is_split():
+    """2^-120 (1 - 2^-26), which is 2^-120 in fp32: not a factor of one."""
+    for norm, want in ((2.0 ** 20 + 2.0 ** -6 - 1e-6, 2.0 ** -120), (2.0 ** 20 - 1e-6, 2.0 ** -120),
+                       (2.0 ** 20 * 1.5 - 1e-6, 2.0 ** -120 / 1.5)):
+        t = torch.ones(5000, device="cuda")
+        sumsq = torch.tensor(norm ** 2, dtype=torch.float64, device="cuda")
+        ops.clip_grads([t], 2.0 ** -100, sumsq=sumsq)
+        assert bool(((t.double() - want).abs() <= want * (2.0 ** -24 + 2.0 ** -25)).all())
+
+
 @pytest.mark.parametrize("bad", [float("nan"), float("inf")])
 def test_values_that_are_not_finite(bad):
     """As the step's clip: a NaN reaches everything, an infinity makes 0 of the rest and NaN of itself."""

@@ -145,6 +145,13 @@ def test_grads_list_refusals(r, word):
     assert word in refused(ops.zs_grads_pieces, [r])
 
 
+def test_a_list_of_too_many_rows_is_refused_without_counting_them():
+    assert "too many" in refused(ops.zs_grads_pieces, [record(P, P, 1 << 40, 1, gs=2)])
+    assert "too many" in refused(ops.zs_grads_pieces, [record(P, P, 1 << 26, 1, gs=2), record(P, P, 1, 1)])
+    assert ops.zs_grads_pieces([record(P, P, 1 << 26, 1, gs=2)]) == 1 << 26
+    assert ops.zs_grads_pieces([record(P, P, 1 << 40, 0, gs=2)]) == 0
+
+
 def table(records):
     n = ops.zs_grads_pieces(records)
     buf = ctypes.create_string_buffer(max(1, n) * 32)
