@@ -282,6 +282,8 @@ size_t zs_prefer_workspace_bytes(int64_t tokens, int64_t pairs);
  *   ZS_SIGMOID  -(1 - smoothing) * log sigma(m) - smoothing * log sigma(-m)
  *   ZS_HINGE    max(0, 1 - m)
  *   ZS_SQUARED  (m - 1/2)^2 / beta^2
+ * which have their limits where m is infinite (a token without probability: its loss or ref_loss
+ * is infinite): 0 for the hinge at +infinity and for the sigmoid where smoothing is 0.
  * lengths: the tokens that count in each sequence (a sequence of none has a = 0).  Sums in fp64.
  * beta > 0, 0 <= smoothing <= 0.5 (ZS_SIGMOID only); tokens < 2^31, pairs <= 2^22.
  */

@@ -7,7 +7,9 @@
 //   hinge     L = max(0, 1 - m)
 //   squared   L = (m - 1/2)^2 / beta^2
 // The gradient of sum_p grad_p L_p by l_t is -+ beta L'(m) grad_p (over the length for means) for
-// the tokens of the chosen and of the rejected.
+// the tokens of the chosen and of the rejected.  A token without probability (l or r infinite) makes
+// the margin infinite, where these have their limits: 0 of the hinge and of the sigmoid's side
+// that is certain.
 //
 // Bound by latency up to some 100 thousand tokens, by HBM beyond.  Forward: half a workgroup a
 // sequence, sums in fp64 in a fixed order, the loss by its last step; few long sequences are
@@ -90,9 +92,9 @@ __device__ __forceinline__ void finish_pair(const PreferArgs& g, int64_t pair, P
   const double m = a[0] - a[1] - (double)g.margin, s = g.smoothing;
   double loss;
   if (g.kind == ZS_SIGMOID)
-    loss = (1.0 - s) * softplus(-m) + s * softplus(m);
+    loss = (1.0 - s) * softplus(-m) + (s > 0.0 ? s * softplus(m) : 0.0);  // not 0 times infinity
   else if (g.kind == ZS_HINGE)
-    loss = m < 1.0 ? 1.0 - m : m - m;  // NaN stays NaN
+    loss = m < 1.0 ? 1.0 - m : m >= 1.0 ? 0.0 : m;  // NaN stays NaN
   else
     loss = (m - 0.5) * (m - 0.5) / ((double)g.beta * (double)g.beta);
   g.margins[pair] = (float)m;
@@ -183,7 +185,7 @@ __global__ __launch_bounds__(256) void prefer_grad_kernel(PreferArgs g,
     if (g.kind == ZS_SIGMOID)
       slope = smooth - 1.0 / (1.0 + exp(m));  // -(1-s) sigma(-m) + s sigma(m)
     else if (g.kind == ZS_HINGE)
-      slope = m < 1.0 ? -1.0 : m - m;
+      slope = m < 1.0 ? -1.0 : m >= 1.0 ? 0.0 : m;
     else
       slope = 2.0 * (m - 0.5) / ((double)g.beta * (double)g.beta);
     slope *= (double)g.beta * (double)grad_loss[pair];
