@@ -284,6 +284,7 @@ size_t zs_prefer_workspace_bytes(int64_t tokens, int64_t pairs);
  *   ZS_SQUARED  (m - 1/2)^2 / beta^2
  * which have their limits where m is infinite (a token without probability: its loss or ref_loss
  * is infinite): 0 for the hinge at +infinity and for the sigmoid where smoothing is 0.
+ * margins are rounded to nearest, but a hinge's below 1 stays below it.
  * lengths: the tokens that count in each sequence (a sequence of none has a = 0).  Sums in fp64.
  * beta > 0, 0 <= smoothing <= 0.5 (ZS_SIGMOID only); tokens < 2^31, pairs <= 2^22.
  */
@@ -295,7 +296,8 @@ int zs_prefer_forward(const float *loss, const float *ref_loss, const void *offs
 
 /*
  * grad[t] = the derivative of sum_p grad_loss[p] * pair_loss[p] by loss[t], for every token: 0
- * where it does not count or lies in no sequence.  margins and lengths are the forward's.
+ * where it does not count or lies in no sequence.  margins and lengths are the forward's; the
+ * slope is the one at the margin as it is held there, in fp32.
  */
 int zs_prefer_backward(const float *margins, const int32_t *lengths, const void *offsets,
                        const void *mask, const float *grad_loss, float *grad, int64_t tokens,

@@ -97,7 +97,11 @@ __device__ __forceinline__ void finish_pair(const PreferArgs& g, int64_t pair, P
     loss = m < 1.0 ? 1.0 - m : m >= 1.0 ? 0.0 : m;  // NaN stays NaN
   else
     loss = (m - 0.5) * (m - 0.5) / ((double)g.beta * (double)g.beta);
-  g.margins[pair] = (float)m;
+  // The slope is taken from the margin as it is returned, in fp32: that moves it by no more than
+  // rounding every token's difference to fp32 once would.  The hinge has a step in it: a margin
+  // below 1 stays below.
+  const float held = (float)m;
+  g.margins[pair] = g.kind == ZS_HINGE && m < 1.0 && held >= 1.0f ? 0x1.fffffep-1f : held;
   g.loss_out[pair] = (float)loss;
 }
 
