@@ -126,6 +126,12 @@ __device__ __forceinline__ uint32_t scale_byte_of(int code, float amax) {
                          : code == ZS_E5M2 ? scale_byte<ZS_E5M2>(amax) : scale_byte<ZS_E2M1>(amax);
 }
 
+// Differences from the mean may pass fp32's range where the elements do not.  Some difference is
+// above 2^127 only where the deviation is above 2^119 (65536 columns): such rows' differences are
+// taken in quarters, which are exact there, and times four times the deviation's inverse, which
+// is then a normal number too.
+constexpr float kFarApart = 0x1p-110f;  // the deviation's inverse
+
 // WHOLE: the threads' chunks cover the row exactly.
 template <int DT, bool NT, int NC, bool CODES, bool WHOLE>
 __device__ __forceinline__ void layer_norm_rows(const RowArgs<DT>& g, double (&slots)[2][16]) {
@@ -182,14 +188,21 @@ __device__ __forceinline__ void layer_norm_rows(const RowArgs<DT>& g, double (&s
   }
   const double variance = sum_row(sq, lanes, 0, slots[1]) * g.inv_width;
   const double root = inverse_root(variance + (double)g.eps);
-  const float r = (float)root;
+  float r = (float)root;
   // the mean in two parts: a difference from it is off by two roundings of itself
-  const float m_high = (float)m, m_low = (float)(m - (double)m_high);
+  float m_high = (float)m, m_low = (float)(m - (double)m_high);
   if (live && in_row == 0) {
     g.mean[row] = m_high;
     g.rstd[row] = r;
   }
   if constexpr (!CODES) {
+    if (r < kFarApart) {
+#pragma unroll
+      for (int k = 0; k < NC; k++) s[k] *= 0.25f;
+      m_high *= 0.25f;
+      m_low *= 0.25f;
+      r = (float)(root * 4.0);
+    }
 #pragma unroll
     for (int k = 0; k < NC; k++) {
       const int c = (k * lanes + in_row) * 8, left = count(k);

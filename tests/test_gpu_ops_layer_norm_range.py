@@ -1,0 +1,40 @@
+"""The layer norm of finite rows whose elements differ from their mean by more than the largest
+fp32 value: the outputs are of ordinary size."""
+import pytest
+import torch
+
+import _ops_ref as R
+from test_gpu_ops_layer_norm import check_forward, gen, rand
+
+pytestmark = pytest.mark.gpu
+WIDTHS = [8, 40, 515, 1001, 2048, 8192, 8200, 12289]
+
+
+def far_apart(rows, width, dtype, seed):
+    """Rows of +-(2.9 to 3.3)e38, one element in eight on the other side, so that the mean is some
+    2.3e38 and the differences up to 5.6e38; the last row is an ordinary one."""
+    g = gen(seed)
+    x = 2.9e38 + torch.rand(rows, width, generator=g, device="cuda") * 0.4e38
+    x[:, ::8] *= -1
+    x[::2] *= -1
+    x[-1] = torch.randn(width, generator=g, device="cuda")
+    x = x.to(dtype)
+    assert bool(torch.isfinite(x).all())
+    d = (R.f64(x) - R.f64(x).mean(1, keepdim=True)).abs()
+    assert bool((d[:-1].amax(1) > torch.finfo(torch.float32).max).all())
+    return x
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("width", WIDTHS)
+def test_forward(dtype, width):
+    g = gen(width)
+    x = far_apart(5, width, dtype, width)
+    w, b = rand(g, width, dtype=dtype, std=0.2, shift=1.0), rand(g, width, dtype=dtype, std=0.3)
+    r = check_forward(x, w, b, None, 1e-5)
+    # the path with codes has the same output
+    assert bool(torch.isfinite(check_forward(x, w, b, None, 1e-5, "e4m3").y).all())
+    assert bool(torch.isfinite(r.y).all())
+    # as the sum with a residual
+    half = x * 0.5
+    check_forward(half, w, b, half, 1e-5)
