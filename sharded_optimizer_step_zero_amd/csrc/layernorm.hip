@@ -289,6 +289,21 @@ __device__ __forceinline__ f32x8 first_of(f32x8 x, int n) {
   return x;
 }
 
+// h = (s - mean) rstd of a row; where it is far apart, the differences in quarters.
+struct Scaled {
+  float part, mean, rstd;  // of the differences, and the others accordingly
+  __device__ __forceinline__ Scaled(float m, float r) {
+    part = r < kFarApart ? 0.25f : 1.0f;
+    mean = m * part;
+    rstd = r < kFarApart ? r * 4.0f : r;
+  }
+  __device__ __forceinline__ f32x8 operator()(f32x8 s) const {
+#pragma unroll
+    for (int i = 0; i < 8; i++) s[i] = __builtin_fmaf(s[i], part, -mean) * rstd;
+    return s;
+  }
+};
+
 // The chunks of a row that the backward pass reads.
 template <int DT, int NC>
 struct GradRow {
@@ -344,6 +359,7 @@ __global__ __launch_bounds__(kGradThreads) void layer_norm_grad_kernel(
     if (row0 + step < rows) next = load(row + step);
     f32x8 h[NC], g[NC];
     f32x2 dot = {};
+    const Scaled scaled(now.mean, now.rstd);
     auto take = [&](const Chunk<DT>& x, int k) {  // zeros behind the row's end, and for no row
       if (whole && row < rows) return widen<DT>(x);
       const int left = row < rows ? width - (k * lanes + in_row) * 8 : 0;
@@ -351,7 +367,7 @@ __global__ __launch_bounds__(kGradThreads) void layer_norm_grad_kernel(
     };
 #pragma unroll
     for (int k = 0; k < NC; k++) {
-      h[k] = (take(now.s[k], k) - now.mean) * now.rstd;
+      h[k] = scaled(take(now.s[k], k));
       // zeros behind the row's end and for no row: -mean rstd, which may be infinite, is not one
       if (!whole || row >= rows) h[k] = first_of(h[k], row < rows ? width - (k * lanes + in_row) * 8 : 0);
       g[k] = take(now.dy[k], k);
@@ -396,13 +412,13 @@ __global__ __launch_bounds__(1024) void wide_means_kernel(
     const float* __restrict__ rstd, f32x2* __restrict__ means, int64_t width) {
   __shared__ f32x2 slots[16];
   const int64_t row = blockIdx.x;
-  const float m = mean[row], r = rstd[row];
+  const Scaled scaled(mean[row], rstd[row]);
   f32x2 dot = {};
   for (int64_t c = threadIdx.x * 8; c < width; c += 1024 * 8) {
     const int64_t left = width - c;
     const Chunk<DT> a = load_row<DT>(sum + row * sum_stride, c, width);
     const Chunk<DT> b = load_row<DT>(dy + row * dy_stride, c, width);
-    const f32x8 h = first_of((take8<DT>(a, left, width) - m) * r, (int)(left < 8 ? left : 8));
+    const f32x8 h = first_of(scaled(take8<DT>(a, left, width)), (int)(left < 8 ? left : 8));
     const f32x8 g = take8<DT>(b, left, width) * load8<DT>(weight + c, left);
 #pragma unroll
     for (int i = 0; i < 8; i++) {
@@ -433,9 +449,9 @@ __global__ __launch_bounds__(256) void wide_strip_kernel(
     const Chunk<DT> b = load_row<DT, NT>(dy + row * dy_stride, c, width);
     Chunk<DT> add = {};
     if (ds) add = load_row<DT, NT>(ds + row * ds_stride, c, width);
-    const float m = mean[row], r = rstd[row];
+    const float r = rstd[row];
     const f32x2 both = means[row];
-    const f32x8 h = (take8<DT>(a, left, width) - m) * r;
+    const f32x8 h = Scaled(mean[row], r)(take8<DT>(a, left, width));
     f32x8 g = take8<DT>(b, left, width);
     dw += g * h;
     db += g;

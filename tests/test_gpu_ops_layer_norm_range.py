@@ -1,12 +1,15 @@
 """The layer norm of finite rows whose elements differ from their mean by more than the largest
-fp32 value: the outputs are of ordinary size."""
+fp32 value: the outputs are of ordinary size, and so are the weight's gradients."""
 import pytest
 import torch
 
+import _more_ref as M
 import _ops_ref as R
+from sharded_optimizer_step_zero_amd import ops
 from test_gpu_ops_layer_norm import check_forward, gen, rand
 
 pytestmark = pytest.mark.gpu
+E = R.E
 WIDTHS = [8, 40, 515, 1001, 2048, 8192, 8200, 12289]
 
 
@@ -38,3 +41,24 @@ def test_forward(dtype, width):
     # as the sum with a residual
     half = x * 0.5
     check_forward(half, w, b, half, 1e-5)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("width", WIDTHS)
+def test_backward(dtype, width):
+    g = gen(width + 1)
+    rows = 41
+    s = far_apart(rows, width, dtype, width + 2)
+    dy, w = rand(g, rows, width, dtype=dtype), rand(g, width, dtype=dtype, std=0.2, shift=1.0)
+    x = R.f64(s)
+    mean = x.mean(1)
+    rstd = 1 / torch.sqrt(((x - mean[:, None]) ** 2).mean(1) + 1e-5)
+    mean, rstd = mean.float(), rstd.float()
+    want = M.layer_norm_grad(R.f64(dy), x, R.f64(w), mean.double(), rstd.double(), None)
+    dx, dw, db = ops.layer_norm_backward(dy, s, w, mean.cuda(), rstd.cuda(), weight_grad_dtype=torch.float32)
+    # as for other rows: a lane adds up to 64 terms and joins 10 times, and ten roundings of a term;
+    # here dx is below fp32's normal range before its rounding to the type, which may round it twice
+    R.close(dx, want[0], want[0].abs() * R.u(dtype) * 1.01 + want[3] * 96 * E + R.sub(dtype) + R.sub(torch.float32), "dx")
+    # under 260 additions of a column
+    R.close(dw, want[1], want[1].abs() * E * 1.01 + want[4] * 260 * E, "dw")
+    R.close(db, want[2], want[2].abs() * E * 1.01 + want[5] * 260 * E, "db")
