@@ -337,8 +337,8 @@ int zs_grads_sumsq(const void *table, int64_t pieces, double *sumsq, void *works
  * With the device double *sumsq (of this list, or summed over the ranks; NULL: this list's is taken
  * here, for which alone the workspace is used): norm = sqrt(*sumsq),
  * out = c * grad with c = min(1, max_norm / (norm + 1e-6)) in fp32, rounded once to the
- * output's type; *norm_out (device, may be NULL) = norm.  Every gradient of the list has an
- * output.  One that is its own output is left alone where c is 1.
+ * output's type; *norm_out (device, may be NULL, not sumsq) = norm.  Every gradient of the list
+ * has an output.  One that is its own output is left alone where c is 1.
  */
 int zs_grads_clip(const void *table, int64_t pieces, float max_norm, const double *sumsq,
                   double *norm_out, void *workspace, size_t workspace_bytes, void *stream);

@@ -333,6 +333,8 @@ extern "C" int zs_grads_clip(const void* table, int64_t pieces, float max_norm,
   if (pieces && !table) return fail(who, "NULL buffer");
   if (!al(sumsq, 8) || !al(norm_out, 8) || !al(table, 32))
     return fail(who, "a buffer is not aligned to its elements");
+  // one workgroup writes the norm while others may not have read the sum yet
+  if (sumsq && sumsq == norm_out) return fail(who, "the sum of squares and the norm are the same buffer");
   int32_t parts = 0;
   if (!sumsq)
     if (int rc = enqueue_squares(who, table, pieces, workspace, workspace_bytes, &parts, (hipStream_t)stream))
