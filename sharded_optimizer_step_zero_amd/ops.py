@@ -1035,7 +1035,9 @@ class GradList:
     (views of a contribution buffer of ZeroShard); without it they are clipped in place.  The
     list holds its tensors and their addresses: a tensor must not be resized or given other
     memory.  Making it copies a table to the device and is not captured in a graph; the calls
-    that use it are."""
+    that use it are, and a graph reads the list's table at every replay: the list has to outlive
+    it.  Calls on any stream hold the table until their work is done, so a list may be dropped
+    behind them."""
 
     def __init__(self, tensors, out=None):
         self.tensors = list(tensors)
@@ -1067,10 +1069,15 @@ class GradList:
         host = torch.empty(max(1, self.pieces) * 32, dtype=torch.uint8, device="cpu")
         _check(_grads_table(words.data_ptr(), len(records), host.data_ptr(), host.numel()))
         self.table = host.to(dev)
+        self._stream = _raw_stream(dev.index)  # the one that the table's memory belongs to
 
 
 def _grad_list(grads):
-    return grads if isinstance(grads, GradList) else GradList(grads)
+    if not isinstance(grads, GradList):
+        return GradList(grads)
+    if _raw_stream(grads.device.index) != grads._stream:
+        grads.table.record_stream(torch.cuda.current_stream(grads.device))
+    return grads
 
 
 def grad_sumsq(grads, out=None, workspace=None):
