@@ -1049,6 +1049,9 @@ class GradList:
         self.device = self.tensors[0].device
         if not self.tensors[0].is_cuda:
             raise ValueError(f"tensors: on {self.device}, expected a GPU")
+        with torch.cuda.device(self.device):
+            if torch.cuda.is_current_stream_capturing():
+                raise ValueError("a GradList copies its table to the device: it is made before a capture")
         dev, codes = self.device, {(a, b): _DTYPES[a] | _DTYPES[b] << 32 for a in _DTYPES for b in _DTYPES}
         records = []  # zs_grad_tensor, word by word
         for i, (g, o) in enumerate(zip(self.tensors, self.out or self.tensors)):
