@@ -238,7 +238,11 @@ int zs_layer_norm_backward(const void *dy, int64_t dy_stride, const void *sum, i
 int zs_mx4_pack(const void *x, int64_t x_stride, void *codes, void *scales, void *codes_t,
                 void *scales_t, int64_t rows, int64_t width, int32_t dtype, void *stream);
 
-/* Back: each value rounded once to `dtype` (exact in bf16 and fp32). */
+/*
+ * Back: each value rounded once to `dtype`.  That is exact in bf16 and fp32 but for 4 * 2^126,
+ * the code of magnitudes from 3.5 * 2^126 on, which becomes infinity (zs_mx4_product takes it
+ * as it is).
+ */
 int zs_mx4_unpack(const void *codes, const void *scales, void *x, int64_t x_stride, int64_t rows,
                   int64_t width, int32_t dtype, void *stream);
 

@@ -875,7 +875,7 @@ def pack4(x, want="rows"):
 
 def unpack4(c, dtype, out=None):
     """The values of a matrix in the 4-bit form, each rounded once to dtype (exact in bf16 and
-    fp32)."""
+    fp32 but for 2^128, the form of magnitudes from 3.5 * 2^126 on: infinity)."""
     dt = _pick(_DTYPES, dtype, "dtype")
     rows = _codes4(c, "c")
     dev = c.codes.device
