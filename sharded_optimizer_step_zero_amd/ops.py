@@ -240,6 +240,7 @@ _CODES = {"e4m3": (ZS_E4M3, torch.float8_e4m3fn), "e5m2": (ZS_E5M2, torch.float8
 _CODE_OF = {torch.float8_e4m3fn: ZS_E4M3, torch.float8_e5m2: ZS_E5M2}
 _SCALE = torch.float8_e8m0fnu
 _FOUR = torch.float4_e2m1fn_x2
+_NORM_CODES = {**_CODES, "e2m1": (ZS_E2M1, _FOUR)}
 _KINDS = {"sigmoid": ZS_SIGMOID, "hinge": ZS_HINGE, "squared": ZS_SQUARED}
 _ACTS = {"silu": ZS_SILU, "gelu": ZS_GELU}
 _ID_BYTES = {torch.int64: 8, torch.int32: 4}
@@ -738,14 +739,14 @@ def layer_norm(x, weight, bias=None, residual=None, eps=1e-5, code=None, group=N
     mean, rstd = stats.unbind()
     codes = scales = None
     cd = 0
-    if code == "e2m1":
-        cd = ZS_E2M1
+    if code is not None:
+        cd, ct = _pick(_NORM_CODES, code, "code")
+    if cd == ZS_E2M1:
         if group not in (None, 32):
             raise ValueError(f"group: {group!r}, the 4-bit form has groups of 32")
         group = 32
         codes, scales = _empty4(rows, width, dev)
     elif code is not None:
-        cd, ct = _pick(_CODES, code, "code")
         group = _group(128 if group is None else group)
         codes = torch.empty(rows, width, dtype=ct, device=dev)
         scales = torch.empty(rows, -(-width // group), dtype=_SCALE, device=dev)
