@@ -6,7 +6,8 @@
 // 4 neighbouring lanes.  Along columns (the transpose's rows) a lane has 32 rows of four columns in
 // registers, so that a column's group is its own; with both wanted a row's group is eight
 // lanes', and the matrix is read once.  16-bit elements are compared and rounded as they are, two
-// at a time.  22016 x 4096 bf16 both ways 57 us (4.8 TB/s), rows 38 (6.0); 8192 x 22016 127 and 87.
+// at a time.  8192 x 22016 bf16, which passes the last-level cache, both ways 125 us (4.4 TB/s), along
+// rows 87 (5.2); 22016 x 4096 69 and 43 from HBM, 57 and 38 where the cache holds it from before.
 // (A tile of 128 x 128 turned in LDS, its 16-byte and single-byte pieces written apart: 150.)
 //
 // The product: out[t][n] = sum_k x[t][k] w[n][k] of the values codes * scales, on 16x16x128
@@ -17,8 +18,9 @@
 //
 // All tiles take 256 k a step, two steps in LDS, which global memory is read straight into: a row
 // has 128 bytes there, a cache line of memory (64-byte pieces of lines have twice the requests,
-// which the L2 answers no faster than one a channel and cycle: 8192 x 4096 x 22016 took 430 us).  A row's chunk c of 16 bytes sits at c ^ (row & 7): no bank conflicts.  Rows past the edge
-// and groups past the end read as zeros by the buffer loads' bounds check.
+// which the L2 answers no faster than one a channel and cycle: 8192 x 4096 x 22016 took 430 us).  A
+// row's chunk c of 16 bytes sits at c ^ (row & 7): no bank conflicts.  Rows past the edge and groups
+// past the end read as zeros by the buffer loads' bounds check.
 //
 // Large products: 256 x 256, four waves of 128 x 128 whose sums fill the accumulation registers
 // (eight waves of 128 x 64: 460 us).  A half step's fragments are read while the half before
@@ -26,17 +28,21 @@
 // under way for a step and a half, have landed and this one's place is free.  A workgroup goes
 // on from tile to tile: the next one's first loads are under way before the last one's
 // products end, and its rows leave through LDS in pieces of 256 bytes (32-byte pieces straight
-// from the registers: 402 us; 64-byte ones: 368; these 360, and 338 streamed).  Smaller products take 128 x 128 or 128 x 64
-// tiles, two or three workgroups a compute unit.
+// from the registers: 402 us; 64-byte ones: 368; these 357, and 330 streamed).  Smaller products take
+// 128 x 128 or 128 x 64 tiles, two or three workgroups a compute unit.
 //
 // Few tokens: the weight is what is read, each of its rows by one workgroup, whose waves share
-// k out between them and add their sums in LDS: 16 x 4096 x 22016 14 us (3.5 TB/s, weights from
-// HBM; a pass of 48 MB has about 3 us of start and end, and the tokens' codes come again for
-// every 32 features: one token 12 us).
+// k out between them and add their sums in LDS: 16 x 4096 x 22016 in a graph 13.6 us (3.5 TB/s, weights
+// from HBM; a pass of 48 MB has about 3 us of start and end, a wave has one span of this width and
+// nothing under way behind it, and the tokens' codes come again for every 32 features: one token
+// 11.5 us).
 //
-// Measured, bf16 out: 8192 x 22016 x 4096 (tokens x width x features) 279 us, 5.3 PFLOP/s; 22016 x
-// 8192 x 4096 311 us; 8192 x 4096 x 22016, sixteen steps a tile and 360 MB to write, 338 us, 4.4
-// PFLOP/s.  The clock gives way under the load: on zeros the first takes 232 us (6.4 PFLOP/s).
+// Measured, bf16 out: 8192 x 22016 x 4096 (tokens x width x features) 285 us, 5.2 PFLOP/s; 22016 x
+// 8192 x 4096 327 us; 8192 x 4096 x 22016, sixteen steps a tile and 360 MB to write, 330 us, 4.5
+// PFLOP/s.  What bounds them is the card's power (on zeros, at a higher clock, the first takes 232 us, 6.4
+// PFLOP/s) and LDS: a half step's 1024 cycles of matrix instructions come with 64 KB of fragments read
+// and 32 KB of codes written there, at 128 bytes a cycle three quarters of them; the matrix cores are
+// busy for 55% of the cycles.
 #include <algorithm>
 
 #include "ops.h"
@@ -105,8 +111,8 @@ __device__ __forceinline__ uint32_t byte4(float amax, float* scale) {
 }
 
 // From so many blocks of 256 x 256 on; below, 64 x 256, so that the card has work.  us with large and
-// with small blocks, bf16 from HBM: 8192 x 4096 (512) 33 and 26, 22016 x 4096 (1376) 70 and 74, 8192
-// x 22016 (2752) 130 and 182.
+// with small blocks, bf16 from HBM: 8192 x 4096 (512) 31 and 24, 22016 x 4096 (1376) 69 and 72, 8192
+// x 22016 (2752) 126 and 178.
 constexpr int64_t kLargeBlocks = 1024;
 
 // WAVES * 32 rows x 256 columns: a lane has 32 rows of four columns, so that a group along columns
@@ -1116,8 +1122,8 @@ extern "C" int zs_mx4_product(const void* x_codes, const void* x_scales, const v
   g.groups = (int32_t)groups_of(width);
   g.c = out;
   g.ldc = out_stride;
-  // 8192 x 4096 x 22016 (360 MB) 338 us streamed and 369 not, 16384 x 8192 x 8192 (268 MB) 453 and
-  // 472, 16384 x 2048 x 8192 141 and 137; smaller outputs are read again from the cache
+  // 8192 x 4096 x 22016 (360 MB) 330 us streamed and 357 not, 16384 x 8192 x 8192 (268 MB) 451 and
+  // 477, 16384 x 2048 x 8192 143 and 140; smaller outputs are read again from the cache
   g.streaming = streams(tokens * features * elem_bytes(dtype));
   const hipStream_t st = (hipStream_t)stream;
   auto tiles = [&](int64_t bm, int64_t bn) {

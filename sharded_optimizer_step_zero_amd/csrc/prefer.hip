@@ -16,8 +16,9 @@
 // divided over workgroups, and a second kernel adds the parts.  Backward: a thread has four
 // neighbouring tokens and looks for their sequence among the offsets, so the work is even
 // whatever the lengths and every token is written once, those of no sequence too (zeros).
-// Measured: 4 pairs of 1600 tokens in all 3.5 + 4.5 us, 256 pairs of a million tokens, with a mask, 6
-// us (0.9 TB/s) + 8; a launch alone takes 3.
+// Measured: 4 pairs of 1600 tokens in all 3.6 + 4.7 us, 256 pairs of a million tokens, with a mask, 6
+// us (0.9 TB/s) + 8 (every thread's search is nine loads of offsets, each behind the one before); a
+// launch alone takes 3.
 #include <algorithm>
 
 #include "ops.h"
@@ -152,7 +153,10 @@ __global__ __launch_bounds__(256) void join_kernel(PreferArgs g, const Part* __r
 }
 
 // Slices of a sequence: until the card has some 512 workgroups, each slice 4096 tokens on the
-// average or more.
+// average or more.  us undivided and divided, in a graph (pairs x tokens a sequence): 4 x 8192 7.8 and
+// 6.9, 4 x 32768 21 and 7.7, 64 x 16384 12.5 and 7.7.  Slices of 2048 take 5.8 for 5.5 at 4 x 4096, 6.0
+// for 6.9 at 4 x 8192 and 15 for 11 at 1 x 131072; 256 workgroups 15 for 11 at 64 x 32768, 1024 32 for
+// 21 at 4 x 524288.
 int64_t slices_of(int64_t tokens, int64_t pairs) {
   const int64_t wanted = 256 / std::max<int64_t>(pairs, 1), most = tokens / (std::max<int64_t>(pairs, 1) * 2) / 4096;
   return std::max<int64_t>(1, std::min(wanted, most));
