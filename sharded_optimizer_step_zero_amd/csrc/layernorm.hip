@@ -17,12 +17,12 @@
 // the odd side, so that each code is one rounding of y.  (The output in fp32 with an error bound,
 // and both of its ends encoded, took 260 us for 203.)
 //
-// Bound by HBM.  Measured, bf16, among other calls: forward at 16384 x 8192 with residual and 8-bit codes 178
-// to 192 us for 943 MB, by where its arrays lie (5.3 to 4.9 TB/s; the vector unit is busy for three quarters
-// of it), in 4 bits 173; backward at 32768 x 2048 96 us for 537 MB (5.6 TB/s), 16384 x 8192 186 us
-// (5.8), 8192 x 12288 in two passes 216 us.  Above 32768 columns a thread has eight chunks and spills
-// registers: with residual, in 16 and in 8 bits, 4096 x 32768 185 and 210 us, 4096 x 49152 420 and
-// 1350, 4096 x 65536 730 and 690.
+// Bound by HBM.  Measured, bf16, among other calls: forward at 16384 x 8192 with residual and 8-bit
+// codes 178 to 192 us for 943 MB, by where its arrays lie (5.3 to 4.9 TB/s; the vector unit is busy for
+// three quarters of it), in 4 bits 173; backward at 32768 x 2048 96 us for 537 MB (5.6 TB/s), 16384 x
+// 8192 186 us (5.8), 8192 x 12288 in two passes 216 us.  Above 32768 columns a thread has eight chunks
+// and spills registers: with residual, in 16 and in 8 bits, 4096 x 32768 185 and 210 us, 4096 x 49152
+// 420 and 1350, 4096 x 65536 730 and 690.
 #include "rows.h"
 
 namespace zs {
@@ -50,7 +50,7 @@ struct RowArgs {
 
 // Sums and maxima over lanes by moves inside the vector unit (the LDS ways of a shuffle wait some
 // hundred cycles each, of which a row has fourteen in a chain: forward at 16384 x 8192 195 us for
-// 183, at 32768 x 2048 115 for 98, backward there 101 for 96, each pair on one box).
+// 183, at 32768 x 2048 115 for 98, backward there 101 for 96).
 
 // x of another lane of the row of 16: CTRL 0xb1 lane ^ 1, 0x4e lane ^ 2, 0x141 the other end of the
 // eight, 0x140 of the sixteen.

@@ -988,7 +988,8 @@ def preference_loss_backward(forward, offsets, grad_loss, tokens, beta=0.1, kind
                              smoothing=0.0, average=False, mask=None, out=None):
     """The gradient of sum(grad_loss * preference_loss(...).loss) by each token's loss, fp32
     [tokens]: linear_xent_backward's grad_loss.  forward is what preference_loss returned for
-    the same offsets, mask and settings; tokens that do not count or lie in no sequence get 0."""
+    the same offsets, mask and settings, and the slope is the one at its margins, as they are held
+    in fp32; tokens that do not count or lie in no sequence get 0."""
     dev = offsets.device
     if not offsets.is_cuda:
         raise ValueError(f"offsets: on {dev}, expected a GPU")

@@ -62,3 +62,34 @@ def test_backward(dtype, width):
     # under 260 additions of a column
     R.close(dw, want[1], want[1].abs() * E * 1.01 + want[4] * 260 * E, "dw")
     R.close(db, want[2], want[2].abs() * E * 1.01 + want[5] * 260 * E, "db")
+
+
+def within(rows, width, dtype, seed):
+    """One row a power of two, from deviations of 2^96 to 2^126, some far from zero."""
+    g = gen(seed)
+    e = torch.linspace(96, 126, rows, device="cuda").round()
+    x = torch.rand(rows, width, generator=g, device="cuda") * 2 - 1
+    x[::3] += 0.75
+    x = (x * torch.exp2(e)[:, None]).to(dtype)
+    assert bool(torch.isfinite(x).all())
+    return x
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("width", [40, 1001, 8200, 40000])
+def test_deviations_below_and_above_the_border(dtype, width):
+    g = gen(width)
+    x = within(31, width, dtype, width)
+    w, b = rand(g, width, dtype=dtype, std=0.2, shift=1.0), rand(g, width, dtype=dtype, std=0.3)
+    check_forward(x, w, b, None, 1e-5)
+    check_forward(x, w, None, None, 0.0)
+    dy = rand(g, 31, width, dtype=dtype)
+    s = R.f64(x)
+    mean = s.mean(1)
+    rstd = 1 / torch.sqrt(((s - mean[:, None]) ** 2).mean(1))
+    mean, rstd = mean.float(), rstd.float()
+    want = M.layer_norm_grad(R.f64(dy), s, R.f64(w), mean.double(), rstd.double(), None)
+    dx, dw, _ = ops.layer_norm_backward(dy, x, w, mean.cuda(), rstd.cuda(), weight_grad_dtype=torch.float32)
+    # as above
+    R.close(dx, want[0], want[0].abs() * R.u(dtype) * 1.01 + want[3] * 96 * E + R.sub(dtype) + R.sub(torch.float32), "dx")
+    R.close(dw, want[1], want[1].abs() * E * 1.01 + want[4] * 260 * E, "dw")
