@@ -1038,8 +1038,8 @@ class GradList:
     list holds its tensors and their addresses: a tensor must not be resized or given other
     memory.  Making it copies a table to the device and is not captured in a graph; the calls
     that use it are, and a graph reads the list's table at every replay: the list has to outlive
-    it.  Calls on any stream hold the table until their work is done, so a list may be dropped
-    behind them."""
+    it.  Calls on any stream hold the table's memory until their work is done; the tensors' is the
+    caller's to hold, as for every call."""
 
     def __init__(self, tensors, out=None):
         self.tensors = list(tensors)
@@ -1074,14 +1074,16 @@ class GradList:
         host = torch.empty(max(1, self.pieces) * 32, dtype=torch.uint8, device="cpu")
         _check(_grads_table(words.data_ptr(), len(records), host.data_ptr(), host.numel()))
         self.table = host.to(dev)
-        self._stream = _raw_stream(dev.index)  # the one that the table's memory belongs to
+        self._streams = {_raw_stream(dev.index)}  # those that the table's memory is held for
 
 
 def _grad_list(grads):
     if not isinstance(grads, GradList):
         return GradList(grads)
-    if _raw_stream(grads.device.index) != grads._stream:
+    stream = _raw_stream(grads.device.index)
+    if stream not in grads._streams:
         grads.table.record_stream(torch.cuda.current_stream(grads.device))
+        grads._streams.add(stream)
     return grads
 
 

@@ -10,7 +10,8 @@ pytestmark = pytest.mark.gpu
 
 @pytest.mark.parametrize("made_on_a_side_stream", [False, True])
 @pytest.mark.parametrize("call", ["clip", "sumsq", "clip by a given sum"])
-def test_a_list_dropped_behind_queued_work(made_on_a_side_stream, call):
+@pytest.mark.parametrize("again", [False, True])
+def test_a_list_dropped_behind_queued_work(made_on_a_side_stream, call, again):
     t = [torch.full((n,), 2.0, device="cuda") for n in (50, 4096, 10000, 7)]
     count = sum(x.numel() for x in t)
     given = torch.full((), 4.0 * count, dtype=torch.float64, device="cuda")
@@ -23,6 +24,9 @@ def test_a_list_dropped_behind_queued_work(made_on_a_side_stream, call):
         at, nbytes = rows.table.data_ptr(), rows.table.numel()
     home.synchronize()
     with torch.cuda.stream(other):
+        if again:  # a call before, whose work is done
+            ops.grad_sumsq(rows)
+            other.synchronize()
         torch.cuda._sleep(200_000_000)  # a tenth of a second or so
         if call == "sumsq":
             got = ops.grad_sumsq(rows)
